@@ -10,6 +10,9 @@ The higher-level helpers (:func:`route_meta`, :func:`dispatch`, :func:`combine`,
 like the dispatcher pages' outputs (``DeepEPNormalDispatchOutput`` /
 ``DeepEPLLDispatchOutput`` on the "sglang token_dispatcher/deepep.py" page).
 
+The expert operators between dispatch and combine (``include/moe_experts.h``) are bound in
+:mod:`.experts` and reachable from here.
+
 There is no CPU fallback: the first call raises when the library has not been built
 (``python -m combine_moe_route_meta_gb300.build``), and every call requires CUDA tensors.
 """
@@ -81,6 +84,15 @@ _SIGNATURES = {
     "moe_combine_partitioned": (_int, [_P, _i64, _i64, _int, _P, _int, _int, _int, _P, _P, _P]),
     "moe_dispatch_partitioned_ex": (_int, [_int, _int, _P, _i64, _i64, _int, _P, _P, _int, _int, _int, _i32, _f32,
                                            _P, _P, _P, _P, _P, _P]),
+    # include/moe_experts.h
+    "moe_quantize_nvfp4": (_int, [_P, _i64, _i64, _int, _P, _int, _P, _P, _P]),
+    "moe_dequantize_nvfp4": (_int, [_P, _P, _i64, _i64, _int, _P, _int, _P, _P]),
+    "moe_expert_gemm": (_int, [_int, _P, _P, _int, _int, _int, _i64, _int, _int, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_gemm_swiglu": (_int, [_int, _P, _P, _int, _int, _int, _i64, _int, _int, _P, _P, _P, _P, _P, _f32, _P,
+                                      _P, _P, _P]),
+    "moe_layer_workspace_size": (_sz, [_i64, _int, _int, _int, _int]),
+    "moe_layer_few_tokens": (_int, [_P, _i64, _int, _int, _P, _P, _int, _int, _int, _P, _P, _P, _P, _P, _P, _P, _P,
+                                    _sz, _P, _P]),
 }
 _lib_handle = None
 
@@ -685,3 +697,6 @@ class MoEDispatcher:
 
     def check(self) -> None:
         check_status(self.status, "MoEDispatcher")
+
+
+from .experts import *  # noqa: E402,F401,F403  (uses the names above)

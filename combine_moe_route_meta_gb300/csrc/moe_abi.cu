@@ -10,35 +10,13 @@
 
 #include "moe_diag.h"
 #include "moe_dispatch.h"
+#include "moe_host.h"
 #include "moe_launch.h"
 
-namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-moe_status_t make_ctx(moe_stream_t stream, moe::LaunchCtx* ctx) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MOE_ERR_CUDA;
-    ctx->stream = reinterpret_cast<cudaStream_t>(stream);
-    ctx->num_sms = sms > 0 ? sms : 1;
-    ctx->device = dev;
-    return MOE_OK;
-}
-
-moe_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-// shared checks of (T, K, E)
-moe_status_t check_shape(int64_t T, int K, int E) {
-    if (T < 0) return MOE_ERR_INVALID_ARG;
-    if (K < 1 || E < 1) return MOE_ERR_INVALID_ARG;
-    if (K > MOE_MAX_TOPK || E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
-    if (T > 0 && T > int64_t(INT32_MAX) / K) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
-
-}  // namespace
+using moe::aligned;
+using moe::check_shape;
+using moe::from_cuda;
+using moe::make_ctx;
 
 extern "C" {
 
