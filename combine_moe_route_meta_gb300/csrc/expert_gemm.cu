@@ -3,115 +3,430 @@
 //   out[r, n] = bf16(alpha[e] * sum_k a[r, k] w[e, n, k])
 //   SwiGLU:  h = silu(gate) * up of two such products, quantised to NVFP4
 //
-// Plain tiles: a block computes 64 columns of one expert (SwiGLU: 32 gate and the 32 up columns beside
-// them) for its rows, 64 at a time, from 64-deep slices decoded to fp32 in shared memory.
+// Persistent CTAs, one per SM, each walking over tiles of 128 rows x 256 columns (SwiGLU: 128 gate columns
+// and the 128 up columns beside them) of one expert. Warps have roles:
+//   0      issues the loads of a ring of kStages slots, each 256 values of K: codes by tensor maps in the
+//          128-byte swizzle (out-of-range rows and columns read as zero), weight scales (whole 512-byte
+//          tiles) by bulk copies, and the rows' scales too where their 128-row tiles are the layout's own
+//   1      copies a slot's scale tiles to tensor memory and issues its block-scaled products
+//   2, 3   gather the rows' scales into the tile layout where rows start inside a tile or scales are row-major
+//   4..11  turn the fp32 accumulator into the output; they free it as soon as they hold its last columns
+// Tiles run with the row tiles of one column block next to each other, so a weight tile comes from DRAM once
+// and from L2 for the others. Every wait is bounded (MOE_ERR_TIMEOUT).
 #include <cstdint>
 
 #include "expert_rows.cuh"
 #include "experts_launch.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kThreads = 256;
+constexpr int kTileM = 128;
+constexpr int kTileN = 256;
+constexpr int kChunk = 256;                           // values of K per slot: 128 bytes of codes a row
+constexpr int kStages = 4;
+constexpr int kWarps = 12;
+constexpr int kThreads = kWarps * 32;
+constexpr int kLoaderWarps = 2;
+constexpr int kEpilogueWarps = 8;
+constexpr uint32_t kBytesA = kTileM * 128;            // codes of a slot
+constexpr uint32_t kBytesB = kTileN * 128;
+constexpr uint32_t kBytesSfA = kTileM * (kChunk / 16);  // scales of a slot
+constexpr uint32_t kBytesSfB = kTileN * (kChunk / 16);
+constexpr uint32_t kSlot = kBytesA + kBytesB + kBytesSfA + kBytesSfB;
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kTmemScales = kTileN;              // after the accumulator: 16 + 32 columns for every slot, so
+constexpr uint32_t kTmemScaleSet = 64;                // that a slot's scales live as long as the slot itself
+static_assert(kTmemScales + kStages * kTmemScaleSet <= kTmemColumns, "scales of every slot in tensor memory");
 
-// 16 values of block `c` of a row into dst[0..15] (stride kTile + 1)
-__device__ __forceinline__ void decode16(const uint8_t* codes, uint32_t sf, float* dst) {
-    const uint2 q = *reinterpret_cast<const uint2*>(codes);
-    const float s = e4m3_value(sf);
-#pragma unroll
-    for (int j = 0; j < 16; j++) {
-        const uint32_t w = j < 8 ? q.x : q.y;
-        dst[j * (kTile + 1)] = e2m1_value((w >> (4 * (j & 7))) & 15u) * s;
+struct GemmArgs {
+    ExpertGemm g;
+    int chunks;       // slots per tile: ceil(k / kChunk)
+    int tiles_n;
+    bool sf_bulk_ok;  // the rows' scales are in 128 x 4 tiles at a 16-byte aligned address
+    bool wide_out;    // out is 32-byte aligned
+};
+
+struct Tile {
+    int e, n0, row0, rows;  // expert, first column (of gate), first row, rows of the expert from there on
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], acc_full, acc_empty;
+    uint32_t tmem;
+    int dead;       // a wait gave up
+    int tiles;
+    int prefix[1];  // [E + 1]: row tiles of the experts before e
+};
+
+template <bool SWIGLU>
+__device__ __forceinline__ Tile find_tile(const GemmArgs& a, const int* prefix, int t) {
+    int lo = 0, hi = a.g.E;  // prefix[lo] * tiles_n <= t < prefix[hi] * tiles_n
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (int64_t(prefix[mid]) * a.tiles_n <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int rows_t = prefix[lo + 1] - prefix[lo];
+    const int i = int(t - int64_t(prefix[lo]) * a.tiles_n);
+    const RowSpan s = expert_rows(a.g, lo);
+    const int m = i % rows_t;
+    return Tile{lo, i / rows_t * (SWIGLU ? kTileN / 2 : kTileN), int(s.base) + m * kTileM, s.count - m * kTileM};
+}
+
+// Bounded wait; false (and the CTA marked dead) when it gave up or another role already had.
+__device__ __forceinline__ bool wait_or_die(const GemmArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(smem_addr(bar), parity)) return true;
+    *const_cast<volatile int*>(&s->dead) = 1;
+    set_status(a.g.status, MOE_ERR_TIMEOUT);
+    return false;
+}
+
+// The same for a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait_or_die(const GemmArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFullMask, wait_or_die(a, s, bar, parity));
+}
+
+template <bool SWIGLU>
+__device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t slots, bool sf_bulk,
+                                          const CUtensorMap* map_a, const CUtensorMap* map_w) {
+    const int k64 = a.g.k / 64;
+    const int np128 = (a.g.n + 127) / 128;  // 128-row blocks of a weight matrix
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x; t < s->tiles; t += gridDim.x) {
+        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        for (int c = 0; c < a.chunks; c++) {
+            if (!wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+            const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * kSlot;
+            const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
+            const int q = min(4, k64 - 4 * c);  // 64-value steps of this slot
+            const int nb = tile.n0 / 128;
+            const bool second = SWIGLU || nb + 1 < np128;
+            mbar_expect_tx(bar, kBytesA + kBytesB + q * 512 * ((sf_bulk ? 1 : 0) + (second ? 2 : 1)));
+            tma_load_2d(slot, map_a, c * 128, tile.row0, bar);
+            // SwiGLU: dimensions (k, column, half, expert), 128 columns of both halves; else (k, column, 1, expert)
+            tma_load_4d(slot + kBytesA, map_w, c * 128, tile.n0, 0, tile.e, bar);
+            if (sf_bulk)
+                bulk_load_announced(sfa, a.g.a_sf + (int64_t(tile.row0 / 128) * k64 + 4 * c) * 512, q * 512, bar);
+            const int64_t block = SWIGLU ? int64_t(tile.e) * 2 * np128 + nb : int64_t(tile.e) * np128 + nb;
+            bulk_load_announced(sfb, a.g.w_sf + (block * k64 + 4 * c) * 512, q * 512, bar);
+            if (second)
+                bulk_load_announced(sfb + kBytesSfB / 2,
+                                    a.g.w_sf + ((block + (SWIGLU ? np128 : 1)) * k64 + 4 * c) * 512, q * 512, bar);
+            if (++st == kStages) st = 0, ph ^= 1;
+        }
     }
 }
 
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreads) expert_gemm_plain_kernel(ExpertGemm a) {
-    __shared__ float sa[kTile][kTile + 1];  // [k][row]
-    __shared__ float sb[kTile][kTile + 1];  // [k][column]
-    pdl_wait();
-    const int e = blockIdx.y;
-    const RowSpan span = expert_rows(a, e);
-    const int C = a.k / 16, np = (a.n + 127) / 128 * 128;
-    const int n0 = blockIdx.x * (SWIGLU ? kTile / 2 : kTile);
-    const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
-    const float alpha = a.alpha ? __ldg(a.alpha + e) : 1.0f;
-
-    for (int m0 = 0; m0 < span.count; m0 += kTile) {
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < a.k; k0 += kTile) {
-            const int row = tid / 4, blk = tid % 4, c = k0 / 16 + blk;
-            __syncthreads();
-            if (m0 + row < span.count) {
-                const int64_t r = span.base + m0 + row;
-                decode16(a.a + (r * C + c) * 8, a.a_sf[act_sf_index(a.scale_layout, r, c, C)], &sa[blk * 16][row]);
-            } else {
-                for (int j = 0; j < 16; j++) sa[blk * 16 + j][row] = 0.0f;
+__device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t slots) {
+    const int k64 = a.g.k / 64;
+    const uint32_t tmem = s->tmem;
+    int st = 0, n_tile = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
+        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const uint32_t idesc = idesc_nvfp4(SWIGLU ? kTileN : min(kTileN, a.g.n - tile.n0));
+        if (!wait_or_die(a, s, &s->acc_empty, (n_tile & 1) ^ 1)) return;
+        tc_fence_after();
+        for (int c = 0; c < a.chunks; c++) {
+            if (!wait_or_die(a, s, &s->full[st], ph)) return;
+            tc_fence_after();
+            const uint32_t slot = slots + st * kSlot;
+            const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
+            const uint32_t ta = tmem + kTmemScales + st * kTmemScaleSet, tb = ta + 16;
+            const int q = min(4, k64 - 4 * c);
+            for (int j = 0; j < q; j++) {
+                tc_copy_scales(ta + j * 4, desc_scales(sfa + j * 512));
+                tc_copy_scales(tb + j * 8, desc_scales(sfb + j * 512));
+                tc_copy_scales(tb + j * 8 + 4, desc_scales(sfb + kBytesSfB / 2 + j * 512));
             }
-            const int half = SWIGLU ? row / (kTile / 2) : 0;
-            const int n = n0 + (SWIGLU ? row % (kTile / 2) : row);
-            if (n < a.n) {
-                const int64_t m = SWIGLU ? int64_t(e) * 2 + half : e;  // weight matrix
-                decode16(a.w + ((m * a.n + n) * C + c) * 8, a.w_sf[m * np * C + swizzled_128x4_index(n, c, C)],
-                         &sb[blk * 16][row]);
-            } else {
-                for (int j = 0; j < 16; j++) sb[blk * 16 + j][row] = 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kTile; k++)
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) acc[i][j] = fmaf(sa[k][tr * 4 + i], sb[k][tc * 4 + j], acc[i][j]);
+            const uint64_t da = desc_k128(slot), db = desc_k128(slot + kBytesA);
+            for (int j = 0; j < q; j++)  // 64 codes: 32 bytes further in the rows, 2 in the descriptor's units
+                tc_mma_nvfp4(tmem, da + 2 * j, db + 2 * j, idesc, ta + j * 4, tb + j * 8, c > 0 || j > 0);
+            tc_commit(smem_addr(&s->empty[st]));
+            if (++st == kStages) st = 0, ph ^= 1;
         }
-        if (!SWIGLU) {
-            for (int i = 0; i < 4; i++)
-                for (int j = 0; j < 4; j++)
-                    if (m0 + tr * 4 + i < span.count && n0 + tc * 4 + j < a.n)
-                        a.out[(span.base + m0 + tr * 4 + i) * a.n + n0 + tc * 4 + j] =
-                            uint16_t(pack_bf16x2(alpha * acc[i][j], 0.0f));
-        } else {
-            __syncthreads();
-            for (int i = 0; i < 4; i++)
-                for (int j = 0; j < 4; j++) sa[tr * 4 + i][tc * 4 + j] = alpha * acc[i][j];
-            __syncthreads();
-            const int row = tid / 2, blk = tid % 2;  // 64 rows x 2 blocks of 16
-            if (tid < 128 && m0 + row < span.count && n0 + blk * 16 < a.n) {
-                uint32_t w[8];
-                for (int p = 0; p < 8; p++)
-                    w[p] = 0;
-                float h[16], amax = 0.0f;
-                for (int j = 0; j < 16; j++) {
-                    h[j] = swiglu(sa[row][blk * 16 + j], sa[row][kTile / 2 + blk * 16 + j]);
-                    amax = fmaxf(amax, fabsf(h[j]));
+        tc_commit(smem_addr(&s->acc_full));
+    }
+}
+
+// Row scales that are not whole tiles of the layout: each of the 64 threads brings the scales of two rows.
+template <bool SWIGLU>
+__device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_t slots, int i) {
+    const int C = a.g.k / 16, k64 = a.g.k / 64;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x; t < s->tiles; t += gridDim.x) {
+        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const uint8_t* src[2];
+        for (int j = 0; j < 2; j++) {
+            const int64_t r = min(int64_t(tile.row0) + i + 64 * j, a.g.rows - 1);
+            src[j] = a.g.a_sf + act_sf_index(a.g.scale_layout, r, 0, C);
+        }
+        const int step = a.g.scale_layout == MOE_SCALES_SWIZZLED_128X4 ? 512 : 4;  // bytes from word to word
+        auto load = [&](int c, uint32_t* v) {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int w = 0; w < 4; w++)
+                    v[j * 4 + w] = c * 4 + w < k64
+                                       ? __ldg(reinterpret_cast<const uint32_t*>(src[j] + int64_t(c * 4 + w) * step))
+                                       : 0u;
+        };
+        uint32_t v[8], next[8];  // the next slot's words are on their way while this one's wait
+        load(0, v);
+        for (int c = 0; c < a.chunks; c++) {
+            load(c + 1, next);
+            if (!warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+            const uint32_t sfa = slots + st * kSlot + kBytesA + kBytesB;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const int r = i + 64 * j;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sfa + w * 512 + (r % 32) * 16 + r / 32 * 4),
+                                 "r"(v[j * 4 + w])
+                                 : "memory");
                 }
-                const uint32_t sf = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), a.h_scale), 0.0f) & 0xffu;
-                const float sff = e4m3_value(sf);
-                if (sff != 0.0f) {
-                    const float rs = __fdiv_rn(a.h_scale, sff);
-                    for (int p = 0; p < 8; p++) w[p] = e2m1x2(__fmul_rn(h[2 * p], rs), __fmul_rn(h[2 * p + 1], rs));
-                }
-                const int64_t r = span.base + m0 + row;
-                const int c = n0 / 16 + blk, hc = a.n / 16;
-                st_v2(a.h + (r * hc + c) * 8, make_uint2(w[0] | w[1] << 8 | w[2] << 16 | w[3] << 24,
-                                                         w[4] | w[5] << 8 | w[6] << 16 | w[7] << 24));
-                a.h_sf[act_sf_index(a.scale_layout, r, c, hc)] = uint8_t(sf);
-            }
-            __syncthreads();
+            fence_proxy_async();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&s->full[st]));
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = next[j];
+            if (++st == kStages) st = 0, ph ^= 1;
         }
     }
+}
+
+__device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float alpha, bool wide) {
+    uint32_t w[8];
+#pragma unroll
+    for (int p = 0; p < 8; p++) w[p] = pack_bf16x2(alpha * v[2 * p], alpha * v[2 * p + 1]);
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        st_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        st_v4(dst + 8, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+// One block of 16 SwiGLU outputs as codes and a scale byte.
+__device__ __forceinline__ uint32_t quantise_h(const float* gate, const float* up, float alpha, float gs, uint2* codes) {
+    float h[16], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; j++) {
+        h[j] = swiglu(alpha * gate[j], alpha * up[j]);
+        amax = fmaxf(amax, fabsf(h[j]));
+    }
+    const uint32_t sf = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), gs), 0.0f) & 0xffu;
+    const float sff = e4m3_value(sf);
+    *codes = make_uint2(0, 0);
+    if (sff != 0.0f) {
+        const float r = __fdiv_rn(gs, sff);
+        uint32_t b[8];
+#pragma unroll
+        for (int p = 0; p < 8; p++) b[p] = e2m1x2(__fmul_rn(h[2 * p], r), __fmul_rn(h[2 * p + 1], r));
+        *codes = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+    }
+    return sf;
+}
+
+template <bool SWIGLU>
+__device__ __forceinline__ void epilogue_role(const GemmArgs& a, Shared* s, int warp) {
+    const int lane = threadIdx.x & 31;
+    const int quad = warp % 4, half = (warp - 4) / 4;  // a warp reads the 32 lanes of tensor memory that are its own
+    const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);
+    int n_tile = 0;
+    for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
+        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const float alpha = a.g.alpha ? __ldg(a.g.alpha + tile.e) : 1.0f;
+        const int m = quad * 32 + lane;
+        const bool valid = m < tile.rows;
+        const int64_t r = int64_t(tile.row0) + m;
+        if (!warp_wait_or_die(a, s, &s->acc_full, n_tile & 1)) return;
+        tc_fence_after();
+        if constexpr (!SWIGLU) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                float v[32];
+                const int col = half * 128 + c * 32;
+                tmem_load32(tmem + col, v);
+                if (c == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty));
+                }
+                uint16_t* dst = a.g.out + r * a.g.n + tile.n0 + col;
+                if (valid && tile.n0 + col < a.g.n) store_out16(dst, v, alpha, a.wide_out);
+                if (valid && tile.n0 + col + 16 < a.g.n) store_out16(dst + 16, v + 16, alpha, a.wide_out);
+            }
+        } else {
+            // 64 columns of h: 32 bytes of codes and one word of scales
+            const int col = half * 64;
+            uint32_t sf = 0;
+            uint2 q[4];
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                float gate[32], up[32];
+                tmem_load32(tmem + col + c * 32, gate);
+                tmem_load32(tmem + kTileN / 2 + col + c * 32, up);
+                if (c == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty));
+                }
+                sf |= quantise_h(gate, up, alpha, a.g.h_scale, &q[2 * c]) << (16 * c);
+                sf |= quantise_h(gate + 16, up + 16, alpha, a.g.h_scale, &q[2 * c + 1]) << (16 * c + 8);
+            }
+            const int n = tile.n0 + col;
+            if (valid && n < a.g.n) {
+                uint8_t* dst = a.g.h + r * (a.g.n / 2) + n / 2;
+                st_v4(dst, make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
+                st_v4(dst + 16, make_uint4(q[2].x, q[2].y, q[3].x, q[3].y));
+                *reinterpret_cast<uint32_t*>(a.g.h_sf + act_sf_index(a.g.scale_layout, r, n / 16, a.g.n / 16)) = sf;
+            }
+        }
+    }
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
+    const uint32_t slots = smem_addr(base);
+    Shared* s = reinterpret_cast<Shared*>(base + kStages * kSlot);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (warp == 1) tmem_alloc(smem_addr(&s->tmem), kTmemColumns);
+    pdl_wait();
+
+    // row tiles of every expert, their prefix sums, and whether all segments start on a tile of scales
+    int ragged = 0;
+    for (int e = threadIdx.x; e < a.g.E; e += kThreads) {
+        const RowSpan r = expert_rows(a.g, e);
+        s->prefix[e + 1] = (r.count + kTileM - 1) / kTileM;
+        ragged |= r.count > 0 && r.base % 128 != 0;
+    }
+    const bool sf_bulk = !__syncthreads_or(ragged) && a.sf_bulk_ok;
+    if (warp == 0) {
+        int sum = 0;
+        for (int e0 = 0; e0 < a.g.E; e0 += 32) {
+            int v = e0 + lane < a.g.E ? s->prefix[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFullMask, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e0 + lane < a.g.E) s->prefix[e0 + lane + 1] = sum + v;
+            sum += __shfl_sync(kFullMask, v, 31);
+        }
+        if (lane == 0) {
+            s->prefix[0] = 0;
+            s->tiles = sum * a.tiles_n;
+            s->dead = 0;
+            for (int i = 0; i < kStages; i++) {
+                mbar_init(smem_addr(&s->full[i]), 1 + (sf_bulk ? 0 : kLoaderWarps));
+                mbar_init(smem_addr(&s->empty[i]), 1);
+            }
+            mbar_init(smem_addr(&s->acc_full), 1);
+            mbar_init(smem_addr(&s->acc_empty), kEpilogueWarps);
+            mbar_fence_init();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp == 0) {
+        if (lane == 0) load_role<SWIGLU>(a, s, slots, sf_bulk, &map_a, &map_w);
+    } else if (warp == 1) {
+        if (lane == 0) mma_role<SWIGLU>(a, s, slots);
+    } else if (warp < 4) {
+        if (!sf_bulk) scale_role<SWIGLU>(a, s, slots, int(threadIdx.x) - 64);
+    } else {
+        epilogue_role<SWIGLU>(a, s, warp);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*const_cast<volatile int*>(&s->dead) && threadIdx.x == 0) {
+        // whatever is still in flight lands in this CTA's memory: give it time before that is freed
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainLimitNs) __nanosleep(1000);
+    }
+    __syncthreads();
+    if (warp == 1) tmem_free(s->tmem, kTmemColumns);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A map of bytes [.., d1, d0] (densely packed) read in boxes of b1 (x b2) rows of 128 bytes.
+bool make_map(CUtensorMap* map, const void* p, int rank, const uint64_t* dims, const uint32_t* box) {
+    if (!encode_tiled()) return false;
+    cuuint64_t size[4], stride[3];
+    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+    uint64_t bytes = 1;
+    for (int i = 0; i < rank; i++) {
+        size[i] = dims[i];
+        b[i] = box[i];
+        bytes *= dims[i];
+        if (i + 1 < rank) stride[i] = bytes;
+    }
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, cuuint32_t(rank), const_cast<void*>(p), size, stride, b,
+                          one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool SWIGLU>
+cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
+    const uint64_t kb = uint64_t(g.k) / 2;
+    CUtensorMap map_a, map_w;
+    const uint64_t da[2] = {kb, uint64_t(g.rows)}, dw[4] = {kb, uint64_t(g.n), SWIGLU ? 2u : 1u, uint64_t(g.E)};
+    const uint32_t ba[2] = {128, kTileM}, bw[4] = {128, SWIGLU ? kTileN / 2 : kTileN, SWIGLU ? 2u : 1u, 1};
+    if (!make_map(&map_a, g.a, 2, da, ba) || !make_map(&map_w, g.w, 4, dw, bw)) return cudaErrorInvalidValue;
+    const int cols = SWIGLU ? kTileN / 2 : kTileN;
+    const GemmArgs a{g, (g.k + kChunk - 1) / kChunk, (g.n + cols - 1) / cols,
+                     g.scale_layout == MOE_SCALES_SWIZZLED_128X4 && reinterpret_cast<uintptr_t>(g.a_sf) % 16 == 0,
+                     reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
+    const size_t smem = 1024 + size_t(kStages) * kSlot + sizeof(Shared) + sizeof(int) * size_t(g.E);
+    auto kern = expert_gemm_kernel<SWIGLU>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (err != cudaSuccess) return err;
+    return launch_pdl(ctx, kern, dim3(unsigned(ctx.num_sms)), dim3(kThreads), smem, a, map_a, map_w);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_gemm(const LaunchCtx& ctx, const ExpertGemm& g) {
-    const bool swiglu = g.out == nullptr;
-    const int cols = swiglu ? kTile / 2 : kTile;
-    const dim3 grid(unsigned((g.n + cols - 1) / cols), unsigned(g.E));
-    return launch_pdl(ctx, swiglu ? expert_gemm_plain_kernel<true> : expert_gemm_plain_kernel<false>, grid,
-                      dim3(kThreads), 0, g);
+    return g.out == nullptr ? launch<true>(ctx, g) : launch<false>(ctx, g);
 }
 
 }  // namespace moe

@@ -41,6 +41,7 @@ static moe_status_t check_gemm(moe_mode_t mode, moe_scale_layout_t layout, int E
     }
     if (*rows < 0 || n <= 0 || n % 16 != 0 || k <= 0 || k % 64 != 0) return MOE_ERR_INVALID_ARG;
     if (*rows > INT32_MAX || n > (1 << 24) || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if ((*rows / 128 + E) * (int64_t(n) / 128 + 1) > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;  // tiles
     if (!status || !count || (!masked && !seg)) return MOE_ERR_INVALID_ARG;
     if (*rows > 0 && (!a || !a_sf || !w || !w_sf)) return MOE_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(a_sf, 4) || !aligned(w, 16) || !aligned(w_sf, 16) || !aligned(alpha, 4) ||
