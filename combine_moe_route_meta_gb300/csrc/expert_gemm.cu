@@ -208,9 +208,7 @@ __device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float
 #pragma unroll
     for (int p = 0; p < 8; p++) w[p] = pack_bf16x2(alpha * v[2 * p], alpha * v[2 * p + 1]);
     if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
+        st_v8(dst, w);
     } else {
         st_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
         st_v4(dst + 8, make_uint4(w[4], w[5], w[6], w[7]));

@@ -7,11 +7,25 @@
 
 namespace moe {
 
-// value of an e2m1 code (its low three bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 the sign)
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float v = m < 2 ? 0.5f * float(m) : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-    return (code & 8u) ? -v : v;
+// 8 codes times their block's scale (twice in s), as 4 pairs of fp16
+__device__ __forceinline__ void decode8(uint32_t codes, uint32_t s, uint32_t* out) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+        : "r"(codes));
+#pragma unroll
+    for (int i = 0; i < 4; i++) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(out[i]) : "r"(s));
+}
+
+// 32 bytes to a 32-byte aligned address
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // The rows [base, base + count) of expert e, cut to the layout's capacity.

@@ -3,9 +3,10 @@
 //   quantise:    sf = e4m3((amax16 / 6) * g),  q = e2m1(x * (g / sf))   (dispatch_slice.cuh's arithmetic)
 //   dequantise:  out = bf16((value(q) * value(sf)) / g)
 //
-// One thread per block of 16 elements: it reads (or writes) 32 contiguous bytes of a bf16 row and
-// writes (or reads) 8 bytes of codes and one scale byte, so a block's amax needs no shuffle.
-// Bound by DRAM: 2.5625 bytes per element.
+// A thread takes one block of 16 elements at a time: 32 contiguous bytes of a bf16 row, 8 bytes of codes and
+// one scale byte, so a block's amax needs no shuffle; four neighbouring threads join their scales to a word.
+// A thread block takes 128 rows x 64 CC columns, so that it fills whole 512-byte scale tiles, and issues
+// all its loads before it computes. Bound by DRAM: 2.5625 bytes per element.
 #include <algorithm>
 #include <cstdint>
 
@@ -16,6 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kQuantThreads = 256;
+constexpr int kQuantRows = 128;
 
 struct QuantArgs {
     const uint16_t* x;
@@ -23,78 +25,158 @@ struct QuantArgs {
     uint8_t* codes;
     uint8_t* sf;
     const float* gs;
-    int64_t G, R, Rp;  // groups, rows, rows with the padding of the tiles
-    int C;             // blocks per row
+    int64_t tiles;        // of 128 rows x 64 CC columns, over all groups
+    int R, C;             // rows and blocks per row of a group
+    int row_tiles, chunks;  // tiles of a group: row_tiles x chunks
+    bool wide;            // bf16 rows are 32-byte aligned
+    bool sf_words;        // four neighbouring blocks' scales are a word (always so in the tiles)
 };
 
-template <bool SWIZZLED>
-__device__ __forceinline__ int64_t sf_index(const QuantArgs& a, int64_t g, int64_t r, int c) {
-    if (SWIZZLED) return g * a.Rp * a.C + swizzled_128x4_index(r, c, a.C);
-    return (g * a.R + r) * a.C + c;
+// Where a thread's blocks lie: column block c of rows r, r + step, .. of group g.
+struct QuantPlace {
+    int g, r, c;
+};
+
+template <int CC>
+__device__ __forceinline__ QuantPlace quant_place(const QuantArgs& a, int64_t tile) {
+    const int chunk = int(tile % a.chunks);
+    const int64_t gr = tile / a.chunks;
+    const int g = int(gr / a.row_tiles);
+    return QuantPlace{g, int(gr - int64_t(g) * a.row_tiles) * kQuantRows + int(threadIdx.x) / (4 * CC),
+                      chunk * 4 * CC + int(threadIdx.x) % (4 * CC)};
 }
 
+// Scale of block (r, c) of group g; with the tiles, a group's matrix has its rows padded to whole tiles.
 template <bool SWIZZLED>
+__device__ __forceinline__ int64_t sf_index(const QuantArgs& a, const QuantPlace& p, int r) {
+    if (SWIZZLED) return int64_t(p.g) * a.row_tiles * kQuantRows * a.C + swizzled_128x4_index(r, p.c, a.C);
+    return (int64_t(p.g) * a.R + r) * a.C + p.c;
+}
+
+__device__ __forceinline__ LaneSlice load_block(const uint16_t* p, bool wide) {
+    if (!wide) return load_slice(p);
+    LaneSlice s;
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(s.v0.x), "=r"(s.v0.y), "=r"(s.v0.z), "=r"(s.v0.w), "=r"(s.v1.x), "=r"(s.v1.y), "=r"(s.v1.z),
+                   "=r"(s.v1.w)
+                 : "l"(p));
+    return s;
+}
+
+template <int CC, bool SWIZZLED>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(QuantArgs a) {
     pdl_wait();
-    const int64_t n = a.G * a.Rp * a.C;
-    for (int64_t i = int64_t(blockIdx.x) * kQuantThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kQuantThreads) {
-        const int c = int(i % a.C);
-        const int64_t gr = i / a.C, g = gr / a.Rp, r = gr - g * a.Rp;
-        uint32_t sf = 0;
-        if (r < a.R) {
-            const int64_t at = (g * a.R + r) * a.C + c;
-            const LaneCodes q = quantise16<MOE_QUANT_NVFP4_B16>(load_slice(a.x + at * 16), __ldg(a.gs + g));
-            st_v2(a.codes + at * 8, make_uint2(q.q.x, q.q.y));
-            sf = q.scale;
+    constexpr int kStep = kQuantThreads / (4 * CC), kTurns = kQuantRows / kStep;
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const QuantPlace p = quant_place<CC>(a, tile);
+        const int64_t at = (int64_t(p.g) * a.R + p.r) * a.C + p.c;  // block of the first row
+        LaneSlice v[kTurns];
+#pragma unroll
+        for (int i = 0; i < kTurns; i++) {
+            v[i].v0 = v[i].v1 = make_uint4(0, 0, 0, 0);
+            if (p.r + i * kStep < a.R && p.c < a.C) v[i] = load_block(a.x + (at + int64_t(i) * kStep * a.C) * 16, a.wide);
         }
-        a.sf[sf_index<SWIZZLED>(a, g, r, c)] = uint8_t(sf);
+        const float gs = __ldg(a.gs + p.g);
+#pragma unroll
+        for (int i = 0; i < kTurns; i++) {
+            const int r = p.r + i * kStep;
+            const bool live = r < a.R && p.c < a.C;
+            const LaneCodes q = quantise16<MOE_QUANT_NVFP4_B16>(v[i], gs);
+            if (live) st_v2(a.codes + (at + int64_t(i) * kStep * a.C) * 8, make_uint2(q.q.x, q.q.y));
+            if (SWIZZLED || a.sf_words) {  // zero in the padding rows of a tile
+                uint32_t w = live ? q.scale << (8 * (threadIdx.x & 3)) : 0u;
+                w |= __shfl_xor_sync(kFullMask, w, 1);
+                w |= __shfl_xor_sync(kFullMask, w, 2);
+                if ((threadIdx.x & 3) == 0 && p.c < a.C && (SWIZZLED || r < a.R))
+                    *reinterpret_cast<uint32_t*>(a.sf + sf_index<SWIZZLED>(a, p, r)) = w;
+            } else if (live) {
+                a.sf[sf_index<SWIZZLED>(a, p, r)] = uint8_t(q.scale);
+            }
+        }
     }
 }
 
-template <bool SWIZZLED>
+// (value(code) * value(scale)) / g of two codes as packed bf16. The product has 6 significant bits and
+// is exact in fp16; the quotient is the correctly rounded one (div_by_scale, whose remainder stays in the normal
+// range for the g that `fast` admits).
+__device__ __forceinline__ uint32_t dequantise2(uint32_t f16x2, float g, float rcp, bool fast) {
+    const float lo = __half2float(__ushort_as_half(uint16_t(f16x2)));
+    const float hi = __half2float(__ushort_as_half(uint16_t(f16x2 >> 16)));
+    if (fast) return pack_bf16x2(div_by_scale(lo, g, rcp), div_by_scale(hi, g, rcp));
+    return pack_bf16x2(__fdiv_rn(lo, g), __fdiv_rn(hi, g));
+}
+
+template <int CC, bool SWIZZLED>
 __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(QuantArgs a) {
     pdl_wait();
-    const int64_t n = a.G * a.R * a.C;
-    for (int64_t i = int64_t(blockIdx.x) * kQuantThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kQuantThreads) {
-        const int c = int(i % a.C);
-        const int64_t gr = i / a.C, g = gr / a.R, r = gr - g * a.R;
-        const uint2 q = *reinterpret_cast<const uint2*>(a.codes + i * 8);
-        const float sf = e4m3_value(a.sf[sf_index<SWIZZLED>(a, g, r, c)]);
-        const float gs = __ldg(a.gs + g);
-        uint32_t w[8];
+    constexpr int kStep = kQuantThreads / (4 * CC), kTurns = kQuantRows / kStep;
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const QuantPlace p = quant_place<CC>(a, tile);
+        const int64_t at = (int64_t(p.g) * a.R + p.r) * a.C + p.c;
+        uint2 q[kTurns];
+        uint32_t sf[kTurns];
 #pragma unroll
-        for (int p = 0; p < 8; p++) {
-            const uint32_t b = ((p < 4 ? q.x : q.y) >> (8 * (p & 3))) & 0xffu;
-            w[p] = pack_bf16x2(__fdiv_rn(e2m1_value(b) * sf, gs), __fdiv_rn(e2m1_value(b >> 4) * sf, gs));
+        for (int i = 0; i < kTurns; i++) {
+            q[i] = make_uint2(0, 0);
+            sf[i] = 0;
+            if (p.r + i * kStep < a.R && p.c < a.C) {
+                q[i] = __ldg(reinterpret_cast<const uint2*>(a.codes + (at + int64_t(i) * kStep * a.C) * 8));
+                sf[i] = __ldg(a.sf + sf_index<SWIZZLED>(a, p, p.r + i * kStep));
+            }
         }
-        st_v4(a.out + i * 16, make_uint4(w[0], w[1], w[2], w[3]));
-        st_v4(a.out + i * 16 + 8, make_uint4(w[4], w[5], w[6], w[7]));
+        const float g = __ldg(a.gs + p.g);
+        const bool fast = fabsf(g) > 0x1p-60f && fabsf(g) < 0x1p60f;
+        const float rcp = fast ? __frcp_rn(g) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTurns; i++) {
+            if (p.r + i * kStep >= a.R || p.c >= a.C) continue;
+            uint32_t s, w[8];
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(uint16_t(sf[i] * 0x101u)));
+            decode8(q[i].x, s, w);
+            decode8(q[i].y, s, w + 4);
+#pragma unroll
+            for (int j = 0; j < 8; j++) w[j] = dequantise2(w[j], g, rcp, fast);
+            uint16_t* dst = a.out + (at + int64_t(i) * kStep * a.C) * 16;
+            if (a.wide) {
+                st_v8(dst, w);
+            } else {
+                st_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
+                st_v4(dst + 8, make_uint4(w[4], w[5], w[6], w[7]));
+            }
+        }
     }
 }
 
-unsigned quant_grid(const LaunchCtx& ctx, int64_t blocks) {
-    const int64_t need = (blocks + kQuantThreads - 1) / kQuantThreads;
-    return unsigned(std::max<int64_t>(1, std::min<int64_t>(need, int64_t(ctx.num_sms) * 8)));
+// 64 columns a tile while that keeps the tiles below four for each SM, 256 above: 128 x 7168 then has 112 tiles
+// instead of 28, and large matrices read 512 contiguous bytes of a row.
+template <typename Kernel>
+cudaError_t launch_quant(const LaunchCtx& ctx, QuantArgs a, int64_t G, Kernel narrow, Kernel broad) {
+    a.row_tiles = (a.R + kQuantRows - 1) / kQuantRows;
+    const bool few = G * a.row_tiles * ((a.C + 3) / 4) <= 4 * int64_t(ctx.num_sms);
+    a.chunks = few ? (a.C + 3) / 4 : (a.C + 15) / 16;
+    a.tiles = G * a.row_tiles * a.chunks;
+    return launch_pdl(ctx, few ? narrow : broad, dim3(unsigned(std::min<int64_t>(a.tiles, 1 << 24))),
+                      dim3(kQuantThreads), 0, a);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_nvfp4(const LaunchCtx& ctx, const uint16_t* x, int64_t G, int64_t R, int H,
                                   const float* gs, int scale_layout, uint8_t* codes, uint8_t* scales) {
-    const bool sw = scale_layout == MOE_SCALES_SWIZZLED_128X4;
-    QuantArgs a{x, nullptr, codes, scales, gs, G, R, sw ? (R + 127) / 128 * 128 : R, H / 16};
-    const unsigned grid = quant_grid(ctx, a.G * a.Rp * a.C);
-    return launch_pdl(ctx, sw ? quantize_kernel<true> : quantize_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, a);
+    const QuantArgs a{x, nullptr, codes, scales, gs, 0, int(R), H / 16, 0, 0, reinterpret_cast<uintptr_t>(x) % 32 == 0,
+                      H % 64 == 0 && reinterpret_cast<uintptr_t>(scales) % 4 == 0};
+    if (scale_layout == MOE_SCALES_SWIZZLED_128X4)
+        return launch_quant(ctx, a, G, quantize_kernel<1, true>, quantize_kernel<4, true>);
+    return launch_quant(ctx, a, G, quantize_kernel<1, false>, quantize_kernel<4, false>);
 }
 
 cudaError_t launch_dequantize_nvfp4(const LaunchCtx& ctx, const uint8_t* codes, const uint8_t* scales, int64_t G,
                                     int64_t R, int H, const float* gs, int scale_layout, uint16_t* out) {
-    const bool sw = scale_layout == MOE_SCALES_SWIZZLED_128X4;
-    QuantArgs a{nullptr, out, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), gs, G, R,
-                sw ? (R + 127) / 128 * 128 : R, H / 16};
-    const unsigned grid = quant_grid(ctx, a.G * a.R * a.C);
-    return launch_pdl(ctx, sw ? dequantize_kernel<true> : dequantize_kernel<false>, dim3(grid), dim3(kQuantThreads), 0,
-                      a);
+    const QuantArgs a{nullptr, out, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), gs, 0, int(R), H / 16,
+                      0, 0, reinterpret_cast<uintptr_t>(out) % 32 == 0, false};
+    if (scale_layout == MOE_SCALES_SWIZZLED_128X4)
+        return launch_quant(ctx, a, G, dequantize_kernel<1, true>, dequantize_kernel<4, true>);
+    return launch_quant(ctx, a, G, dequantize_kernel<1, false>, dequantize_kernel<4, false>);
 }
 
 }  // namespace moe

@@ -188,24 +188,27 @@ class NVFP4Rows(NamedTuple):
 
 def quantize_nvfp4(x: torch.Tensor, global_scales: torch.Tensor, scale_layout: str = "swizzled",
                    stream=None) -> NVFP4Rows:
-    """Quantise x [rows, hidden] or [groups, rows, hidden], one global scale per group."""
-    R, H = x.shape[-2:]
-    lead = x.shape[:-2]
-    G = x.numel() // (R * H) if R * H else (lead[0] if lead else 1)
-    codes = torch.empty((*lead, R, H // 2), dtype=torch.uint8, device=x.device)
-    tail = (R, H // 16) if scale_layout == "row" else (nvfp4_scale_bytes(R, H, scale_layout),)
-    scales = torch.empty((*lead, *tail), dtype=torch.uint8, device=x.device)
-    moe_quantize_nvfp4(x.view(G, R, H), global_scales, codes, scales, scale_layout, stream)
+    """Quantise x [groups, rows, hidden], or one matrix [rows, hidden], with one global scale per group."""
+    if x.dim() == 2:
+        q = quantize_nvfp4(x.unsqueeze(0), global_scales, scale_layout, stream)
+        return NVFP4Rows(q.codes[0], q.scales[0], scale_layout)
+    G, R, H = x.shape
+    byte, dev = torch.uint8, x.device
+    codes = torch.empty((G, R, H // 2), dtype=byte, device=dev)
+    tail = (G, R, H // 16) if scale_layout == "row" else (G, nvfp4_scale_bytes(R, H, scale_layout))
+    scales = torch.empty(tail, dtype=byte, device=dev)
+    moe_quantize_nvfp4(x, global_scales, codes, scales, scale_layout, stream)
     return NVFP4Rows(codes, scales, scale_layout)
 
 
 def dequantize_nvfp4(q: NVFP4Rows, global_scales: torch.Tensor, stream=None) -> torch.Tensor:
     """The bf16 values that q stands for."""
-    R, H = q.codes.shape[-2], 2 * q.codes.shape[-1]
-    lead = q.codes.shape[:-2]
-    G = lead.numel()
-    out = torch.empty((*lead, R, H), dtype=torch.bfloat16, device=q.codes.device)
-    moe_dequantize_nvfp4(q.codes, q.scales, global_scales, out.view(G, R, H), q.scale_layout, stream)
+    codes, scales, scale_layout = q
+    if codes.dim() == 2:
+        return dequantize_nvfp4(NVFP4Rows(codes.unsqueeze(0), scales, scale_layout), global_scales, stream)[0]
+    G, R, C = codes.shape
+    out = torch.empty((G, R, 2 * C), dtype=torch.bfloat16, device=codes.device)
+    moe_dequantize_nvfp4(codes, scales, global_scales, out, scale_layout, stream)
     return out
 
 

@@ -82,6 +82,24 @@ def test_every_scale_is_read_back():
     assert np.array_equal(back[0, :, 0], x[0, :, 0])
 
 
+def test_unaligned_buffers():
+    """bf16 rows at 16 bytes, codes at 8, row-major scales at any byte."""
+    m = moe()
+    x = torch.randn(1, 70, 192, device="cuda").bfloat16()
+    g = torch.tensor([300.0], device="cuda")
+    want = m.quantize_nvfp4(x, g, scale_layout="row")
+    shifted = torch.empty(x.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(x.shape)
+    shifted.copy_(x)
+    n = want.scales.numel()
+    codes, scales = filled((want.codes.numel() + 8,), torch.uint8), filled((n + 1,), torch.uint8)
+    m.moe_quantize_nvfp4(shifted, g, codes[8:], scales[1:], "row")
+    assert torch.equal(codes[8:], want.codes.flatten()) and torch.equal(scales[1:], want.scales.flatten())
+    assert (codes[:8] == 0xa5).all() and int(scales[0]) == 0xa5
+    out = filled((x.numel() + 8,), torch.bfloat16)
+    m.moe_dequantize_nvfp4(codes[8:], scales[1:], g, out[8:].view(x.shape), "row")
+    assert torch.equal(out[8:].view(torch.int16), m.dequantize_nvfp4(want, g).view(torch.int16).flatten())
+
+
 def test_empty_calls_write_nothing():
     m = moe()
     g = torch.ones(1, device="cuda")
@@ -108,3 +126,11 @@ def test_offsets_past_32_bits():
     assert torch.equal(q.scales[0][at], tail.scales.flatten())
     back = m.dequantize_nvfp4(q, g)
     assert torch.equal(back[0, -2:], m.dequantize_nvfp4(tail, g)[0]) and not back[0, :-2].any()
+
+
+def test_one_matrix():
+    m = moe()
+    x, g = torch.randn(5, 128, device="cuda").bfloat16(), torch.tensor([200.0], device="cuda")
+    one, group = m.quantize_nvfp4(x, g), m.quantize_nvfp4(x[None], g)
+    assert one.codes.shape == (5, 64) and torch.equal(one.codes, group.codes[0]) and torch.equal(one.scales, group.scales[0])
+    assert torch.equal(m.dequantize_nvfp4(one, g), m.dequantize_nvfp4(group, g)[0])
