@@ -18,6 +18,7 @@
 #include "expert_rows.cuh"
 #include "experts_launch.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
@@ -153,6 +154,8 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t 
         }
         tc_commit(smem_addr(&s->acc_full));
     }
+    // the last slot's arrival is the last that is on its way to this CTA's memory
+    if (n_tile > 0) wait_or_die(a, s, &s->empty[st == 0 ? kStages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
 }
 
 // Row scales that are not whole tiles of the layout: each of the 64 threads brings the scales of two rows.
@@ -369,40 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
-// A map of bytes [.., d1, d0] (densely packed) read in boxes of b1 (x b2) rows of 128 bytes.
-bool make_map(CUtensorMap* map, const void* p, int rank, const uint64_t* dims, const uint32_t* box) {
-    if (!encode_tiled()) return false;
-    cuuint64_t size[4], stride[3];
-    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
-    uint64_t bytes = 1;
-    for (int i = 0; i < rank; i++) {
-        size[i] = dims[i];
-        b[i] = box[i];
-        bytes *= dims[i];
-        if (i + 1 < rank) stride[i] = bytes;
-    }
-    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, cuuint32_t(rank), const_cast<void*>(p), size, stride, b,
-                          one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool SWIGLU>
 cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
     const uint64_t kb = uint64_t(g.k) / 2;
