@@ -123,39 +123,54 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t
     }
 }
 
+// The products of a slot: q steps of 64 values, their scales first.
+__device__ __forceinline__ void multiply_slot(uint32_t slot, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool add) {
+    const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
+    const uint64_t da = desc_k128(slot), db = desc_k128(slot + kBytesA);
+    const uint64_t sa = desc_scales(sfa), s0 = desc_scales(sfb), s1 = desc_scales(sfb + kBytesSfB / 2);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (j >= q) break;
+        tc_copy_scales(ts + j * 4, sa + j * 32);
+        tc_copy_scales(ts + 16 + j * 8, s0 + j * 32);
+        tc_copy_scales(ts + 16 + j * 8 + 4, s1 + j * 32);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (j >= q) break;
+        // 64 codes: 32 bytes further in the rows, 2 in the descriptor's units
+        tc_mma_nvfp4(d, da + 2 * j, db + 2 * j, idesc, ts + j * 4, ts + 16 + j * 8, add || j > 0);
+    }
+}
+
+// A whole warp; one lane issues.
 template <bool SWIGLU>
 __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t slots) {
     const int k64 = a.g.k / 64;
     const uint32_t tmem = s->tmem;
+    const bool leader = elect_one();
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
         const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
         const uint32_t idesc = idesc_nvfp4(SWIGLU ? kTileN : min(kTileN, a.g.n - tile.n0));
-        if (!wait_or_die(a, s, &s->acc_empty, (n_tile & 1) ^ 1)) return;
+        if (!warp_wait_or_die(a, s, &s->acc_empty, (n_tile & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = 0; c < a.chunks; c++) {
-            if (!wait_or_die(a, s, &s->full[st], ph)) return;
+            if (!warp_wait_or_die(a, s, &s->full[st], ph)) return;
             tc_fence_after();
-            const uint32_t slot = slots + st * kSlot;
-            const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
-            const uint32_t ta = tmem + kTmemScales + st * kTmemScaleSet, tb = ta + 16;
-            const int q = min(4, k64 - 4 * c);
-            for (int j = 0; j < q; j++) {
-                tc_copy_scales(ta + j * 4, desc_scales(sfa + j * 512));
-                tc_copy_scales(tb + j * 8, desc_scales(sfb + j * 512));
-                tc_copy_scales(tb + j * 8 + 4, desc_scales(sfb + kBytesSfB / 2 + j * 512));
+            if (leader) {
+                multiply_slot(slots + st * kSlot, tmem, tmem + kTmemScales + st * kTmemScaleSet, idesc,
+                              min(4, k64 - 4 * c), c > 0);
+                tc_commit(smem_addr(&s->empty[st]));
+                if (c + 1 == a.chunks) tc_commit(smem_addr(&s->acc_full));
             }
-            const uint64_t da = desc_k128(slot), db = desc_k128(slot + kBytesA);
-            for (int j = 0; j < q; j++)  // 64 codes: 32 bytes further in the rows, 2 in the descriptor's units
-                tc_mma_nvfp4(tmem, da + 2 * j, db + 2 * j, idesc, ta + j * 4, tb + j * 8, c > 0 || j > 0);
-            tc_commit(smem_addr(&s->empty[st]));
+            __syncwarp();
             if (++st == kStages) st = 0, ph ^= 1;
         }
-        tc_commit(smem_addr(&s->acc_full));
     }
     // the last slot's arrival is the last that is on its way to this CTA's memory
-    if (n_tile > 0) wait_or_die(a, s, &s->empty[st == 0 ? kStages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
+    if (n_tile > 0) warp_wait_or_die(a, s, &s->empty[st == 0 ? kStages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
 }
 
 // Row scales that are not whole tiles of the layout: each of the 64 threads brings the scales of two rows.
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) load_role<SWIGLU>(a, s, slots, sf_bulk, &map_a, &map_w);
     } else if (warp == 1) {
-        if (lane == 0) mma_role<SWIGLU>(a, s, slots);
+        mma_role<SWIGLU>(a, s, slots);
     } else if (warp < 4) {
         if (!sf_bulk) scale_role<SWIGLU>(a, s, slots, int(threadIdx.x) - 64);
     } else {

@@ -245,55 +245,72 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     }
 }
 
+// The products of a slot, 32 bytes of a row each: 64 NVFP4 or 16 bf16 values.
+template <bool NVFP4, bool DOWN>
+__device__ __forceinline__ void multiply_slot(uint32_t slot, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool second,
+                                              bool add) {
+    using S = Shape<NVFP4, DOWN>;
+    const uint64_t a0 = desc_k128(slot), a1 = desc_k128(slot + S::kA / 2), b = desc_k128(slot + S::kA);
+    if (NVFP4) {
+        const uint32_t sf = slot + S::kA + S::kB;
+        const uint64_t s0 = desc_scales(sf), s1 = desc_scales(sf + S::kSfA / 2), sb = desc_scales(sf + S::kSfA);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j >= q) break;
+            tc_copy_scales(ts + j * 4, s0 + j * 32);
+            tc_copy_scales(ts + 16 + j * 4, s1 + j * 32);
+            tc_copy_scales(ts + 32 + j * 4, sb + j * 32);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        if (t == 1 && !second) break;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j >= q) break;
+            if (NVFP4)
+                tc_mma_nvfp4(d + t * kColumns, (t ? a1 : a0) + 2 * j, b + 2 * j, idesc, ts + t * 16 + j * 4,
+                             ts + 32 + j * 4, add || j > 0);
+            else
+                tc_mma_bf16(d + t * kColumns, (t ? a1 : a0) + 2 * j, b + 2 * j, idesc, add || j > 0);
+        }
+    }
+}
+
+// A whole warp; one lane issues.
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
                                          uint32_t slots) {
     using S = Shape<NVFP4, DOWN>;
     const int tasks = work.tasks();
+    const bool leader = elect_one();
+    const uint32_t tmem = s->tmem;
     int st = 0;
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         const int buf = i & 1, n = S::columns(t.n);
-        const uint32_t d = s->tmem + buf * 2 * kColumns;
+        const uint32_t d = tmem + buf * 2 * kColumns;
         const uint32_t idesc = NVFP4 ? idesc_nvfp4(n) : idesc_bf16(n);
         const bool second = !DOWN || t.block + 1 < a.blocks;
-        if (!wait_or_die(a, s, &s->acc_empty[buf], (i >> 1 & 1) ^ 1)) return;
+        if (!warp_wait_or_die(a, s, &s->acc_empty[buf], (i >> 1 & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = 0; c < a.chunks; c++) {
-            if (!wait_or_die(a, s, &s->full[st], ph)) return;
+            if (!warp_wait_or_die(a, s, &s->full[st], ph)) return;
             tc_fence_after();
-            const uint32_t slot = slots + st * S::kSlot, sf = slot + S::kA + S::kB;
-            const uint64_t a0 = desc_k128(slot), a1 = desc_k128(slot + S::kA / 2), b = desc_k128(slot + S::kA);
-            // 32 bytes of a row each: 64 NVFP4 or 16 bf16 values
             const int q = min(4, (a.row_bytes - c * 128) / 32);
-            if (NVFP4) {
-                const uint32_t ts = s->tmem + kTmemScales + st * kTmemScaleSet;
-                for (int j = 0; j < q; j++) {
-                    tc_copy_scales(ts + j * 4, desc_scales(sf + j * 512));
-                    tc_copy_scales(ts + 16 + j * 4, desc_scales(sf + S::kSfA / 2 + j * 512));
-                    tc_copy_scales(ts + 32 + j * 4, desc_scales(sf + S::kSfA + j * 512));
-                }
-                for (int j = 0; j < q; j++) {
-                    const bool add = c > 0 || j > 0;
-                    tc_mma_nvfp4(d, a0 + 2 * j, b + 2 * j, idesc, ts + j * 4, ts + 32 + j * 4, add);
-                    if (second)
-                        tc_mma_nvfp4(d + kColumns, a1 + 2 * j, b + 2 * j, idesc, ts + 16 + j * 4, ts + 32 + j * 4, add);
-                }
-            } else {
-                for (int j = 0; j < q; j++) {
-                    const bool add = c > 0 || j > 0;
-                    tc_mma_bf16(d, a0 + 2 * j, b + 2 * j, idesc, add);
-                    if (second) tc_mma_bf16(d + kColumns, a1 + 2 * j, b + 2 * j, idesc, add);
-                }
+            if (leader) {
+                multiply_slot<NVFP4, DOWN>(slots + st * S::kSlot, d, tmem + kTmemScales + st * kTmemScaleSet, idesc, q,
+                                           second, c > 0);
+                tc_commit(smem_addr(&s->empty[st]));
+                if (c + 1 == a.chunks) tc_commit(smem_addr(&s->acc_full[buf]));
             }
-            tc_commit(smem_addr(&s->empty[st]));
+            __syncwarp();
             if (++st == a.stages) st = 0, ph ^= 1;
         }
-        tc_commit(smem_addr(&s->acc_full[buf]));
     }
     // the last slot's arrival is the last that is on its way to this block's memory
-    if (tasks > 0) wait_or_die(a, s, &s->empty[st == 0 ? a.stages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
+    if (tasks > 0) warp_wait_or_die(a, s, &s->empty[st == 0 ? a.stages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
 }
 
 // 2^e as fp32, e in [-126, 127]
@@ -572,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kLoadWarp) {
         if (lane == 0) load_role<NVFP4, DOWN>(a, s, r, work, slots, &map);
     } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_role<NVFP4, DOWN>(a, s, r, work, slots);
+        mma_role<NVFP4, DOWN>(a, s, r, work, slots);
     } else {
         convert_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kConvertWarp);
     }

@@ -55,6 +55,14 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// True in one lane of a converged warp. The issuing warps run their loops with all lanes, so that descriptors and
+// addresses stay in uniform registers, where the instructions want them; one lane issues.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // 32 columns of the calling warp's 32 lanes. The wait is part of the statement, so that no use of the
 // registers can move ahead of it.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
