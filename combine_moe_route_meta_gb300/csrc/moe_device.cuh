@@ -223,10 +223,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 // ---------------------------------------------------------------------------
 // Wait until the kernels this launch depends on have completed and flushed memory.
 // A no-op when the kernel was not launched as a programmatic dependent.
-// No kernel here issues griddepcontrol.launch_dependents: a dependent is released as the
+// The dispatch and combine kernels do not issue griddepcontrol.launch_dependents: a dependent is released as the
 // blocks of the kernel before it exit. Releasing it at the start of a kernel let its blocks
 // take SM resources while they waited, which slowed the large dispatch/combine steps by up to
 // 30 % on GB300 (measured), and gained nothing at decode sizes.
+// The few-token layer's first kernel does (pdl_release): its blocks are all resident from the start, so its
+// dependent's take only SMs that are free, and load weights there.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace moe

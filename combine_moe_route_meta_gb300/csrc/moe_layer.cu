@@ -19,12 +19,14 @@
 //   warp 4       issues the weight loads of a ring of slots, each 128 bytes of 256 weight rows
 //   warp 5       issues the products
 //   warps 6..13  bring a slot's columns of x or h to shared memory, two warps a slot
-// gate_up walks persistently over (pairs of an expert, 128 gate rows and their up rows). In down a cluster of
-// blocks owns 256 rows of out and shares out the experts; each block adds up its experts in order, the cluster
-// adds up the blocks in order. No atomics on values: the same arguments give the same bits. Every wait
-// is bounded (MOE_ERR_TIMEOUT).
+// gate_up walks persistently over (pairs of an expert, 128 gate rows and their up rows); where that leaves more than
+// half of the SMs without work, a cluster of blocks shares out the length of a row. In down a cluster owns 256 rows
+// of out and shares out the experts; each block adds up its experts in order. A cluster adds up its blocks in order.
+// No atomics on values: the same arguments give the same bits. down starts on SMs that gate_up leaves or does
+// not need, and loads weights until h is there. Every wait is bounded (MOE_ERR_TIMEOUT).
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include <cooperative_groups.h>
 
@@ -47,7 +49,8 @@ constexpr int kRows = 256;                    // weight rows of a slot: two tile
 constexpr int kColumns = 64;                  // columns of a group of pairs
 constexpr int kTerms = 5;                     // columns of a pair, NVFP4
 constexpr int kMaxStages = 5;
-constexpr int kShifts = 16;                   // tasks whose powers of two are kept
+constexpr int kKept = 32;                      // tasks whose columns' largest magnitudes are kept
+constexpr int kMaxRanks = 8;
 constexpr uint32_t kTmemScales = 4 * kColumns;  // after two accumulators of two tiles
 constexpr uint32_t kTmemScaleSet = 48;          // two tiles' and the columns' scales of a slot, 16 each
 static_assert(kTmemScales + kMaxStages * kTmemScaleSet <= 512, "tensor memory");
@@ -73,12 +76,13 @@ struct LayerArgs {
     int row_bytes;       // of a weight row
     int blocks;          // 128-row blocks of a weight matrix
     int k;
+    int summed;          // columns of a block's sums: T in down, the pairs of the one task of a cluster in gate_up
 };
 
-// Workspace: h as fp32 [pairs][I] and the largest magnitude of each 32 of it [pairs][I/32] (NVFP4), or
+// Workspace: h as fp32 [pairs][I] and the largest magnitude of each 32 of it [pairs][4 ceil(I/128)] (NVFP4), or
 // two bf16 parts [pairs][2][I].
 __device__ __forceinline__ float* h_values(const FewTokens& a) { return static_cast<float*>(a.workspace); }
-__host__ __device__ __forceinline__ int h_parts(int I) { return (I + 31) / 32; }
+__host__ __device__ __forceinline__ int h_parts(int I) { return (I + 127) / 128 * 4; }
 __device__ __forceinline__ float* h_largest(const FewTokens& a) { return h_values(a) + int64_t(a.T) * a.K * a.I; }
 
 // ---------------------------------------------------------------------------
@@ -91,78 +95,83 @@ struct Routing {
     uint16_t* first;    // [groups + 1] into list
 };
 
-__host__ __device__ __forceinline__ size_t routing_bytes(int pairs, int E) {
-    return (size_t(5) * pairs + 1 + size_t(2) * E + 7) / 8 * 16;
+__host__ __device__ __forceinline__ size_t routing_bytes(int pairs) {
+    return (size_t(3) * pairs + 1 + 7) / 8 * 16;
 }
-
-// All threads of a block; ends with a barrier. `report`: write bad ids to the status word.
-__device__ __forceinline__ Routing route(const FewTokens& a, uint8_t* smem, int group, bool report) {
-    __shared__ int n_groups;
-    const int pairs = a.T * a.K, lane = threadIdx.x & 31;
+// A stable counting sort of the pairs by expert, by all threads of a block: chunks of 32 pairs are counted at
+// once by warps (match), the experts' prefix sums by threads. `scratch`: E bytes for each chunk, 4 for each pair, 2
+// for each expert (less than a ring of slots), 16-byte aligned, free again afterwards. `report`: write bad ids to the
+// status word.
+__device__ __forceinline__ Routing route(const FewTokens& a, uint8_t* smem, uint8_t* scratch, int group, bool report) {
+    __shared__ int warp_sum[kThreads / 32], n_groups;
+    const int pairs = a.T * a.K, chunks = (pairs + 31) / 32, E = a.E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Routing r;
-    int16_t* ids = reinterpret_cast<int16_t*>(smem);
-    r.expert = reinterpret_cast<uint16_t*>(ids + pairs);  // first the experts in the order of their first pairs
+    r.list = reinterpret_cast<uint16_t*>(smem);
+    r.expert = r.list + pairs;
     r.first = r.expert + pairs;
-    r.list = r.first + pairs + 1;
-    uint16_t* rank = r.list + pairs;
-    uint16_t* count = rank + pairs;
-    uint16_t* start = count + a.E;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) count[e] = 0;
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-        const int e = __ldg(a.ids + p);
-        const bool ok = e >= 0 && e < a.E;
-        if (!ok && e != -1 && report) set_status(a.status, MOE_ERR_BAD_EXPERT_ID);
-        ids[p] = int16_t(ok ? e : -1);
+    uint8_t* table = scratch;  // [chunks][E]: pairs of the chunk that name e
+    int16_t* ids = reinterpret_cast<int16_t*>(scratch + (size_t(chunks) * E + 15) / 16 * 16);
+    uint16_t* rank = reinterpret_cast<uint16_t*>(ids + pairs);
+    uint16_t* start = rank + pairs;
+    for (int i = tid; i < (chunks * E + 15) / 16; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+    int mine = -1;  // the first id of a thread, on its way while the table is cleared
+    if (tid < pairs) mine = __ldg(a.ids + tid);
+    __syncthreads();
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+        const int p = c * 32 + lane;
+        int e = c == warp ? mine : p < pairs ? __ldg(a.ids + p) : -1;
+        const bool ok = p < pairs && e >= 0 && e < E;
+        if (p < pairs && !ok && e != -1 && report) set_status(a.status, MOE_ERR_BAD_EXPERT_ID);
+        if (!ok) e = -1;
+        const unsigned same = __match_any_sync(kFullMask, e);
+        const int before = __popc(same & ((1u << lane) - 1));
+        if (p < pairs) ids[p] = int16_t(e), rank[p] = uint16_t(before);
+        if (ok && (same >> lane) == 1) table[c * E + e] = uint8_t(before + 1);  // the last of its kind
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const unsigned below = (1u << lane) - 1;
+    // a thread's neighbouring experts: pairs (low half) and groups (high half) of those before
+    const int per = (E + kThreads - 1) / kThreads;
+    int sum = 0;
+    for (int e = tid * per; e < min(E, (tid + 1) * per); e++) {
         int n = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 32) {
-            const int p = p0 + lane, e = p < pairs ? ids[p] : -1;
-            const unsigned same = __match_any_sync(kFullMask, e);
-            const int before = e >= 0 ? count[e] + __popc(same & below) : 1;
-            const unsigned firsts = __ballot_sync(kFullMask, before == 0);
-            if (before == 0) r.expert[n + __popc(firsts & below)] = uint16_t(e);
-            if (p < pairs) rank[p] = uint16_t(before);
-            __syncwarp();
-            if (e >= 0 && (same >> lane) == 1) count[e] = uint16_t(before + 1);  // the last of its kind
-            n += __popc(firsts);
-            __syncwarp();
-        }
-        // prefix sums of the experts' pairs and groups; the groups are written from the last experts to the
-        // first, so that the list of experts that they take the place of is read before
-        int pairs_before = 0, groups_before = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane, c = i < n ? count[r.expert[i]] : 0;
-            int v = c, u = (c + group - 1) / group;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v1 = __shfl_up_sync(kFullMask, v, o), u1 = __shfl_up_sync(kFullMask, u, o);
-                if (lane >= o) v += v1, u += u1;
-            }
-            if (i < n) {
-                start[r.expert[i]] = uint16_t(pairs_before + v - c);
-                r.first[i] = uint16_t(groups_before + u - (c + group - 1) / group);  // its first group, for now
-            }
-            pairs_before += __shfl_sync(kFullMask, v, 31);
-            groups_before += __shfl_sync(kFullMask, u, 31);
-        }
-        for (int i0 = (n - 1) / 32 * 32; i0 >= 0 && n > 0; i0 -= 32) {
-            const int i = i0 + lane;
-            const int e = i < n ? r.expert[i] : 0, c = i < n ? count[e] : 0, g0 = i < n ? r.first[i] : 0;
-            __syncwarp();
-            for (int g = 0; g * group < c; g++) {
-                r.expert[g0 + g] = uint16_t(e);
-                r.first[g0 + g] = uint16_t(start[e] + g * group);
-            }
-            __syncwarp();
-        }
-        if (lane == 0) r.first[groups_before] = uint16_t(pairs_before), n_groups = groups_before;
+        for (int c = 0; c < chunks; c++) n += table[c * E + e];
+        sum += n + ((n + group - 1) / group << 16);
     }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFullMask, before, o);
+        if (lane >= o) before += u;
+    }
+    if (lane == 31) warp_sum[warp] = before;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x)
-        if (ids[p] >= 0) r.list[start[ids[p]] + rank[p]] = uint16_t(p);
+    before -= sum;
+    int total = 0;
+    for (int w = 0; w < kThreads / 32; w++) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    for (int e = tid * per; e < min(E, (tid + 1) * per); e++) {
+        const int first = before & 0xffff, g = before >> 16;
+        start[e] = uint16_t(first);
+        int n = 0;
+        for (int c = 0; c < chunks; c++) n += table[c * E + e];
+        for (int j = 0; j * group < n; j++) {
+            r.expert[g + j] = uint16_t(e);
+            r.first[g + j] = uint16_t(first + j * group);
+        }
+        before += n + ((n + group - 1) / group << 16);
+    }
+    if (tid == 0) r.first[total >> 16] = uint16_t(total & 0xffff), n_groups = total >> 16;
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = ids[p];
+        if (e < 0) continue;
+        int at = start[e] + rank[p];
+        for (int c = 0; c < p / 32; c++) at += table[c * E + e];
+        r.list[at] = uint16_t(p);
+    }
     __syncthreads();
     r.groups = n_groups;
     return r;
@@ -175,7 +184,8 @@ struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], shifts_ready;
     uint32_t tmem;
     int dead;  // a wait gave up
-    int8_t shift[kShifts][kColumns];
+    // NVFP4: bits of the largest magnitude of x for the pairs of a task; down has them for all its pairs at once
+    int largest[kKept][kColumns / 16 * 3];
 };
 
 __device__ __forceinline__ bool wait_or_die(const LayerArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
@@ -197,12 +207,15 @@ struct Task {
 template <bool DOWN>
 struct Work {
     int index, step, count, block;  // down: groups index, index + step, ..; gate_up: (group, block) likewise
+    int c0, c1;                     // the slots of a weight row that are this block's
 
     __device__ __forceinline__ Work(const LayerArgs& a, const Routing& r, int rank, int ranks) {
-        index = DOWN ? rank : int(blockIdx.x);
-        step = DOWN ? ranks : int(gridDim.x);
+        index = DOWN ? rank : int(blockIdx.x) / ranks;
+        step = DOWN ? ranks : int(gridDim.x) / ranks;
         count = DOWN ? r.groups : r.groups * a.blocks;
         block = DOWN ? int(blockIdx.x) / ranks * 2 : 0;
+        c0 = DOWN ? 0 : a.chunks * rank / ranks;
+        c1 = DOWN ? a.chunks : a.chunks * (rank + 1) / ranks;
     }
     __device__ __forceinline__ int tasks() const { return index < count ? (count - index + step - 1) / step : 0; }
     __device__ __forceinline__ Task task(const LayerArgs& a, const Routing& r, int i) const {
@@ -224,7 +237,7 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
-        for (int c = 0; c < a.chunks; c++) {
+        for (int c = work.c0; c < work.c1; c++) {
             if (!wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
             const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * S::kSlot;
             const bool second = !DOWN || t.block + 1 < a.blocks;
@@ -295,15 +308,15 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
         const bool second = !DOWN || t.block + 1 < a.blocks;
         if (!warp_wait_or_die(a, s, &s->acc_empty[buf], (i >> 1 & 1) ^ 1)) return;
         tc_fence_after();
-        for (int c = 0; c < a.chunks; c++) {
+        for (int c = work.c0; c < work.c1; c++) {
             if (!warp_wait_or_die(a, s, &s->full[st], ph)) return;
             tc_fence_after();
             const int q = min(4, (a.row_bytes - c * 128) / 32);
             if (leader) {
                 multiply_slot<NVFP4, DOWN>(slots + st * S::kSlot, d, tmem + kTmemScales + st * kTmemScaleSet, idesc, q,
-                                           second, c > 0);
+                                           second, c > work.c0);
                 tc_commit(smem_addr(&s->empty[st]));
-                if (c + 1 == a.chunks) tc_commit(smem_addr(&s->acc_full[buf]));
+                if (c + 1 == work.c1) tc_commit(smem_addr(&s->acc_full[buf]));
             }
             __syncwarp();
             if (++st == a.stages) st = 0, ph ^= 1;
@@ -330,121 +343,192 @@ __device__ __forceinline__ float warp_max(float v) {
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
-__device__ __forceinline__ void st_shared_v2(uint32_t at, uint32_t x, uint32_t y) {
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
-}
-
-// A block of 16 values as the sum of kTerms NVFP4 blocks: codes to q[i], their scales to sf[i].
-__device__ __forceinline__ void split16(float* f, uint2* q, uint32_t* sf) {
+// Four lanes' blocks of 16 values (of two pairs, for their steps to overlap), four values each, as the sum of
+// kTerms NVFP4 blocks: a lane's four codes to q[.][i], the scale to sf[.][i].
+__device__ __forceinline__ void split16(float (&f)[2][4], uint32_t (&q)[2][kTerms], uint32_t (&sf)[2][kTerms]) {
 #pragma unroll
     for (int i = 0; i < kTerms; i++) {
-        float amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(f[j]));
-        sf[i] = e4m3x2(amax * (1.0f / 6.0f), 0.0f) & 0xffu;
-        const float s = e4m3_value(sf[i]);
-        const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-        uint32_t b[8];
-#pragma unroll
-        for (int p = 0; p < 8; p++) b[p] = e2m1x2(f[2 * p] * r, f[2 * p + 1] * r);
-        q[i] = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-        if (i + 1 < kTerms) {
-            uint32_t s2, v[8];
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(uint16_t(sf[i] * 0x101u)));
-            decode8(q[i].x, s2, v);  // exact
-            decode8(q[i].y, s2, v + 4);
-#pragma unroll
-            for (int p = 0; p < 8; p++) {
-                f[2 * p] = 8.0f * (f[2 * p] - __half2float(__ushort_as_half(uint16_t(v[p]))));
-                f[2 * p + 1] = 8.0f * (f[2 * p + 1] - __half2float(__ushort_as_half(uint16_t(v[p] >> 16))));
-            }
+        for (int b = 0; b < 2; b++) {
+            float(&v)[4] = f[b];
+            float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+            sf[b][i] = e4m3x2(amax * (1.0f / 6.0f), 0.0f) & 0xffu;
+            const float s = e4m3_value(sf[b][i]);
+            const float r = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
+            q[b][i] = e2m1x2(v[0] * r, v[1] * r) | e2m1x2(v[2] * r, v[3] * r) << 8;
+            if (i + 1 == kTerms) continue;
+            uint32_t v0, v1;
+            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+                "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
+                : "=r"(v0), "=r"(v1)
+                : "r"(q[b][i]));
+            // the product is exact, and the remainder as exact as fp32 gets
+            v[0] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0))), v[0]);
+            v[1] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0 >> 16))), v[1]);
+            v[2] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1))), v[2]);
+            v[3] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1 >> 16))), v[3]);
         }
     }
 }
 
-// Warp `v` of the converters: half the work of every `turns`th slot.
+// Four neighbouring values of x (bf16) or h (fp32) as they are in memory.
+template <bool DOWN>
+struct Four {
+    uint32_t w[DOWN ? 4 : 2];
+
+    __device__ __forceinline__ void load(const LayerArgs& a, int p, int k, bool ok) {
+#pragma unroll
+        for (int l = 0; l < (DOWN ? 4 : 2); l++) w[l] = 0;
+        if (!ok) return;
+        if constexpr (DOWN) {
+            const uint4 v = *reinterpret_cast<const uint4*>(h_values(a.f) + int64_t(p) * a.k + k);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.f.x + int64_t(p / a.f.K) * a.k + k));
+            w[0] = v.x, w[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void scaled(float scale, float (&f)[4]) const {
+        if constexpr (DOWN) {
+#pragma unroll
+            for (int l = 0; l < 4; l++) f[l] = __uint_as_float(w[l]) * scale;
+        } else {
+            f[0] = bf16_lo(w[0]) * scale, f[1] = bf16_hi(w[0]) * scale;
+            f[2] = bf16_lo(w[1]) * scale, f[3] = bf16_hi(w[1]) * scale;
+        }
+    }
+};
+
+// Warp `v` of the converters: half the work of every `turns`th slot. down: `shifts` [pairs in the list].
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
-                                             uint32_t slots, int v) {
+                                             uint32_t slots, int v, int8_t* shifts) {
     using S = Shape<NVFP4, DOWN>;
     const int lane = threadIdx.x & 31, tasks = work.tasks();
     const int turns = min(kTurns, a.stages), turn = v / 2, half = v % 2;
     if (turn >= turns) return;
     int seq = 0, st = 0;  // slots so far, over all tasks; their place in the ring
     uint32_t ph = 0;
+    if (NVFP4 && DOWN) {  // of every pair of the list, a thread a pair
+        const int parts = h_parts(a.k);
+        for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
+            const float4* from = reinterpret_cast<const float4*>(h_largest(a.f) + int64_t(r.list[at]) * parts);
+            float m = 0.0f;
+#pragma unroll 8
+            for (int p = 0; p < parts / 4; p++) {
+                const float4 w = from[p];
+                m = fmaxf(m, fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
+            }
+            shifts[at] = int8_t(shift_of(m));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
+        if (!warp_wait_or_die(a, s, &s->shifts_ready, 0)) return;
+    }
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         const uint16_t* list = r.list + t.first;
+        // NVFP4: four lanes a block, eight of a slot's sixteen blocks a warp, one pair after the other; the values of
+        // four pairs, and of the next slot's first four, are on their way (the task's first ones while the largest
+        // are looked for)
+        const int block = half * 8 + lane / 4, in = block * 16 + lane % 4 * 4;
+        Four<DOWN> now[4], then[4];
+        auto load = [&](Four<DOWN>& v4, int c, int j) {
+            const int k = c * S::kChunk + in;
+            const bool ok = c < work.c1 && j < t.n && k < a.k;
+            v4.load(a, list[ok ? j : 0], k, ok);
+        };
         if (NVFP4) {
-            int8_t* shift = s->shift[i % kShifts];
-            for (int j = v; j < t.n; j += 2 * turns) {
-                float m = 0.0f;
-                if (DOWN) {
-                    const int parts = h_parts(a.k);
-                    const float* from = h_largest(a.f) + int64_t(list[j]) * parts;
-                    for (int p = lane; p < parts; p += 32) m = fmaxf(m, __ldg(from + p));
-                } else {
-                    const uint16_t* x = a.f.x + int64_t(list[j] / a.f.K) * a.k;
-#pragma unroll 4
-                    for (int k = lane * 8; k < a.k; k += 256) {
-                        float f[8];
-                        unpack8(__ldg(reinterpret_cast<const uint4*>(x + k)), f);
+            const int first = work.c0 + (turn + turns - seq % turns) % turns;
 #pragma unroll
-                        for (int l = 0; l < 8; l++) m = fmaxf(m, fabsf(f[l]));
-                    }
+            for (int j = 0; j < 4; j++) load(now[j], first, j);
+        }
+        if (NVFP4 && !DOWN) {
+            int* largest = s->largest[i % kKept];
+            // every warp looks at its part of the rows, two at a time
+            for (int j = 0; j < t.n; j += 2) {
+                const uint16_t* x[2];
+                float m[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int l = 0; l < 2; l++) x[l] = a.f.x + int64_t(list[min(j + l, t.n - 1)] / a.f.K) * a.k;
+                for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * 2 * turns * 256) {
+                    uint4 w[2][4];
+#pragma unroll
+                    for (int l = 0; l < 2; l++)
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            const int k = k0 + u * 2 * turns * 256;
+                            w[l][u] = k < a.k ? __ldg(reinterpret_cast<const uint4*>(x[l] + k)) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                    for (int l = 0; l < 2; l++)
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            float f[8];
+                            unpack8(w[l][u], f);
+#pragma unroll
+                            for (int e = 0; e < 8; e++) m[l] = fmaxf(m[l], fabsf(f[e]));
+                        }
                 }
-                const int sh = shift_of(warp_max(m));
-                if (lane == 0) shift[j] = int8_t(sh);
+#pragma unroll
+                for (int l = 0; l < 2; l++) {
+                    const float most = warp_max(m[l]);
+                    if (lane == 0 && j + l < t.n) atomicMax(largest + j + l, __float_as_int(most));  // non-negative floats
+                }
             }
+            // long done with: a converter is at most 8 tasks ahead of what turns accumulators into results
+            if (v == 0 && lane < kColumns / 16 * 3) s->largest[(i + kKept / 2) % kKept][lane] = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
             if (!warp_wait_or_die(a, s, &s->shifts_ready, i & 1)) return;
         }
-        for (int c = 0; c < a.chunks; c++, seq++) {
+        for (int c = work.c0; c < work.c1; c++, seq++) {
             if (seq % turns == turn) {
                 const uint32_t to = slots + st * S::kSlot + S::kA;
                 bool free = false;  // the slot: the first values are ready before it is waited for
                 if (NVFP4) {
                     const uint32_t sf_to = to + S::kB + S::kSfA;
-                    for (int u0 = half * 32; u0 < t.n * 16; u0 += 64) {  // blocks of 16: pair u / 16, block u % 16 of the slot
-                        const int u = u0 + lane, j = u / 16, b = u % 16, k = c * S::kChunk + b * 16;
-                        float f[16];
 #pragma unroll
-                        for (int l = 0; l < 16; l++) f[l] = 0.0f;
-                        if (j < t.n && k < a.k) {
-                            if (DOWN) {
-                                const float4* h = reinterpret_cast<const float4*>(h_values(a.f) + int64_t(list[j]) * a.k + k);
+                    for (int j = 0; j < 4; j++) load(then[j], c + turns, j);
+#pragma unroll 1
+                    for (int j = 0; j < t.n; j += 2) {
+                        float f[2][4];
 #pragma unroll
-                                for (int l = 0; l < 4; l++) {
-                                    const float4 w = __ldg(h + l);
-                                    f[4 * l] = w.x, f[4 * l + 1] = w.y, f[4 * l + 2] = w.z, f[4 * l + 3] = w.w;
-                                }
-                            } else {
-                                const uint4* x = reinterpret_cast<const uint4*>(a.f.x + int64_t(list[j] / a.f.K) * a.k + k);
-                                unpack8(__ldg(x), f);
-                                unpack8(__ldg(x + 1), f + 8);
-                            }
-                            const float scale = pow2(s->shift[i % kShifts][j]);
-#pragma unroll
-                            for (int l = 0; l < 16; l++) f[l] *= scale;
+                        for (int l = 0; l < 2; l++) {
+                            const int at = min(j + l, t.n - 1);
+                            now[l].scaled(
+                                pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))), f[l]);
+                            now[l] = now[l + 2];
+                            if (j + l + 4 < t.n) load(now[l + 2], c, j + l + 4);
                         }
-                        uint2 q[kTerms];
-                        uint32_t sf[kTerms];
+                        uint32_t q[2][kTerms], sf[2][kTerms];
                         split16(f, q, sf);
                         if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
                         free = true;
-                        if (j < t.n) {
+#pragma unroll
+                        for (int b = 0; b < 2; b++) {
+                            if (j + b == t.n) break;
 #pragma unroll
                             for (int l = 0; l < kTerms; l++) {
-                                const int row = S::column(j) + l;
-                                st_shared_v2(to + swizzled(row, b >> 1) + (b & 1) * 8, q[l].x, q[l].y);
-                                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (b >> 2) * 512 + (row % 32) * 16 +
-                                                                            row / 32 * 4 + (b & 3)),
-                                             "r"(sf[l])
+                                const int row = S::column(j + b) + l;
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + swizzled(row, block >> 1) + (block & 1) * 8 +
+                                                                             lane % 4 * 2),
+                                             "h"(uint16_t(q[b][l]))
                                              : "memory");
+                                if (lane % 4 == 0)
+                                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
+                                                                                row / 32 * 4 + (block & 3)),
+                                                 "r"(sf[b][l])
+                                                 : "memory");
                             }
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; j++) now[j] = then[j];
                 } else {
                     const int parts = DOWN ? 2 : 1;
                     for (int u0 = half * 128; u0 < t.n * parts * 8; u0 += 256) {  // pieces of 8 values: row u / 8, piece u % 8
@@ -458,7 +542,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                                 const uint16_t* from =
                                     DOWN ? static_cast<const uint16_t*>(a.f.workspace) + (int64_t(p) * 2 + row % 2) * a.k
                                          : a.f.x + int64_t(p / a.f.K) * a.k;
-                                w[l] = __ldg(reinterpret_cast<const uint4*>(from + k));
+                                w[l] = *reinterpret_cast<const uint4*>(from + k);
                             }
                         }
                         if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
@@ -493,10 +577,27 @@ __device__ __forceinline__ float pair_sum(const float* v, int j) {
     return y;
 }
 
-// `sums`: down's [T][kRows] of this block; a thread has two rows of its own.
+// h of row `row` and pair p from its gate and up sums; a warp's lanes have 32 neighbouring rows.
+template <bool NVFP4>
+__device__ __forceinline__ void store_h(const FewTokens& f, int p, int row, float gate, float up) {
+    const float h = row < f.I ? swiglu(gate, up) : 0.0f;
+    if (NVFP4) {
+        if (row < f.I) h_values(f)[int64_t(p) * f.I + row] = h;
+        const float m = warp_max(fabsf(h));
+        if (row % 32 == 0) h_largest(f)[int64_t(p) * h_parts(f.I) + row / 32] = m;
+    } else if (row < f.I) {
+        uint16_t* to = static_cast<uint16_t*>(f.workspace) + int64_t(p) * 2 * f.I + row;
+        const uint32_t hi = pack_bf16x2(h, 0.0f) & 0xffffu;
+        to[0] = uint16_t(hi);
+        to[f.I] = uint16_t(pack_bf16x2(h - bf16_lo(hi), 0.0f));
+    }
+}
+
+// `sums` (of two rows, a thread's own): down's [T][kRows], or [pairs][kRows] of the one task that a cluster of
+// gate_up has together; null where gate_up's tasks are its own.
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
-                                            float* sums) {
+                                            float* sums, const int8_t* shifts) {
     constexpr int kPairs = NVFP4 ? 3 : DOWN ? 8 : 16;  // pairs of 16 columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tasks = work.tasks();
     const uint32_t lanes = uint32_t(warp * 32) << 16;
@@ -520,26 +621,22 @@ __device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const
             for (int j = 0; j < kPairs; j++) {
                 if (j0 + j >= t.n) break;
                 const int p = r.list[t.first + j0 + j];
-                const float unscale = alpha * (NVFP4 ? pow2(-s->shift[i % kShifts][j0 + j]) : 1.0f);
+                float unscale = alpha;
+                if (NVFP4)
+                    unscale *= pow2(DOWN ? -shifts[t.first + j0 + j]
+                                         : -shift_of(__int_as_float(s->largest[i % kKept][j0 + j])));
                 const float y0 = pair_sum<NVFP4, DOWN>(v0, j) * unscale, y1 = pair_sum<NVFP4, DOWN>(v1, j) * unscale;
                 if (DOWN) {
                     float* to = sums + (p / a.f.K) * kRows + warp * 32 + lane;
                     const float f = __ldg(a.f.w + p);
                     to[0] = fmaf(f, y0, to[0]);
                     to[128] = fmaf(f, y1, to[128]);
+                } else if (sums) {
+                    float* to = sums + (j0 + j) * kRows + warp * 32 + lane;
+                    to[0] = y0;
+                    to[128] = y1;
                 } else {
-                    const int row = t.block * 128 + warp * 32 + lane, I = a.f.I;
-                    const float h = row < I ? swiglu(y0, y1) : 0.0f;
-                    if (NVFP4) {
-                        if (row < I) h_values(a.f)[int64_t(p) * I + row] = h;
-                        const float m = warp_max(fabsf(h));
-                        if (lane == 0 && row < I) h_largest(a.f)[int64_t(p) * h_parts(I) + row / 32] = m;
-                    } else if (row < I) {
-                        uint16_t* to = static_cast<uint16_t*>(a.f.workspace) + int64_t(p) * 2 * I + row;
-                        const uint32_t hi = pack_bf16x2(h, 0.0f) & 0xffffu;
-                        to[0] = uint16_t(hi);
-                        to[I] = uint16_t(pack_bf16x2(h - bf16_lo(hi), 0.0f));
-                    }
+                    store_h<NVFP4>(a.f, p, t.block * 128 + warp * 32 + lane, y0, y1);
                 }
             }
         }
@@ -556,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
     float* sums = reinterpret_cast<float*>(base + a.stages * S::kSlot);
-    uint8_t* lists = base + a.stages * S::kSlot + (DOWN ? sizeof(float) * kRows * a.f.T : 0);
+    uint8_t* lists = base + a.stages * S::kSlot + sizeof(float) * kRows * a.summed;
+    int8_t* shifts = reinterpret_cast<int8_t*>(lists + routing_bytes(a.f.T * a.f.K));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s->tmem), 512);
@@ -575,24 +673,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (DOWN && warp < 4)
         for (int i = threadIdx.x; i < kRows * a.f.T; i += 128) sums[i] = 0.0f;  // a thread's own two rows
-    pdl_wait();
-    const Routing r = route(a.f, lists, S::kGroup, !DOWN && blockIdx.x == 0);
+    if (NVFP4)
+        for (int i = threadIdx.x; i < kKept * (kColumns / 16 * 3); i += kThreads) s->largest[0][i] = 0;
+    // down is released once every block of gate_up has come past its own wait: what came before gate_up is done, and
+    // only h, which the converters wait for, is not
+    if (!DOWN) {
+        pdl_wait();
+        pdl_release();
+        // the tokens' rows to L2, before the first weights: behind these they would wait for a whole ring of every SM
+        const char* x = reinterpret_cast<const char*>(a.f.x);
+        const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 128;
+        if (at < int64_t(a.f.T) * a.f.H * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + at));
+    }
+    const Routing r = route(a.f, lists, base, S::kGroup, !DOWN && blockIdx.x == 0);
     const cg::cluster_group cluster = cg::this_cluster();
-    const int rank = DOWN ? int(cluster.block_rank()) : 0, ranks = DOWN ? int(cluster.num_blocks()) : 1;
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
     const Work<DOWN> work(a, r, rank, ranks);
+    fence_proxy_async();  // route()'s scratch is where the first loads land
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
     if (warp < 4)
-        result_role<NVFP4, DOWN>(a, s, r, work, sums);
+        result_role<NVFP4, DOWN>(a, s, r, work, a.summed > 0 ? sums : nullptr, shifts);
     else if (warp == kLoadWarp) {
         if (lane == 0) load_role<NVFP4, DOWN>(a, s, r, work, slots, &map);
     } else if (warp == kMmaWarp) {
         mma_role<NVFP4, DOWN>(a, s, r, work, slots);
     } else {
-        convert_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kConvertWarp);
+        if (DOWN) pdl_wait();
+        convert_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kConvertWarp, shifts);
     }
+    if (DOWN) pdl_wait();  // a block without work does not end before gate_up has either
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -604,61 +716,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (warp == kMmaWarp) tmem_free(s->tmem, 512);
+    if (a.summed == 0) return;
+    cluster.sync();
+    auto total = [&](int i) {  // of the cluster's sums, in order
+        float y = 0.0f;
+        for (int b = 0; b < ranks; b++) y += cluster.map_shared_rank(sums, b)[i];
+        return y;
+    };
     if (DOWN) {
-        cluster.sync();
         for (int i = rank * kThreads + int(threadIdx.x); i < kRows * a.f.T; i += ranks * kThreads) {
             const int row = work.block * 128 + i % kRows;
-            float y = 0.0f;
-            for (int b = 0; b < ranks; b++) y += cluster.map_shared_rank(sums, b)[i];
+            const float y = total(i);
             if (row < a.f.H) a.f.out[int64_t(i / kRows) * a.f.H + row] = uint16_t(pack_bf16x2(y, 0.0f));
         }
-        cluster.sync();  // no block's sums go before the others have read them
+    } else if (work.tasks() > 0) {
+        const Task t = work.task(a, r, 0);
+        for (int i = rank * kThreads + int(threadIdx.x); i < 128 * t.n; i += ranks * kThreads) {
+            const int j = i / 128, row = i % 128;
+            store_h<NVFP4>(a.f, r.list[t.first + j], t.block * 128 + row, total(j * kRows + row),
+                           total(j * kRows + 128 + row));
+        }
     }
+    cluster.sync();  // no block's sums go before the others have read them
 }
 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+// Whether `owners` clusters of `ranks` blocks can be resident at once (GPCs hold whole clusters), cached per
+// device: it depends on the kernel, its shared memory and the device alone.
+template <typename Kernel>
+bool clusters_fit(const LaunchCtx& ctx, Kernel kern, cudaLaunchConfig_t cfg, int owners, int ranks) {
+    constexpr int kDevices = 64;
+    static std::mutex mu;
+    static struct {
+        size_t smem;
+        int most;
+    } cache[kDevices][kMaxRanks + 1];
+    const bool known = ctx.device >= 0 && ctx.device < kDevices;
+    if (known) {
+        std::lock_guard<std::mutex> lock(mu);
+        const auto& c = cache[ctx.device][ranks];
+        if (c.smem == cfg.dynamicSmemBytes) return owners <= c.most;
+    }
+    int most = 0;
+    cfg.gridDim = dim3(unsigned(ranks));
+    if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that the device does not have does not fit
+        most = 0;
+    }
+    if (known) {
+        std::lock_guard<std::mutex> lock(mu);
+        cache[ctx.device][ranks].smem = cfg.dynamicSmemBytes;
+        cache[ctx.device][ranks].most = most;
+    }
+    return owners <= most;
+}
+
 template <bool NVFP4, bool DOWN>
 cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     using S = Shape<NVFP4, DOWN>;
     constexpr size_t kMost = 226 * 1024;  // dynamic shared memory beside the static part
     const int rows = DOWN ? f.H : f.I, k = DOWN ? f.I : f.H, pairs = f.T * f.K;
-    LayerArgs a{f, 0, 0, NVFP4 ? k / 2 : 2 * k, (rows + 127) / 128, k};
+    LayerArgs a{f, 0, 0, NVFP4 ? k / 2 : 2 * k, (rows + 127) / 128, k, 0};
     a.chunks = (a.row_bytes + 127) / 128;
-    const size_t fixed = 1024 + (DOWN ? sizeof(float) * kRows * f.T : 0) + routing_bytes(pairs, f.E) + sizeof(Shared);
-    a.stages = int(std::min<size_t>(kMaxStages, (kMost - fixed) / S::kSlot));
-    const size_t smem = fixed - sizeof(Shared) + size_t(a.stages) * S::kSlot;
 
     CUtensorMap map;
     const uint64_t dims[4] = {uint64_t(a.row_bytes), uint64_t(rows), DOWN ? 1u : 2u, uint64_t(f.E)};
     const uint32_t box[4] = {128, DOWN ? 256u : 128u, DOWN ? 1u : 2u, 1};
     if (!make_map(&map, DOWN ? f.w2 : f.w13, 4, dims, box)) return cudaErrorInvalidValue;
-    auto kern = few_tokens_kernel<NVFP4, DOWN>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (err != cudaSuccess) return err;
 
-    const int experts = std::min(pairs, f.E);
-    if (!DOWN) {
-        // one block for each SM; fewer where there are fewer tasks
-        const int64_t tasks = int64_t(pairs) * a.blocks;
-        return launch_pdl(ctx, kern, dim3(unsigned(std::min<int64_t>(tasks, ctx.num_sms))), dim3(kThreads), smem, a, map);
-    }
-    const int owners = (a.blocks + 1) / 2;
-    int ranks = 1;  // as many as there are SMs and experts for
-    while (ranks < 8 && owners * ranks * 2 <= ctx.num_sms && ranks * 2 <= experts) ranks *= 2;
+    // gate_up: a cluster for each task while at least two blocks a task fit the SMs, else a block for each SM
+    const int64_t tasks = int64_t(pairs) * a.blocks;
+    const int64_t owners = DOWN ? (a.blocks + 1) / 2 : std::min<int64_t>(tasks, ctx.num_sms);
+    int ranks = int(std::min<int64_t>({kMaxRanks, ctx.num_sms / owners, DOWN ? std::min(pairs, f.E) : a.chunks}));
+    // whole pairs of SMs: with odd sizes, clusters that start as SMs become free did not all fit (a second
+    // round of down, 28 clusters of 5: 459 us for 32 tokens against 345 us)
+    ranks = ranks > 1 ? ranks / 2 * 2 : 1;
+    if (DOWN) a.summed = f.T;
+    else if (ranks > 1) a.summed = std::min(pairs, S::kGroup);
+    const size_t fixed = 1024 + sizeof(float) * kRows * a.summed + routing_bytes(pairs) + pairs;
+    a.stages = int(std::min<size_t>(kMaxStages, (kMost - sizeof(Shared) - fixed) / S::kSlot));
+
+    auto kern = few_tokens_kernel<NVFP4, DOWN>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(owners * ranks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = fixed + size_t(a.stages) * S::kSlot;
     cfg.stream = ctx.stream;
+    cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(cfg.dynamicSmemBytes));
+    if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(ranks);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    for (;; ranks -= ranks > 2 ? 2 : 1) {
+        attr[0].val.clusterDim.x = unsigned(ranks);
+        if (ranks == 1 || clusters_fit(ctx, kern, cfg, int(owners), ranks)) break;
+    }
+    cfg.gridDim = dim3(unsigned(owners * ranks));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a, map);
 }
