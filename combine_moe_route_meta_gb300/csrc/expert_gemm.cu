@@ -221,10 +221,10 @@ __device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_
     }
 }
 
-__device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float alpha, bool wide) {
+__device__ __forceinline__ void store_out16(uint16_t* dst, const uint32_t* v, float alpha, bool wide) {
     uint32_t w[8];
 #pragma unroll
-    for (int p = 0; p < 8; p++) w[p] = pack_bf16x2(alpha * v[2 * p], alpha * v[2 * p + 1]);
+    for (int p = 0; p < 8; p++) w[p] = pack_bf16x2(alpha * __uint_as_float(v[2 * p]), alpha * __uint_as_float(v[2 * p + 1]));
     if (wide) {
         st_v8(dst, w);
     } else {
@@ -234,11 +234,11 @@ __device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float
 }
 
 // One block of 16 SwiGLU outputs as codes and a scale byte.
-__device__ __forceinline__ uint32_t quantise_h(const float* gate, const float* up, float alpha, float gs, uint2* codes) {
+__device__ __forceinline__ uint32_t quantise_h(const uint32_t* gate, const uint32_t* up, float alpha, float gs, uint2* codes) {
     float h[16], amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; j++) {
-        h[j] = swiglu(alpha * gate[j], alpha * up[j]);
+        h[j] = swiglu(alpha * __uint_as_float(gate[j]), alpha * __uint_as_float(up[j]));
         amax = fmaxf(amax, fabsf(h[j]));
     }
     const uint32_t sf = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), gs), 0.0f) & 0xffu;
@@ -268,46 +268,36 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, Shared* s, int 
         const int64_t r = int64_t(tile.row0) + m;
         if (!warp_wait_or_die(a, s, &s->acc_full, n_tile & 1)) return;
         tc_fence_after();
-        if constexpr (!SWIGLU) {
+        // the warp's half of the tile to registers at once, so that the next tile's products can begin: 128
+        // columns, with SwiGLU 64 gate columns and their up columns
+        uint32_t r32[128];
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                float v[32];
-                const int col = half * 128 + c * 32;
-                tmem_load32(tmem + col, v);
-                if (c == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty));
-                }
-                uint16_t* dst = a.g.out + r * a.g.n + tile.n0 + col;
-                if (valid && tile.n0 + col < a.g.n) store_out16(dst, v, alpha, a.wide_out);
-                if (valid && tile.n0 + col + 16 < a.g.n) store_out16(dst + 16, v + 16, alpha, a.wide_out);
-            }
+        for (int c = 0; c < 4; c++)
+            tmem_load32(tmem + (SWIGLU ? c / 2 * (kTileN / 2) + half * 64 + c % 2 * 32 : half * 128 + c * 32), r32 + c * 32);
+        tmem_wait(r32, 128);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty));
+        if (!valid) continue;
+        if constexpr (!SWIGLU) {
+            const int col = tile.n0 + half * 128;
+            uint16_t* dst = a.g.out + r * a.g.n + col;
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                if (col + c * 16 < a.g.n) store_out16(dst + c * 16, r32 + c * 16, alpha, a.wide_out);
         } else {
             // 64 columns of h: 32 bytes of codes and one word of scales
-            const int col = half * 64;
+            const int n = tile.n0 + half * 64;
+            if (n >= a.g.n) continue;
             uint32_t sf = 0;
             uint2 q[4];
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                float gate[32], up[32];
-                tmem_load32(tmem + col + c * 32, gate);
-                tmem_load32(tmem + kTileN / 2 + col + c * 32, up);
-                if (c == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty));
-                }
-                sf |= quantise_h(gate, up, alpha, a.g.h_scale, &q[2 * c]) << (16 * c);
-                sf |= quantise_h(gate + 16, up + 16, alpha, a.g.h_scale, &q[2 * c + 1]) << (16 * c + 8);
-            }
-            const int n = tile.n0 + col;
-            if (valid && n < a.g.n) {
-                uint8_t* dst = a.g.h + r * (a.g.n / 2) + n / 2;
-                st_v4(dst, make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
-                st_v4(dst + 16, make_uint4(q[2].x, q[2].y, q[3].x, q[3].y));
-                *reinterpret_cast<uint32_t*>(a.g.h_sf + act_sf_index(a.g.scale_layout, r, n / 16, a.g.n / 16)) = sf;
-            }
+            for (int c = 0; c < 4; c++)
+                sf |= quantise_h(r32 + c * 16, r32 + 64 + c * 16, alpha, a.g.h_scale, &q[c]) << (8 * c);
+            uint8_t* dst = a.g.h + r * (a.g.n / 2) + n / 2;
+            st_v4(dst, make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
+            st_v4(dst + 16, make_uint4(q[2].x, q[2].y, q[3].x, q[3].y));
+            *reinterpret_cast<uint32_t*>(a.g.h_sf + act_sf_index(a.g.scale_layout, r, n / 16, a.g.n / 16)) = sf;
         }
     }
 }
