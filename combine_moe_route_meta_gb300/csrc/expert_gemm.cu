@@ -29,7 +29,8 @@ constexpr int kChunk = 256;                           // values of K per slot: 1
 constexpr int kStages = 4;
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr int kLoaderWarps = 2;
+constexpr int kLoaderWarps = 2;                       // of row scales, taking slots in turn
+static_assert(kStages % kLoaderWarps == 0, "a loader's next slot is less than a round of the ring ahead");
 constexpr int kEpilogueWarps = 8;
 constexpr uint32_t kBytesA = kTileM * 128;            // codes of a slot
 constexpr uint32_t kBytesB = kTileN * 128;
@@ -173,51 +174,67 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t 
     if (n_tile > 0) warp_wait_or_die(a, s, &s->empty[st == 0 ? kStages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
 }
 
-// Row scales that are not whole tiles of the layout: each of the 64 threads brings the scales of two rows.
+// Row scales that are not whole tiles of the layout: a warp brings every second slot's, a lane those of four rows
+// (16 bytes of a tile's line), with its next slot's (of the next tile too) on their way while it waits for one.
 template <bool SWIGLU>
-__device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_t slots, int i) {
-    const int C = a.g.k / 16, k64 = a.g.k / 64;
-    int st = 0;
+__device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_t slots, int turn) {
+    const int C = a.g.k / 16, k64 = a.g.k / 64, lane = threadIdx.x & 31;
+    const bool tiles = a.g.scale_layout == MOE_SCALES_SWIZZLED_128X4;
+    const int step = tiles ? 512 : 4;  // bytes from word to word
+    const bool whole = !tiles && C % 16 == 0 && reinterpret_cast<uintptr_t>(a.g.a_sf) % 16 == 0;  // a slot's words at once
+    int t = blockIdx.x, c = turn;  // of the words to load next
+    int64_t src[4];
+    bool fresh = true;
+    uint32_t next[4][4];
+    int st = turn;
     uint32_t ph = 0;
-    for (int t = blockIdx.x; t < s->tiles; t += gridDim.x) {
-        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
-        const uint8_t* src[2];
-        for (int j = 0; j < 2; j++) {
-            const int64_t r = min(int64_t(tile.row0) + i + 64 * j, a.g.rows - 1);
-            src[j] = a.g.a_sf + act_sf_index(a.g.scale_layout, r, 0, C);
+    for (bool first = true;; first = false) {
+        uint32_t v[4][4];
+        const bool have = !first && t < s->tiles;
+        if (!first) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int w = 0; w < 4; w++) v[j][w] = next[j][w];
+            if (!have) return;
+            for (c += kLoaderWarps; c >= a.chunks; c -= a.chunks) t += gridDim.x, fresh = true;
+        } else {
+            for (; c >= a.chunks; c -= a.chunks) t += gridDim.x;
         }
-        const int step = a.g.scale_layout == MOE_SCALES_SWIZZLED_128X4 ? 512 : 4;  // bytes from word to word
-        auto load = [&](int c, uint32_t* v) {
+        if (t < s->tiles) {
+            if (fresh) {
+                const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+                for (int j = 0; j < 4; j++)
+                    src[j] = act_sf_index(a.g.scale_layout, min(int64_t(tile.row0) + lane + 32 * j, a.g.rows - 1), 0, C);
+                fresh = false;
+            }
 #pragma unroll
-                for (int w = 0; w < 4; w++)
-                    v[j * 4 + w] = c * 4 + w < k64
-                                       ? __ldg(reinterpret_cast<const uint32_t*>(src[j] + int64_t(c * 4 + w) * step))
-                                       : 0u;
-        };
-        uint32_t v[8], next[8];  // the next slot's words are on their way while this one's wait
-        load(0, v);
-        for (int c = 0; c < a.chunks; c++) {
-            load(c + 1, next);
-            if (!warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
-            const uint32_t sfa = slots + st * kSlot + kBytesA + kBytesB;
+            for (int j = 0; j < 4; j++) {
+                const uint8_t* from = a.g.a_sf + src[j] + int64_t(c) * 4 * step;
+                if (whole) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(from));
+                    next[j][0] = u.x, next[j][1] = u.y, next[j][2] = u.z, next[j][3] = u.w;
+                } else {
 #pragma unroll
-            for (int j = 0; j < 2; j++)
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    const int r = i + 64 * j;
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sfa + w * 512 + (r % 32) * 16 + r / 32 * 4),
-                                 "r"(v[j * 4 + w])
-                                 : "memory");
+                    for (int w = 0; w < 4; w++)
+                        next[j][w] = c * 4 + w < k64 ? __ldg(reinterpret_cast<const uint32_t*>(from + w * step)) : 0u;
                 }
-            fence_proxy_async();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&s->full[st]));
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = next[j];
-            if (++st == kStages) st = 0, ph ^= 1;
+            }
         }
+        if (first) continue;
+        if (!warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+        const uint32_t to = slots + st * kSlot + kBytesA + kBytesB + lane * 16;
+#pragma unroll
+        for (int w = 0; w < 4; w++)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + w * 512), "r"(v[0][w]), "r"(v[1][w]),
+                         "r"(v[2][w]), "r"(v[3][w])
+                         : "memory");
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s->full[st]));
+        st += kLoaderWarps;
+        if (st >= kStages) st -= kStages, ph ^= 1;
     }
 }
 
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s->tiles = sum * a.tiles_n;
             s->dead = 0;
             for (int i = 0; i < kStages; i++) {
-                mbar_init(smem_addr(&s->full[i]), 1 + (sf_bulk ? 0 : kLoaderWarps));
+                mbar_init(smem_addr(&s->full[i]), sf_bulk ? 1 : 2);
                 mbar_init(smem_addr(&s->empty[i]), 1);
             }
             mbar_init(smem_addr(&s->acc_full), 1);
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         mma_role<SWIGLU>(a, s, slots);
     } else if (warp < 4) {
-        if (!sf_bulk) scale_role<SWIGLU>(a, s, slots, int(threadIdx.x) - 64);
+        if (!sf_bulk) scale_role<SWIGLU>(a, s, slots, warp - 2);
     } else {
         epilogue_role<SWIGLU>(a, s, warp);
     }

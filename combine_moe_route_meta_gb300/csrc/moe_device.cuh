@@ -227,8 +227,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 // blocks of the kernel before it exit. Releasing it at the start of a kernel let its blocks
 // take SM resources while they waited, which slowed the large dispatch/combine steps by up to
 // 30 % on GB300 (measured), and gained nothing at decode sizes.
-// The few-token layer's first kernel does (pdl_release): its blocks are all resident from the start, so its
-// dependent's take only SMs that are free, and load weights there.
+// The expert kernels that fill an SM with one block do (pdl_release): their blocks are all resident from the start and
+// leave no room beside them, so a dependent's blocks take only SMs that are free.
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
