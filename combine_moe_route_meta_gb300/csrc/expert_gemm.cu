@@ -51,7 +51,7 @@ struct GemmArgs {
 };
 
 struct Tile {
-    int e, n0, row0, rows;  // expert, first column (of gate), first row, rows of the expert from there on
+    int e, n0, row0, rows;  // expert, first column (of gate), first row, rows
 };
 
 struct Shared {
@@ -59,11 +59,17 @@ struct Shared {
     uint32_t tmem;
     int dead;       // a wait gave up
     int tiles;
-    int prefix[1];  // [E + 1]: row tiles of the experts before e
+    // behind: prefix [E + 1], row tiles of the experts before e; base [E], first rows; last [E], rows of the last tile - 1
+    __device__ __forceinline__ int* prefix() { return reinterpret_cast<int*>(this + 1); }
+    __device__ __forceinline__ int* base(int E) { return prefix() + E + 1; }
+    __device__ __forceinline__ uint8_t* last(int E) { return reinterpret_cast<uint8_t*>(base(E) + E); }
 };
+constexpr size_t shared_bytes(int E) { return sizeof(Shared) + size_t(E + 1) * 4 + size_t(E) * 5; }
+static_assert(1024 + kStages * kSlot + shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
 
 template <bool SWIGLU>
-__device__ __forceinline__ Tile find_tile(const GemmArgs& a, const int* prefix, int t) {
+__device__ __forceinline__ Tile find_tile(const GemmArgs& a, Shared* s, int t) {
+    const int* prefix = s->prefix();
     int lo = 0, hi = a.g.E;  // prefix[lo] * tiles_n <= t < prefix[hi] * tiles_n
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -74,9 +80,9 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, const int* prefix, 
     }
     const int rows_t = prefix[lo + 1] - prefix[lo];
     const int i = int(t - int64_t(prefix[lo]) * a.tiles_n);
-    const RowSpan s = expert_rows(a.g, lo);
     const int m = i % rows_t;
-    return Tile{lo, i / rows_t * (SWIGLU ? kTileN / 2 : kTileN), int(s.base) + m * kTileM, s.count - m * kTileM};
+    return Tile{lo, i / rows_t * (SWIGLU ? kTileN / 2 : kTileN), s->base(a.g.E)[lo] + m * kTileM,
+                m + 1 < rows_t ? kTileM : s->last(a.g.E)[lo] + 1};
 }
 
 // Bounded wait; false (and the CTA marked dead) when it gave up or another role already had.
@@ -100,7 +106,7 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x) {
-        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const Tile tile = find_tile<SWIGLU>(a, s, t);
         for (int c = 0; c < a.chunks; c++) {
             if (!wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
             const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * kSlot;
@@ -153,7 +159,7 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t 
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
-        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const Tile tile = find_tile<SWIGLU>(a, s, t);
         const uint32_t idesc = idesc_nvfp4(SWIGLU ? kTileN : min(kTileN, a.g.n - tile.n0));
         if (!warp_wait_or_die(a, s, &s->acc_empty, (n_tile & 1) ^ 1)) return;
         tc_fence_after();
@@ -203,7 +209,7 @@ __device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_
         }
         if (t < s->tiles) {
             if (fresh) {
-                const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+                const Tile tile = find_tile<SWIGLU>(a, s, t);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     src[j] = act_sf_index(a.g.scale_layout, min(int64_t(tile.row0) + lane + 32 * j, a.g.rows - 1), 0, C);
@@ -278,7 +284,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, Shared* s, int 
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);
     int n_tile = 0;
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
-        const Tile tile = find_tile<SWIGLU>(a, s->prefix, t);
+        const Tile tile = find_tile<SWIGLU>(a, s, t);
         const float alpha = a.g.alpha ? __ldg(a.g.alpha + tile.e) : 1.0f;
         const int m = quad * 32 + lane;
         const bool valid = m < tile.rows;
@@ -336,24 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ragged = 0;
     for (int e = threadIdx.x; e < a.g.E; e += kThreads) {
         const RowSpan r = expert_rows(a.g, e);
-        s->prefix[e + 1] = (r.count + kTileM - 1) / kTileM;
+        s->prefix()[e + 1] = (r.count + kTileM - 1) / kTileM;
+        s->base(a.g.E)[e] = int(r.base);
+        s->last(a.g.E)[e] = uint8_t((r.count + kTileM - 1) % kTileM);
         ragged |= r.count > 0 && r.base % 128 != 0;
     }
     const bool sf_bulk = !__syncthreads_or(ragged) && a.sf_bulk_ok;
     if (warp == 0) {
         int sum = 0;
         for (int e0 = 0; e0 < a.g.E; e0 += 32) {
-            int v = e0 + lane < a.g.E ? s->prefix[e0 + lane + 1] : 0;
+            int v = e0 + lane < a.g.E ? s->prefix()[e0 + lane + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int u = __shfl_up_sync(kFullMask, v, o);
                 if (lane >= o) v += u;
             }
-            if (e0 + lane < a.g.E) s->prefix[e0 + lane + 1] = sum + v;
+            if (e0 + lane < a.g.E) s->prefix()[e0 + lane + 1] = sum + v;
             sum += __shfl_sync(kFullMask, v, 31);
         }
         if (lane == 0) {
-            s->prefix[0] = 0;
+            s->prefix()[0] = 0;
             s->tiles = sum * a.tiles_n;
             s->dead = 0;
             for (int i = 0; i < kStages; i++) {
@@ -405,7 +413,7 @@ cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
     const GemmArgs a{g, (g.k + kChunk - 1) / kChunk, (g.n + cols - 1) / cols,
                      g.scale_layout == MOE_SCALES_SWIZZLED_128X4 && reinterpret_cast<uintptr_t>(g.a_sf) % 16 == 0,
                      reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
-    const size_t smem = 1024 + size_t(kStages) * kSlot + sizeof(Shared) + sizeof(int) * size_t(g.E);
+    const size_t smem = 1024 + size_t(kStages) * kSlot + shared_bytes(g.E);
     auto kern = expert_gemm_kernel<SWIGLU>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (err != cudaSuccess) return err;

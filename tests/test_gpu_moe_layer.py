@@ -105,6 +105,28 @@ def test_same_bits_every_time():
         assert torch.equal(layer.run(torch.cuda.Stream()).view(torch.int16), first)
 
 
+def test_gates_far_from_zero():
+    """silu of gates from -3e38 to 3e38, by one-element dot products: x W13 = (gate, 1), W2 picks h."""
+    m = moe()
+    gates = torch.tensor([-3e38, -1e30, -200, -104, -89, -80.5, -50, -3, -1e-3, 0, 1e-3, 3, 50, 80.5, 89, 104, 1e30, 3e38])
+    H = I = 32
+    w13 = torch.zeros(1, 2 * I, H, dtype=torch.bfloat16)
+    n = len(gates)
+    w13[0, :n, 0] = gates.bfloat16()
+    w13[0, I:, 0] = 1
+    w2 = torch.eye(H)[None].bfloat16()
+    x = torch.zeros(1, H, dtype=torch.bfloat16)
+    x[0, 0] = 1
+    out, status = torch.empty(1, H, dtype=torch.bfloat16, device="cuda"), m.new_status()
+    m.moe_layer_few_tokens(x.cuda(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 1, device="cuda"),
+                           w13.cuda(), w2.cuda(), out, m.new_layer_workspace(1, 1, H, I, 1), status)
+    m.check_status(status)
+    g = w13[0, :n, 0].double()
+    want = g / (1 + torch.exp(-g))
+    got = out[0, :n].double().cpu()
+    assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-31).all(), got.tolist()
+
+
 def test_bad_ids_are_skipped_and_reported():
     m = moe()
     layer = Layer(6, 256, 128, 4, 3, "bf16", 0, False)
