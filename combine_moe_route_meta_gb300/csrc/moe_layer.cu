@@ -76,7 +76,7 @@ struct LayerArgs {
     int row_bytes;       // of a weight row
     int blocks;          // 128-row blocks of a weight matrix
     int k;
-    int summed;          // columns of a block's sums: T in down, the pairs of the one task of a cluster in gate_up
+    int summed;          // columns of sums: T in down, in gate_up the pairs of the one task of a cluster
 };
 
 // Workspace: h as fp32 [pairs][I] and the largest magnitude of each 32 of it [pairs][4 ceil(I/128)] (NVFP4), or
@@ -340,39 +340,38 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
-// Four lanes' blocks of 16 values (of two pairs, for their steps to overlap), four values each, as the sum of
-// kTerms NVFP4 blocks: a lane's four codes to q[.][i], the scale to sf[.][i].
-__device__ __forceinline__ void split16(float (&f)[2][4], uint32_t (&q)[2][kTerms], uint32_t (&sf)[2][kTerms]) {
-#pragma unroll
-    for (int i = 0; i < kTerms; i++) {
-#pragma unroll
-        for (int b = 0; b < 2; b++) {
-            float(&v)[4] = f[b];
-            float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
-            sf[b][i] = e4m3x2(amax * (1.0f / 6.0f), 0.0f) & 0xffu;
-            const float s = e4m3_value(sf[b][i]);
-            const float r = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
-            q[b][i] = e2m1x2(v[0] * r, v[1] * r) | e2m1x2(v[2] * r, v[3] * r) << 8;
-            if (i + 1 == kTerms) continue;
-            uint32_t v0, v1;
-            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-                "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
-                : "=r"(v0), "=r"(v1)
-                : "r"(q[b][i]));
-            // the product is exact, and the remainder as exact as fp32 gets
-            v[0] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0))), v[0]);
-            v[1] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0 >> 16))), v[1]);
-            v[2] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1))), v[2]);
-            v[3] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1 >> 16))), v[3]);
-        }
-    }
+// One term of a block of 16 values, four of them in each of four lanes: the lane's four codes, the scale, and in f 8
+// times what is left.
+__device__ __forceinline__ uint32_t split_term(float (&f)[4], uint32_t* sf) {
+    float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+    *sf = e4m3x2(amax * (1.0f / 6.0f), 0.0f) & 0xffu;
+    const float s = e4m3_value(*sf);
+    const float r = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
+    const uint32_t q = e2m1x2(f[0] * r, f[1] * r) | e2m1x2(f[2] * r, f[3] * r) << 8;
+    uint32_t v0, v1;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
+        : "=r"(v0), "=r"(v1)
+        : "r"(q));
+    // the product is exact, and the remainder as exact as fp32 gets
+    f[0] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0))), f[0]);
+    f[1] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0 >> 16))), f[1]);
+    f[2] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1))), f[2]);
+    f[3] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1 >> 16))), f[3]);
+    return q;
 }
 
 // Four neighbouring values of x (bf16) or h (fp32) as they are in memory.
@@ -413,22 +412,6 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
     if (turn >= turns) return;
     int seq = 0, st = 0;  // slots so far, over all tasks; their place in the ring
     uint32_t ph = 0;
-    if (NVFP4 && DOWN) {  // of every pair of the list, a thread a pair
-        const int parts = h_parts(a.k);
-        for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
-            const float4* from = reinterpret_cast<const float4*>(h_largest(a.f) + int64_t(r.list[at]) * parts);
-            float m = 0.0f;
-#pragma unroll 8
-            for (int p = 0; p < parts / 4; p++) {
-                const float4 w = from[p];
-                m = fmaxf(m, fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
-            }
-            shifts[at] = int8_t(shift_of(m));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
-        if (!warp_wait_or_die(a, s, &s->shifts_ready, 0)) return;
-    }
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         const uint16_t* list = r.list + t.first;
@@ -447,38 +430,42 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
 #pragma unroll
             for (int j = 0; j < 4; j++) load(now[j], first, j);
         }
+        if (NVFP4 && DOWN && i == 0) {  // of every pair of the list, a thread a pair
+            const int parts = h_parts(a.k);
+            for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
+                const float4* from = reinterpret_cast<const float4*>(h_largest(a.f) + int64_t(r.list[at]) * parts);
+                float m = 0.0f;
+#pragma unroll 8
+                for (int p = 0; p < parts / 4; p++) {
+                    const float4 w = from[p];
+                    m = fmaxf(m, fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
+                }
+                shifts[at] = int8_t(shift_of(m));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
+            if (!warp_wait_or_die(a, s, &s->shifts_ready, 0)) return;
+        }
         if (NVFP4 && !DOWN) {
             int* largest = s->largest[i % kKept];
-            // every warp looks at its part of the rows, two at a time
-            for (int j = 0; j < t.n; j += 2) {
-                const uint16_t* x[2];
-                float m[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int l = 0; l < 2; l++) x[l] = a.f.x + int64_t(list[min(j + l, t.n - 1)] / a.f.K) * a.k;
+            // every warp looks at its part of the rows
+            for (int j = 0; j < t.n; j++) {
+                const uint16_t* x = a.f.x + int64_t(list[j] / a.f.K) * a.k;
+                uint32_t m = 0;  // two bf16 magnitudes
                 for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * 2 * turns * 256) {
-                    uint4 w[2][4];
+                    uint4 w[4];
 #pragma unroll
-                    for (int l = 0; l < 2; l++)
+                    for (int u = 0; u < 4; u++) {
+                        const int k = k0 + u * 2 * turns * 256;
+                        w[u] = k < a.k ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            const int k = k0 + u * 2 * turns * 256;
-                            w[l][u] = k < a.k ? __ldg(reinterpret_cast<const uint4*>(x[l] + k)) : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                    for (int l = 0; l < 2; l++)
-#pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            float f[8];
-                            unpack8(w[l][u], f);
-#pragma unroll
-                            for (int e = 0; e < 8; e++) m[l] = fmaxf(m[l], fabsf(f[e]));
-                        }
+                    for (int u = 0; u < 4; u++)
+                        m = max_bf16x2(m, max_bf16x2(max_bf16x2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu),
+                                                     max_bf16x2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu)));
                 }
-#pragma unroll
-                for (int l = 0; l < 2; l++) {
-                    const float most = warp_max(m[l]);
-                    if (lane == 0 && j + l < t.n) atomicMax(largest + j + l, __float_as_int(most));  // non-negative floats
-                }
+                const float most = warp_max(fmaxf(bf16_lo(m), bf16_hi(m)));
+                if (lane == 0) atomicMax(largest + j, __float_as_int(most));  // non-negative floats
             }
             // long done with: a converter is at most 8 tasks ahead of what turns accumulators into results
             if (v == 0 && lane < kColumns / 16 * 3) s->largest[(i + kKept / 2) % kKept][lane] = 0;
@@ -506,7 +493,10 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                             if (j + l + 4 < t.n) load(now[l + 2], c, j + l + 4);
                         }
                         uint32_t q[2][kTerms], sf[2][kTerms];
-                        split16(f, q, sf);
+#pragma unroll
+                        for (int l = 0; l < kTerms; l++)
+#pragma unroll
+                            for (int b = 0; b < 2; b++) q[b][l] = split_term(f[b], &sf[b][l]);
                         if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
                         free = true;
 #pragma unroll
@@ -593,8 +583,8 @@ __device__ __forceinline__ void store_h(const FewTokens& f, int p, int row, floa
     }
 }
 
-// `sums` (of two rows, a thread's own): down's [T][kRows], or [pairs][kRows] of the one task that a cluster of
-// gate_up has together; null where gate_up's tasks are its own.
+// `sums` (of two rows, a thread's own): down's [T][kRows], or this block's [pairs][kRows] in the first block of a cluster
+// of gate_up, which has one task together; null where gate_up's tasks are its own.
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
                                             float* sums, const int8_t* shifts) {
@@ -652,8 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared* s = &shared;
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
     float* sums = reinterpret_cast<float*>(base + a.stages * S::kSlot);
-    uint8_t* lists = base + a.stages * S::kSlot + sizeof(float) * kRows * a.summed;
+    uint8_t* lists = base + a.stages * S::kSlot + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks);
     int8_t* shifts = reinterpret_cast<int8_t*>(lists + routing_bytes(a.f.T * a.f.K));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -686,16 +678,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (at < int64_t(a.f.T) * a.f.H * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + at));
     }
     const Routing r = route(a.f, lists, base, S::kGroup, !DOWN && blockIdx.x == 0);
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
     const Work<DOWN> work(a, r, rank, ranks);
     fence_proxy_async();  // route()'s scratch is where the first loads land
     tc_fence_before();
-    __syncthreads();
+    if (!DOWN && a.summed > 0)
+        cluster.sync();  // the first block's shared memory is there
+    else
+        __syncthreads();
     tc_fence_after();
 
     if (warp < 4)
-        result_role<NVFP4, DOWN>(a, s, r, work, a.summed > 0 ? sums : nullptr, shifts);
+        result_role<NVFP4, DOWN>(a, s, r, work, a.summed == 0 ? nullptr
+                                                : DOWN      ? sums
+                                                            : cluster.map_shared_rank(sums, 0) + rank * a.summed * kRows,
+                                 shifts);
     else if (warp == kLoadWarp) {
         if (lane == 0) load_role<NVFP4, DOWN>(a, s, r, work, slots, &map);
     } else if (warp == kMmaWarp) {
@@ -718,26 +714,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_free(s->tmem, 512);
     if (a.summed == 0) return;
     cluster.sync();
-    auto total = [&](int i) {  // of the cluster's sums, in order
-        float y = 0.0f;
-        for (int b = 0; b < ranks; b++) y += cluster.map_shared_rank(sums, b)[i];
-        return y;
-    };
     if (DOWN) {
         for (int i = rank * kThreads + int(threadIdx.x); i < kRows * a.f.T; i += ranks * kThreads) {
             const int row = work.block * 128 + i % kRows;
-            const float y = total(i);
+            float v[kMaxRanks], y = 0.0f;
+#pragma unroll
+            for (int b = 0; b < kMaxRanks; b++) v[b] = b < ranks ? cluster.map_shared_rank(sums, b)[i] : 0.0f;
+#pragma unroll
+            for (int b = 0; b < kMaxRanks; b++) y += v[b];
             if (row < a.f.H) a.f.out[int64_t(i / kRows) * a.f.H + row] = uint16_t(pack_bf16x2(y, 0.0f));
         }
-    } else if (work.tasks() > 0) {
+    } else if (rank == 0 && work.tasks() > 0) {
         const Task t = work.task(a, r, 0);
-        for (int i = rank * kThreads + int(threadIdx.x); i < 128 * t.n; i += ranks * kThreads) {
+        for (int i = threadIdx.x; i < 128 * t.n; i += kThreads) {
             const int j = i / 128, row = i % 128;
-            store_h<NVFP4>(a.f, r.list[t.first + j], t.block * 128 + row, total(j * kRows + row),
-                           total(j * kRows + 128 + row));
+            float gate = 0.0f, up = 0.0f;
+            for (int b = 0; b < ranks; b++) {
+                const float* from = sums + (b * a.summed + j) * kRows + row;
+                gate += from[0], up += from[128];
+            }
+            store_h<NVFP4>(a.f, r.list[t.first + j], t.block * 128 + row, gate, up);
         }
     }
-    cluster.sync();  // no block's sums go before the others have read them
+    if (DOWN)     cluster.sync();  // no block's sums go before the others have read them
 }
 
 // ---------------------------------------------------------------------------
@@ -793,9 +792,12 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     // whole pairs of SMs: with odd sizes, clusters that start as SMs become free did not all fit (a second
     // round of down, 28 clusters of 5: 459 us for 32 tokens against 345 us)
     ranks = ranks > 1 ? ranks / 2 * 2 : 1;
+    const int task_pairs = std::min(pairs, S::kGroup);
+    if (!DOWN) ranks = std::min(ranks, std::max(1, 32 / task_pairs / 2 * 2));  // their sums: at most 32 KB
     if (DOWN) a.summed = f.T;
-    else if (ranks > 1) a.summed = std::min(pairs, S::kGroup);
-    const size_t fixed = 1024 + sizeof(float) * kRows * a.summed + routing_bytes(pairs) + pairs;
+    else if (ranks > 1) a.summed = task_pairs;
+    const size_t fixed =
+        1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + pairs;
     a.stages = int(std::min<size_t>(kMaxStages, (kMost - sizeof(Shared) - fixed) / S::kSlot));
 
     auto kern = few_tokens_kernel<NVFP4, DOWN>;
