@@ -258,22 +258,11 @@ __device__ __forceinline__ void store_out16(uint16_t* dst, const uint32_t* v, fl
 
 // One block of 16 SwiGLU outputs as codes and a scale byte.
 __device__ __forceinline__ uint32_t quantise_h(const uint32_t* gate, const uint32_t* up, float alpha, float gs, uint2* codes) {
-    float h[16], amax = 0.0f;
+    float h[16];
 #pragma unroll
-    for (int j = 0; j < 16; j++) {
-        h[j] = swiglu(alpha * __uint_as_float(gate[j]), alpha * __uint_as_float(up[j]));
-        amax = fmaxf(amax, fabsf(h[j]));
-    }
-    const uint32_t sf = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), gs), 0.0f) & 0xffu;
-    const float sff = e4m3_value(sf);
-    *codes = make_uint2(0, 0);
-    if (sff != 0.0f) {
-        const float r = __fdiv_rn(gs, sff);
-        uint32_t b[8];
-#pragma unroll
-        for (int p = 0; p < 8; p++) b[p] = e2m1x2(__fmul_rn(h[2 * p], r), __fmul_rn(h[2 * p + 1], r));
-        *codes = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-    }
+    for (int j = 0; j < 16; j++) h[j] = swiglu(alpha * __uint_as_float(gate[j]), alpha * __uint_as_float(up[j]));
+    uint32_t sf;
+    *codes = quantise_block(h, gs, &sf);
     return sf;
 }
 

@@ -21,6 +21,22 @@ __device__ __forceinline__ void decode8(uint32_t codes, uint32_t s, uint32_t* ou
     for (int i = 0; i < 4; i++) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(out[i]) : "r"(s));
 }
 
+// A block of 16 values as NVFP4: its codes, and the scale. Binary32 steps: sf = e4m3((amax * (1/6)) * g) with 1/6 rounded,
+// r = g / value(sf), q = e2m1(x * r); all codes 0 where value(sf) is 0.
+__device__ __forceinline__ uint2 quantise_block(const float (&f)[16], float g, uint32_t* sf) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(f[j]));
+    *sf = e4m3x2(__fmul_rn(__fmul_rn(amax, 1.0f / 6.0f), g), 0.0f) & 0xffu;
+    const float s = e4m3_value(*sf);
+    if (s == 0.0f) return make_uint2(0, 0);
+    const float r = __fdiv_rn(g, s);
+    uint32_t b[8];
+#pragma unroll
+    for (int p = 0; p < 8; p++) b[p] = e2m1x2(__fmul_rn(f[2 * p], r), __fmul_rn(f[2 * p + 1], r));
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+}
+
 // 32 bytes to a 32-byte aligned address
 __device__ __forceinline__ void st_v8(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),

@@ -1,6 +1,6 @@
 // nvfp4_quant.cu -- bf16 rows to NVFP4 codes and block scales, and back.
 //
-//   quantise:    sf = e4m3((amax16 / 6) * g),  q = e2m1(x * (g / sf))   (dispatch_slice.cuh's arithmetic)
+//   quantise:    sf = e4m3((amax16 * (1/6)) * g),  q = e2m1(x * (g / sf))   (quantise_block)
 //   dequantise:  out = bf16((value(q) * value(sf)) / g)
 //
 // A thread takes one block of 16 elements at a time: 32 contiguous bytes of a bf16 row, 8 bytes of codes and
@@ -83,16 +83,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(QuantArgs a) {
         for (int i = 0; i < kTurns; i++) {
             const int r = p.r + i * kStep;
             const bool live = r < a.R && p.c < a.C;
-            const LaneCodes q = quantise16<MOE_QUANT_NVFP4_B16>(v[i], gs);
-            if (live) st_v2(a.codes + (at + int64_t(i) * kStep * a.C) * 8, make_uint2(q.q.x, q.q.y));
+            float f[16];
+            unpack8(v[i].v0, f);
+            unpack8(v[i].v1, f + 8);
+            uint32_t sf;
+            const uint2 q = quantise_block(f, gs, &sf);
+            if (live) st_v2(a.codes + (at + int64_t(i) * kStep * a.C) * 8, q);
             if (SWIZZLED || a.sf_words) {  // zero in the padding rows of a tile
-                uint32_t w = live ? q.scale << (8 * (threadIdx.x & 3)) : 0u;
+                uint32_t w = live ? sf << (8 * (threadIdx.x & 3)) : 0u;
                 w |= __shfl_xor_sync(kFullMask, w, 1);
                 w |= __shfl_xor_sync(kFullMask, w, 2);
                 if ((threadIdx.x & 3) == 0 && p.c < a.C && (SWIZZLED || r < a.R))
                     *reinterpret_cast<uint32_t*>(a.sf + sf_index<SWIZZLED>(a, p, r)) = w;
             } else if (live) {
-                a.sf[sf_index<SWIZZLED>(a, p, r)] = uint8_t(q.scale);
+                a.sf[sf_index<SWIZZLED>(a, p, r)] = uint8_t(sf);
             }
         }
     }

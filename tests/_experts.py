@@ -31,6 +31,21 @@ def values(codes, sf):
     return v * np.repeat(E4M3[sf], 16, axis=1)
 
 
+def quantise_rows(x_bits, g):
+    """codes and scales of bf16 rows [R, K], in the quantiser's binary32 steps (the formats are the oracle's)."""
+    R, K = x_bits.shape
+    x = bf16_bits_to_f32(x_bits).reshape(R, K // 16, 16)
+    g = np.float32(g)
+    with np.errstate(all="ignore"):
+        t = (np.abs(x).max(-1) * np.float32(1 / 6)) * g
+        sf = oracle.e4m3_from_float_array(t).reshape(R, K // 16)
+        v = E4M3[sf].astype(np.float32)
+        r = np.where(v > 0, g / v, np.float32(0))
+        q = oracle.e2m1_from_float_array(x * r[..., None]).reshape(R, K)
+    q = np.where(np.repeat(v > 0, 16, axis=1), q, 0).astype(np.uint8)
+    return q[:, 0::2] | (q[:, 1::2] << 4), sf
+
+
 def quantised(rng, R, K, std=1.0):
     """NVFP4 rows of N(0, std^2): codes, scales [R, K/16] and their global scale."""
     x = random_bf16(rng, (R, K), std)

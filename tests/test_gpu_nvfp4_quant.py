@@ -1,10 +1,10 @@
-"""NVFP4 quantisation and read-back against the CPU oracle, bit for bit."""
+"""NVFP4 quantisation and read-back against the definition on the CPU, bit for bit."""
 import numpy as np
 import pytest
 import torch
 
 import oracle
-from _experts import E4M3, interleave, values
+from _experts import E4M3, interleave, quantise_rows, values
 from _harness import filled, moe
 from workloads import bf16_bits_to_f32, f32_to_bf16_bits, random_bf16
 
@@ -30,9 +30,7 @@ def _check(x, g, layout):
     codes, scales, back = _run(x, g, layout)
     G, R, H = x.shape
     for j in range(G):
-        want_q, want_s = np.zeros((R, H // 2), np.uint8), np.zeros((R, H // 16), np.uint8)
-        for r in range(R):
-            want_q[r], want_s[r] = oracle.quant_nvfp4_row(x[j, r], float(np.float32(g[j])))
+        want_q, want_s = quantise_rows(x[j], g[j])
         assert np.array_equal(codes[j], want_q)
         flat = interleave(want_s) if layout == "swizzled" else want_s.reshape(-1)
         assert np.array_equal(scales[j], flat)
@@ -126,6 +124,27 @@ def test_offsets_past_32_bits():
     assert torch.equal(q.scales[0][at], tail.scales.flatten())
     back = m.dequantize_nvfp4(q, g)
     assert torch.equal(back[0, -2:], m.dequantize_nvfp4(tail, g)[0]) and not back[0, :-2].any()
+
+
+def test_agrees_with_the_dispatch_quantiser():
+    """The dispatch divides by 6 where the quantiser multiplies by 1/6: a block's scale may go to the other neighbour of a
+    boundary, and to nothing else; blocks with the same scale have the same codes."""
+    rng = np.random.default_rng(11)
+    x = random_bf16(rng, (1, 64, 1024))
+    g = 2688.0 / 4.0                     # many scales on boundaries
+    codes, scales, _ = _run(x, [g], "row")
+    same = total = 0
+    for r in range(64):
+        q, sf = oracle.quant_nvfp4_row(x[0, r], g)
+        s = scales[0].reshape(64, 64)[r]
+        assert (np.abs(sf.astype(int) - s.astype(int)) <= 1).all()
+        eq = sf == s
+        assert (codes[0, r].reshape(64, 8)[eq] == q.reshape(64, 8)[eq]).all()
+        t = np.abs(bf16_bits_to_f32(x[0, r])).reshape(64, 16).max(1).astype(np.float64) / 6 * g
+        mid = (E4M3[sf] + E4M3[s]) / 2
+        assert (np.abs(t - mid)[~eq] <= 2.0 ** -22 * t[~eq]).all()
+        same, total = same + int(eq.sum()), total + 64
+    assert same >= 0.9 * total
 
 
 def test_one_matrix():
