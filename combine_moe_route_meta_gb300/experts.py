@@ -11,7 +11,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (MOE_ERR_UNSUPPORTED, MOE_QUANT_NONE, MOE_QUANT_NVFP4_B16, MOE_SCALES_SWIZZLED_128X4, MODES,
+from . import (MOE_ERR_UNSUPPORTED, MOE_MODE_MASKED, MOE_QUANT_NONE, MOE_QUANT_NVFP4_B16, MOE_SCALES_SWIZZLED_128X4, MODES,
                SCALE_LAYOUTS, MoEError, _check, _need, _ptr, _stream, check_status, load_library, moe_combine_ex,
                moe_dispatch_ex, moe_route_meta_ex, new_status, new_workspace)
 
@@ -43,6 +43,31 @@ def _mode(mode: str) -> int:
     return MODES[mode]
 
 
+def _pointers(*specs):
+    """Checks (tensor or None, bytes needed, name, dtype) and returns the data pointers: element types and sizes of all of
+    them first, then that they are contiguous device tensors."""
+    out, wrong = [], None
+    for t, nbytes, name, dtype in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.nbytes < nbytes:
+            _need(t, nbytes, name, dtype)
+        if wrong is None and not (t.is_cuda and t.is_contiguous()):
+            wrong = t
+        out.append(t.data_ptr())
+    if wrong is not None:
+        _ptr(wrong)
+    return out
+
+
+def _on(stream):
+    """The handle of `stream`, or of torch's current one (the tensors are on the device: torch has its context)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
 # ---------------------------------------------------------------------------
 # thin wrappers with the C names
 # ---------------------------------------------------------------------------
@@ -51,12 +76,11 @@ def moe_quantize_nvfp4(x: torch.Tensor, global_scales: torch.Tensor, codes: torc
                        scale_layout: str = "swizzled", stream=None) -> None:
     """x [groups, rows, hidden] bf16 -> codes [groups, rows, hidden/2] and the groups' block scales."""
     G, R, H = x.shape
-    _need(x, 2 * G * R * H, "x", torch.bfloat16)
-    _need(global_scales, 4 * G, "global_scales", torch.float32)
-    _need(codes, G * R * (H // 2), "codes", torch.uint8)
-    _need(scales, G * nvfp4_scale_bytes(R, H, scale_layout), "scales", torch.uint8)
-    st = load_library().moe_quantize_nvfp4(_ptr(x), G, R, H, _ptr(global_scales), _layout(scale_layout), _ptr(codes),
-                                           _ptr(scales), _stream(stream))
+    layout = _layout(scale_layout)
+    px, pg, pc, ps = _pointers((x, 0, "x", torch.bfloat16), (global_scales, 4 * G, "global_scales", torch.float32),
+                               (codes, G * R * (H // 2), "codes", torch.uint8),
+                               (scales, G * nvfp4_scale_bytes(R, H, scale_layout), "scales", torch.uint8))
+    st = load_library().moe_quantize_nvfp4(px, G, R, H, pg, layout, pc, ps, _on(stream))
     _check(st, "moe_quantize_nvfp4")
 
 
@@ -64,30 +88,23 @@ def moe_dequantize_nvfp4(codes: torch.Tensor, scales: torch.Tensor, global_scale
                          scale_layout: str = "swizzled", stream=None) -> None:
     """The reverse of :func:`moe_quantize_nvfp4`, into out [groups, rows, hidden] bf16."""
     G, R, H = out.shape
-    _need(codes, G * R * (H // 2), "codes", torch.uint8)
-    _need(scales, G * nvfp4_scale_bytes(R, H, scale_layout), "scales", torch.uint8)
-    _need(global_scales, 4 * G, "global_scales", torch.float32)
-    _need(out, 2 * G * R * H, "out", torch.bfloat16)
-    st = load_library().moe_dequantize_nvfp4(_ptr(codes), _ptr(scales), G, R, H, _ptr(global_scales),
-                                             _layout(scale_layout), _ptr(out), _stream(stream))
+    layout = _layout(scale_layout)
+    pc, ps, pg, po = _pointers((codes, G * R * (H // 2), "codes", torch.uint8),
+                               (scales, G * nvfp4_scale_bytes(R, H, scale_layout), "scales", torch.uint8),
+                               (global_scales, 4 * G, "global_scales", torch.float32),
+                               (out, 0, "out", torch.bfloat16))
+    st = load_library().moe_dequantize_nvfp4(pc, ps, G, R, H, pg, layout, po, _on(stream))
     _check(st, "moe_dequantize_nvfp4")
 
 
-def _gemm_rows(mode: str, a_codes: torch.Tensor, E: int, M: int) -> int:
-    return E * M if mode == "masked" else a_codes.numel() // a_codes.shape[-1]
-
-
-def _check_gemm(mode, a_codes, a_scales, masked_m, seg_indptr, alpha, dev_status, scale_layout, E, rows, K):
-    _mode(mode)
-    _layout(scale_layout)
-    _need(a_codes, rows * (K // 2), "a_codes", torch.uint8)
-    _need(a_scales, nvfp4_scale_bytes(rows, K, scale_layout), "a_scales", torch.uint8)
-    _need(masked_m, 4 * E, "masked_m", torch.int32)
-    if mode == "normal" and seg_indptr is None:
+def _rows(mode: str, a_codes: torch.Tensor, K: int, E: int, M: int, seg_indptr) -> int:
+    if a_codes.shape[-1] != K // 2:
+        raise ValueError(f"a_codes: rows of {K // 2} bytes needed, got {a_codes.shape[-1]}")
+    if _mode(mode) == MOE_MODE_MASKED:
+        return E * M
+    if seg_indptr is None:
         raise ValueError("seg_indptr: needed in normal mode")
-    _need(seg_indptr, 8 * (E + 1) if mode == "normal" else 0, "seg_indptr", torch.int64)
-    _need(alpha, 4 * E, "alpha", torch.float32)
-    _need(dev_status, 4, "dev_status", torch.int32)
+    return a_codes.numel() // a_codes.shape[-1]
 
 
 def moe_expert_gemm(mode: str, a_codes: torch.Tensor, a_scales: torch.Tensor, masked_m: torch.Tensor,
@@ -97,18 +114,21 @@ def moe_expert_gemm(mode: str, a_codes: torch.Tensor, a_scales: torch.Tensor, ma
     """out[r] = alpha[e] * w[e] a[r] for the rows of every expert e of a dispatched layout.
 
     w_codes [E, n, k/2]; a_codes [rows, k/2] (normal) or [E, M, k/2] (masked, M = max_tokens_per_expert)."""
-    E, N, K = w_codes.shape[0], w_codes.shape[1], 2 * w_codes.shape[2]
-    rows = _gemm_rows(mode, a_codes, E, max_tokens_per_expert)
-    _check_gemm(mode, a_codes, a_scales, masked_m, seg_indptr, alpha, dev_status, scale_layout, E, rows, K)
-    _need(w_codes, E * N * (K // 2), "w_codes", torch.uint8)
-    _need(w_scales, E * nvfp4_scale_bytes(N, K, "swizzled"), "w_scales", torch.uint8)
-    _need(out, 2 * rows * N, "out", torch.bfloat16)
-    if a_codes.shape[-1] != K // 2:
-        raise ValueError(f"a_codes: rows of {K // 2} bytes needed, got {a_codes.shape[-1]}")
-    st = load_library().moe_expert_gemm(_mode(mode), _ptr(a_codes), _ptr(a_scales), _layout(scale_layout), E,
-                                        max_tokens_per_expert, rows, N, K, _ptr(seg_indptr), _ptr(masked_m),
-                                        _ptr(w_codes), _ptr(w_scales), _ptr(alpha), _ptr(out), _ptr(dev_status),
-                                        _stream(stream))
+    E, N, K = w_codes.shape
+    K *= 2
+    rows = _rows(mode, a_codes, K, E, max_tokens_per_expert, seg_indptr)
+    layout = _layout(scale_layout)
+    pa, pas, pm, pseg, pal, pw, pws, po, pst = _pointers(
+        (a_codes, rows * (K // 2), "a_codes", torch.uint8),
+        (a_scales, nvfp4_scale_bytes(rows, K, scale_layout), "a_scales", torch.uint8),
+        (masked_m, 4 * E, "masked_m", torch.int32),
+        (seg_indptr, 8 * (E + 1) if mode == "normal" else 0, "seg_indptr", torch.int64),
+        (alpha, 4 * E, "alpha", torch.float32),
+        (w_codes, 0, "w_codes", torch.uint8),
+        (w_scales, E * ((N + 127) // 128 * 128) * (K // 16), "w_scales", torch.uint8),
+        (out, 2 * rows * N, "out", torch.bfloat16), (dev_status, 4, "dev_status", torch.int32))
+    st = load_library().moe_expert_gemm(MODES[mode], pa, pas, layout, E, max_tokens_per_expert, rows, N, K, pseg, pm, pw,
+                                        pws, pal, po, pst, _on(stream))
     _check(st, "moe_expert_gemm")
 
 
@@ -118,19 +138,25 @@ def moe_expert_gemm_swiglu(mode: str, a_codes: torch.Tensor, a_scales: torch.Ten
                            alpha: Optional[torch.Tensor] = None, seg_indptr: Optional[torch.Tensor] = None,
                            max_tokens_per_expert: int = 0, scale_layout: str = "swizzled", stream=None) -> None:
     """The gate and up products (w13_codes [E, 2*inter, k/2]), SwiGLU and quantisation of its result in one kernel."""
-    E, N, K = w13_codes.shape[0], w13_codes.shape[1] // 2, 2 * w13_codes.shape[2]
-    rows = _gemm_rows(mode, a_codes, E, max_tokens_per_expert)
-    _check_gemm(mode, a_codes, a_scales, masked_m, seg_indptr, alpha, dev_status, scale_layout, E, rows, K)
-    _need(w13_codes, E * 2 * N * (K // 2), "w13_codes", torch.uint8)
-    _need(w13_scales, 2 * E * nvfp4_scale_bytes(N, K, "swizzled"), "w13_scales", torch.uint8)
-    _need(out_codes, rows * (N // 2), "out_codes", torch.uint8)
-    _need(out_scales, nvfp4_scale_bytes(rows, N, scale_layout), "out_scales", torch.uint8)
-    if a_codes.shape[-1] != K // 2 or w13_codes.shape[1] % 2:
-        raise ValueError(f"a_codes {tuple(a_codes.shape)} and w13_codes {tuple(w13_codes.shape)} do not fit")
-    st = load_library().moe_expert_gemm_swiglu(
-        _mode(mode), _ptr(a_codes), _ptr(a_scales), _layout(scale_layout), E, max_tokens_per_expert, rows, N, K,
-        _ptr(seg_indptr), _ptr(masked_m), _ptr(w13_codes), _ptr(w13_scales), _ptr(alpha), float(out_global_scale),
-        _ptr(out_codes), _ptr(out_scales), _ptr(dev_status), _stream(stream))
+    E, N, K = w13_codes.shape
+    if N % 2:
+        raise ValueError(f"w13_codes: gate and up rows do not fit {N} rows")
+    N, K = N // 2, 2 * K
+    rows = _rows(mode, a_codes, K, E, max_tokens_per_expert, seg_indptr)
+    layout = _layout(scale_layout)
+    pa, pas, pm, pseg, pal, pw, pws, po, pos, pst = _pointers(
+        (a_codes, rows * (K // 2), "a_codes", torch.uint8),
+        (a_scales, nvfp4_scale_bytes(rows, K, scale_layout), "a_scales", torch.uint8),
+        (masked_m, 4 * E, "masked_m", torch.int32),
+        (seg_indptr, 8 * (E + 1) if mode == "normal" else 0, "seg_indptr", torch.int64),
+        (alpha, 4 * E, "alpha", torch.float32),
+        (w13_codes, 0, "w13_codes", torch.uint8),
+        (w13_scales, 2 * E * ((N + 127) // 128 * 128) * (K // 16), "w13_scales", torch.uint8),
+        (out_codes, rows * (N // 2), "out_codes", torch.uint8),
+        (out_scales, nvfp4_scale_bytes(rows, N, scale_layout), "out_scales", torch.uint8),
+        (dev_status, 4, "dev_status", torch.int32))
+    st = load_library().moe_expert_gemm_swiglu(MODES[mode], pa, pas, layout, E, max_tokens_per_expert, rows, N, K, pseg,
+                                               pm, pw, pws, pal, float(out_global_scale), po, pos, pst, _on(stream))
     _check(st, "moe_expert_gemm_swiglu")
 
 
@@ -149,30 +175,29 @@ def moe_layer_few_tokens(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: 
     Weights bf16 (w13 [E, 2*inter, hidden], w2 [E, hidden, inter]) or, as uint8, NVFP4 codes with their scales."""
     T, H = x.shape
     K = topk_ids.shape[1]
-    E, I = w13.shape[0], w13.shape[1] // 2
-    nvfp4 = w13.dtype == torch.uint8
+    E, I2, W = w13.shape
+    I = I2 // 2
+    nvfp4 = w13.dtype is torch.uint8
     dtype, per = (torch.uint8, 2) if nvfp4 else (torch.bfloat16, 1)
-    if tuple(w13.shape) != (E, 2 * I, H // per) or tuple(w2.shape) != (E, H, I // per):
+    if I2 % 2 or W != H // per or tuple(w2.shape) != (E, H, I // per):
         raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit hidden {H}")
-    _need(x, 2 * T * H, "x", torch.bfloat16)
-    _need(topk_ids, 4 * T * K, "topk_ids", torch.int32)
-    _need(topk_weights, 4 * T * K, "topk_weights", torch.float32)
-    _need(w13, 0, "w13", dtype)
-    _need(w2, 0, "w2", dtype)
     if nvfp4 and (w13_scales is None or w2_scales is None):
         raise ValueError("w13_scales, w2_scales: needed with NVFP4 weights")
-    if nvfp4:
-        _need(w13_scales, 2 * E * nvfp4_scale_bytes(I, H, "swizzled"), "w13_scales", torch.uint8)
-        _need(w2_scales, E * nvfp4_scale_bytes(H, I, "swizzled"), "w2_scales", torch.uint8)
-    _need(alpha13, 4 * E, "alpha13", torch.float32)
-    _need(alpha2, 4 * E, "alpha2", torch.float32)
-    _need(out, 2 * T * H, "out", torch.bfloat16)
-    _need(dev_status, 4, "dev_status", torch.int32)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if not nvfp4:
+        w13_scales = w2_scales = None
+    px, pi, pt, p13, p2, ps13, ps2, pa13, pa2, po, pws, pst = _pointers(
+        (x, 0, "x", torch.bfloat16), (topk_ids, 0, "topk_ids", torch.int32),
+        (topk_weights, 4 * T * K, "topk_weights", torch.float32), (w13, 0, "w13", dtype), (w2, 0, "w2", dtype),
+        (w13_scales, 2 * E * ((I + 127) // 128 * 128) * (H // 16), "w13_scales", torch.uint8),
+        (w2_scales, E * ((H + 127) // 128 * 128) * (I // 16), "w2_scales", torch.uint8),
+        (alpha13, 4 * E, "alpha13", torch.float32), (alpha2, 4 * E, "alpha2", torch.float32),
+        (out, 2 * T * H, "out", torch.bfloat16), (workspace, 0, "workspace", torch.uint8),
+        (dev_status, 4, "dev_status", torch.int32))
+    if topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids: {T} rows needed, got {topk_ids.shape[0]}")
     st = load_library().moe_layer_few_tokens(
-        _ptr(x), T, H, I, _ptr(topk_ids), _ptr(topk_weights), K, E,
-        MOE_QUANT_NVFP4_B16 if nvfp4 else MOE_QUANT_NONE, _ptr(w13), _ptr(w13_scales), _ptr(alpha13), _ptr(w2),
-        _ptr(w2_scales), _ptr(alpha2), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
+        px, T, H, I, pi, pt, K, E, MOE_QUANT_NVFP4_B16 if nvfp4 else MOE_QUANT_NONE, p13, ps13, pa13, p2, ps2, pa2, po,
+        pws, workspace.nbytes if workspace is not None else 0, pst, _on(stream))
     _check(st, "moe_layer_few_tokens")
 
 
