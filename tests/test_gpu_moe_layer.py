@@ -230,3 +230,14 @@ def test_layer_object_refuses():
     layer = m.MoELayer(m.ExpertWeights(w13, w2), 2, 4)
     with pytest.raises(ValueError, match="5 tokens"):
         layer(torch.zeros(5, 128, dtype=torch.bfloat16, device="cuda"), None, None)
+
+
+def test_example_runs():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "moe_layer_nvfp4.py"), "--tokens", "1,70", "--experts",
+                        "8", "--hidden", "512", "--inter", "256", "--topk", "2"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.count("tokens:") == 2
