@@ -8,7 +8,7 @@
 // M side of its products, the few tokens of an expert the N side.
 //
 // NVFP4 weights need NVFP4 on the other side too. A block of 16 values of x (or h) is a sum of five such blocks,
-//   r0 = x 2^s;  q_i = nvfp4(8^i r_i);  r_{i+1} = r_i - 8^-i q_i;   x 2^s ~ sum 8^-i q_i,
+//   r_0 = x 2^s;  q_i = nvfp4(8^i r_i);  r_{i+1} = r_i - 8^-i q_i;   x 2^s ~ sum 8^-i q_i,
 // each of which leaves at most a sixth of the block's largest value (typically a twelfth): after five, 2^-13 of
 // it (typically 2^-18). So a pair has five columns, whose products are added in fp32 with the weights 8^-i.
 // s, for each column's whole length, brings its largest value to [2^8, 2^9), in the range of e4m3 scales.
@@ -349,56 +349,77 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
-// One term of a block of 16 values, four of them in each of four lanes: the lane's four codes, the scale, and in f 8
-// times what is left.
-__device__ __forceinline__ uint32_t split_term(float (&f)[4], uint32_t* sf) {
-    float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
-    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
-    *sf = e4m3x2(amax * (1.0f / 6.0f), 0.0f) & 0xffu;
-    const float s = e4m3_value(*sf);
-    const float r = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
-    const uint32_t q = e2m1x2(f[0] * r, f[1] * r) | e2m1x2(f[2] * r, f[3] * r) << 8;
-    uint32_t v0, v1;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
-        : "=r"(v0), "=r"(v1)
-        : "r"(q));
-    // the product is exact, and the remainder as exact as fp32 gets
-    f[0] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0))), f[0]);
-    f[1] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v0 >> 16))), f[1]);
-    f[2] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1))), f[2]);
-    f[3] = 8.0f * fmaf(-s, __half2float(__ushort_as_half(uint16_t(v1 >> 16))), f[3]);
-    return q;
-}
-
-// Four neighbouring values of x (bf16) or h (fp32) as they are in memory.
-template <bool DOWN>
-struct Four {
-    uint32_t w[DOWN ? 4 : 2];
-
-    __device__ __forceinline__ void load(const LayerArgs& a, int p, int k, bool ok) {
+// Term i of what is left of a block of 16 values: its codes, the scale, and in f what is left after it. The scale is
+// that of 8^i f.
+__device__ __forceinline__ uint2 split_term(float (&f)[16], int i, uint32_t* sf) {
+    const float up = float(1 << 3 * i);
+    float amax = 0.0f;
 #pragma unroll
-        for (int l = 0; l < (DOWN ? 4 : 2); l++) w[l] = 0;
-        if (!ok) return;
-        if constexpr (DOWN) {
-            const uint4 v = *reinterpret_cast<const uint4*>(h_values(a.f) + int64_t(p) * a.k + k);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.f.x + int64_t(p / a.f.K) * a.k + k));
-            w[0] = v.x, w[1] = v.y;
+    for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(f[j]));
+    *sf = e4m3x2(amax * (up / 6.0f), 0.0f) & 0xffu;
+    const float s = e4m3_value(*sf) * (1.0f / up);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s > 0.0f ? r : 0.0f;
+    uint32_t q[2];
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+        float* v = f + 8 * w;
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(q[w])
+            : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r), "f"(v[5] * r), "f"(v[6] * r),
+              "f"(v[7] * r));
+        uint32_t h[4];
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+            : "r"(q[w]));
+        // the product is exact, and the remainder as exact as fp32 gets
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[2 * j] = fmaf(-s, __half2float(__ushort_as_half(uint16_t(h[j]))), v[2 * j]);
+            v[2 * j + 1] = fmaf(-s, __half2float(__ushort_as_half(uint16_t(h[j] >> 16))), v[2 * j + 1]);
         }
     }
-    __device__ __forceinline__ void scaled(float scale, float (&f)[4]) const {
+    return make_uint2(q[0], q[1]);
+}
+
+// 16 neighbouring values of x (bf16) or h (fp32) as they are in memory.
+template <bool DOWN>
+struct Sixteen {
+    uint4 w[DOWN ? 4 : 2];
+
+    __device__ __forceinline__ void load(const LayerArgs& a, int p, int k, bool ok) {
+        const uint4* from = DOWN ? reinterpret_cast<const uint4*>(h_values(a.f) + int64_t(p) * a.k + k)
+                                 : reinterpret_cast<const uint4*>(a.f.x + int64_t(p / a.f.K) * a.k + k);
+#pragma unroll
+        for (int l = 0; l < (DOWN ? 4 : 2); l++) {
+            w[l] = make_uint4(0, 0, 0, 0);
+            if (ok) w[l] = DOWN ? from[l] : __ldg(from + l);
+        }
+    }
+    __device__ __forceinline__ void scaled(float scale, float (&f)[16]) const {
         if constexpr (DOWN) {
 #pragma unroll
-            for (int l = 0; l < 4; l++) f[l] = __uint_as_float(w[l]) * scale;
+            for (int l = 0; l < 4; l++) {
+                f[4 * l] = __uint_as_float(w[l].x), f[4 * l + 1] = __uint_as_float(w[l].y);
+                f[4 * l + 2] = __uint_as_float(w[l].z), f[4 * l + 3] = __uint_as_float(w[l].w);
+            }
         } else {
-            f[0] = bf16_lo(w[0]) * scale, f[1] = bf16_hi(w[0]) * scale;
-            f[2] = bf16_lo(w[1]) * scale, f[3] = bf16_hi(w[1]) * scale;
+            unpack8(w[0], f);
+            unpack8(w[1], f + 8);
         }
+#pragma unroll
+        for (int l = 0; l < 16; l++) f[l] *= scale;
     }
 };
 
@@ -415,21 +436,17 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         const uint16_t* list = r.list + t.first;
-        // NVFP4: four lanes a block, eight of a slot's sixteen blocks a warp, one pair after the other; the values of
-        // four pairs, and of the next slot's first four, are on their way (the task's first ones while the largest
-        // are looked for)
-        const int block = half * 8 + lane / 4, in = block * 16 + lane % 4 * 4;
-        Four<DOWN> now[4], then[4];
-        auto load = [&](Four<DOWN>& v4, int c, int j) {
-            const int k = c * S::kChunk + in;
+        // NVFP4: a lane a block, a warp the sixteen blocks of two pairs, the slot's two warps every other two; the values
+        // of the next pairs, or of the next slot's first, are on their way (the task's first ones while the largest are
+        // looked for)
+        const int block = lane % 16, pair = half * 2 + lane / 16;
+        Sixteen<DOWN> now;
+        auto load = [&](int c, int j) {
+            const int k = c * S::kChunk + block * 16;
             const bool ok = c < work.c1 && j < t.n && k < a.k;
-            v4.load(a, list[ok ? j : 0], k, ok);
+            now.load(a, list[ok ? j : 0], k, ok);
         };
-        if (NVFP4) {
-            const int first = work.c0 + (turn + turns - seq % turns) % turns;
-#pragma unroll
-            for (int j = 0; j < 4; j++) load(now[j], first, j);
-        }
+        if (NVFP4) load(work.c0 + (turn + turns - seq % turns) % turns, pair);
         if (NVFP4 && DOWN && i == 0) {  // of every pair of the list, a thread a pair
             const int parts = h_parts(a.k);
             for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
@@ -479,46 +496,35 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                 bool free = false;  // the slot: the first values are ready before it is waited for
                 if (NVFP4) {
                     const uint32_t sf_to = to + S::kB + S::kSfA;
-#pragma unroll
-                    for (int j = 0; j < 4; j++) load(then[j], c + turns, j);
 #pragma unroll 1
-                    for (int j = 0; j < t.n; j += 2) {
-                        float f[2][4];
+                    for (int j0 = 0; j0 < t.n; j0 += 4) {
+                        const int j = j0 + pair, at = min(j, t.n - 1);
+                        float f[16];
+                        now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
+                                   f);
+                        load(j0 + 4 < t.n ? c : c + turns, j0 + 4 < t.n ? j + 4 : pair);
+                        if (j0 + half * 2 >= t.n) continue;
+                        uint2 q[kTerms];
+                        uint32_t sf[kTerms];
 #pragma unroll
-                        for (int l = 0; l < 2; l++) {
-                            const int at = min(j + l, t.n - 1);
-                            now[l].scaled(
-                                pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))), f[l]);
-                            now[l] = now[l + 2];
-                            if (j + l + 4 < t.n) load(now[l + 2], c, j + l + 4);
-                        }
-                        uint32_t q[2][kTerms], sf[2][kTerms];
-#pragma unroll
-                        for (int l = 0; l < kTerms; l++)
-#pragma unroll
-                            for (int b = 0; b < 2; b++) q[b][l] = split_term(f[b], &sf[b][l]);
+                        for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l]);
                         if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
                         free = true;
+                        if (j >= t.n) continue;
+                        const int row0 = S::column(j);
 #pragma unroll
-                        for (int b = 0; b < 2; b++) {
-                            if (j + b == t.n) break;
-#pragma unroll
-                            for (int l = 0; l < kTerms; l++) {
-                                const int row = S::column(j + b) + l;
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + swizzled(row, block >> 1) + (block & 1) * 8 +
-                                                                             lane % 4 * 2),
-                                             "h"(uint16_t(q[b][l]))
-                                             : "memory");
-                                if (lane % 4 == 0)
-                                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
-                                                                                row / 32 * 4 + (block & 3)),
-                                                 "r"(sf[b][l])
-                                                 : "memory");
-                            }
+                        for (int l = 0; l < kTerms; l++) {
+                            const int row = row0 + l;
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + swizzled(row, block >> 1) +
+                                                                                  (block & 1) * 8),
+                                         "r"(q[l].x), "r"(q[l].y)
+                                         : "memory");
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
+                                                                        row / 32 * 4 + (block & 3)),
+                                         "r"(sf[l])
+                                         : "memory");
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; j++) now[j] = then[j];
                 } else {
                     const int parts = DOWN ? 2 : 1;
                     for (int u0 = half * 128; u0 < t.n * parts * 8; u0 += 256) {  // pieces of 8 values: row u / 8, piece u % 8

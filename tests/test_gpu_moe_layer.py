@@ -179,7 +179,8 @@ def test_layer_object_chooses_by_tokens_and_agrees_with_bf16():
     m = moe()
     E, I, H, K, T = 6, 256, 512, 3, 200
     w13, w2 = _experts(E, I, H, 1)
-    layer = m.MoELayer(m.quantize_experts(w13, w2), K, T, input_scale=2688.0 / 6.0, inter_scale=2688.0 / 12.0)
+    layer = m.MoELayer(m.quantize_experts(w13, w2), K, T, input_scale=2688.0 / 6.0, inter_scale=2688.0 / 12.0,
+                       few_tokens=64)
     gen = torch.Generator(device="cuda").manual_seed(2)
     x = torch.randn(T, H, device="cuda", generator=gen).bfloat16()
     ids = torch.rand(T, E, device="cuda", generator=gen).argsort(1)[:, :K].int().contiguous()
@@ -205,6 +206,7 @@ def test_layer_object_in_a_graph():
     E, I, H, K = 4, 128, 256, 2
     w13, w2 = _experts(E, I, H, 3)
     layer = m.MoELayer(m.quantize_experts(w13, w2), K, 96, input_scale=400.0, inter_scale=200.0)
+    assert layer.few == 4 * E // K
     for T in (5, 96):
         x = torch.randn(T, H, device="cuda").bfloat16()
         ids = torch.randint(0, E, (T, K), dtype=torch.int32, device="cuda")
