@@ -26,6 +26,9 @@ CASES = [  # mode, counts, M, align, n, k, scales
     ("normal", [130, 0, 5, 300, 77], 0, 128, 640, 1024, "swizzled"),
     ("normal", [256, 512, 128], 0, 128, 512, 2112, "row"),
     ("normal", [2] * 150 + [0] * 40 + [9] * 10, 0, 8, 80, 128, "swizzled"),
+    ("normal", [1, 0, 2] * 341 + [3], 0, 1, 16, 64, "row"),             # 1024 experts, the most there can be
+    ("masked", [257, 130], 260, 1, 272, 4160, "row"),                   # many slots, scales not whole 16-byte pieces
+    ("masked", [257, 130], 260, 1, 272, 4096, "row"),                   # the same with whole ones
 ]
 IDS = ["-".join(map(str, (c[0], len(c[1]), max(c[1]), c[4], c[5], c[6], c[3]))) for c in CASES]
 
@@ -79,6 +82,33 @@ def test_product_on_another_stream():
     s = torch.cuda.Stream()
     a, wv, al, out = _product(case, stream=s)
     _check_product(case[1], a, wv, al, out)
+
+
+def test_products_on_two_streams_at_once():
+    """Calls that share nothing may overlap: each result is that of the call alone."""
+    m = moe()
+    jobs = []
+    for i, case in enumerate([("masked", [200, 3, 140], 256, 1, 512, 1024, "swizzled"),
+                              ("normal", [90, 300], 0, 1, 768, 512, "row")]):
+        mode, counts, M, align, n, k, scales = case
+        rng = np.random.default_rng(i)
+        a = Activations(rng, mode, counts, M, align, k, scales)
+        wq, ws, wv, inv = weights(rng, len(counts), n, k)
+        args = (dev(a.codes), dev(a.scales), dev(np.array(counts, np.int32)), dev(wq), dev(ws))
+        outs = [filled((a.rows, n), torch.bfloat16) for _ in range(6)]
+        jobs.append((mode, args, outs, dict(seg_indptr=dev(a.seg), max_tokens_per_expert=M, scale_layout=scales),
+                     torch.cuda.Stream(), a, wv, counts))
+    status = m.new_status()
+    torch.cuda.synchronize()
+    for r in range(6):
+        for mode, args, outs, kw, stream, *_ in jobs:
+            m.moe_expert_gemm(mode, *args, outs[r], status, stream=stream, **kw)
+    torch.cuda.synchronize()
+    m.check_status(status)
+    for *_, outs, kw, stream, a, wv, counts in jobs:
+        _check_product(counts, a, wv, np.ones(len(counts)), outs[0])
+        for o in outs[1:]:
+            assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
 
 
 def test_counts_beyond_the_layout_are_cut_and_reported():

@@ -23,6 +23,11 @@ CASES = [  # T, H, I, E, K, weights, invalid rate, duplicates
     (64, 192, 448, 2, 2, "nvfp4", 0.05, False),
     (64, 256, 64, 300, 16, "bf16", 0.3, False),
     (64, 128, 128, 3, 16, "nvfp4", 0, True),
+    (64, 64, 64, 1024, 16, "nvfp4", 0.02, False),       # the most experts and slots
+    (1, 2112, 192, 2, 2, "nvfp4", 0, False),            # a row shared out over a cluster of eight
+    (2, 1040, 144, 3, 2, "bf16", 0, False),
+    (40, 8256, 64, 5, 1, "nvfp4", 0, False),            # several rounds of the ring, groups of 12 pairs
+    (64, 4112, 48, 1, 1, "bf16", 0, False),             # an expert with 64 tokens
 ]
 
 
@@ -125,6 +130,28 @@ def test_gates_far_from_zero():
     want = g / (1 + torch.exp(-g))
     got = out[0, :n].double().cpu()
     assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-31).all(), got.tolist()
+
+
+def test_layers_on_two_streams_at_once():
+    layers = [Layer(9, 576, 320, 12, 6, "nvfp4", 0.1, False), Layer(30, 272, 336, 5, 4, "bf16", 0.1, True, seed=1)]
+    alone = [layer.run().view(torch.int16).clone() for layer in layers]
+    m = moe()
+    runs, status = [], m.new_status()
+    for layer in layers:
+        T, H = layer.x.shape
+        E, I, K = layer.w13.shape[0], layer.w13.shape[1] // 2, layer.ids.shape[1]
+        x = torch.from_numpy(layer.x.view(np.int16)).cuda().view(torch.bfloat16)
+        runs.append((x, dev(layer.ids), dev(layer.w), layer, m.new_layer_workspace(T, K, H, I, E), torch.cuda.Stream(),
+                     [torch.empty_like(x) for _ in range(8)]))
+    torch.cuda.synchronize()
+    for r in range(8):
+        for x, ids, w, layer, ws, stream, outs in runs:
+            m.moe_layer_few_tokens(x, ids, w, layer.w13, layer.w2, outs[r], ws, status, stream=stream, **layer.kw)
+    torch.cuda.synchronize()
+    m.check_status(status)
+    for (*_, outs), want in zip(runs, alone):
+        for o in outs:
+            assert torch.equal(o.view(torch.int16), want)
 
 
 def test_bad_ids_are_skipped_and_reported():
