@@ -11,9 +11,9 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (MOE_ERR_UNSUPPORTED, MOE_MODE_MASKED, MOE_QUANT_NONE, MOE_QUANT_NVFP4_B16, MOE_SCALES_SWIZZLED_128X4, MODES,
-               SCALE_LAYOUTS, MoEError, _check, _need, _ptr, _stream, check_status, load_library, moe_combine_ex,
-               moe_dispatch_ex, moe_route_meta_ex, new_status, new_workspace)
+from . import (MOE_ERR_UNSUPPORTED, MOE_MODE_MASKED, MOE_QUANT_NONE, MOE_QUANT_NVFP4_B16, MOE_SCALES_ROW_MAJOR,
+               MOE_SCALES_SWIZZLED_128X4, MODES, SCALE_LAYOUTS, MoEError, _check, _need, _ptr, _stream, check_status,
+               load_library, moe_combine_ex, moe_dispatch_ex, moe_route_meta_ex, new_status, new_workspace)
 
 __all__ = [
     "MOE_LAYER_MAX_TOKENS", "NVFP4Rows", "ExpertWeights", "MoELayer", "moe_quantize_nvfp4", "moe_dequantize_nvfp4",
@@ -214,26 +214,36 @@ class NVFP4Rows(NamedTuple):
 def quantize_nvfp4(x: torch.Tensor, global_scales: torch.Tensor, scale_layout: str = "swizzled",
                    stream=None) -> NVFP4Rows:
     """Quantise x [groups, rows, hidden], or one matrix [rows, hidden], with one global scale per group."""
-    if x.dim() == 2:
+    shape = x.shape
+    if len(shape) == 2:
         q = quantize_nvfp4(x.unsqueeze(0), global_scales, scale_layout, stream)
         return NVFP4Rows(q.codes[0], q.scales[0], scale_layout)
-    G, R, H = x.shape
-    byte, dev = torch.uint8, x.device
-    codes = torch.empty((G, R, H // 2), dtype=byte, device=dev)
-    tail = (G, R, H // 16) if scale_layout == "row" else (G, nvfp4_scale_bytes(R, H, scale_layout))
-    scales = torch.empty(tail, dtype=byte, device=dev)
-    moe_quantize_nvfp4(x, global_scales, codes, scales, scale_layout, stream)
+    G, R, H = shape
+    layout = _layout(scale_layout)
+    px, pg = _pointers((x, 0, "x", torch.bfloat16), (global_scales, 4 * G, "global_scales", torch.float32))
+    dev = x.device
+    codes = torch.empty((G, R, H // 2), dtype=torch.uint8, device=dev)
+    tail = (R, H // 16) if layout == MOE_SCALES_ROW_MAJOR else ((R + 127) // 128 * 128 * (H // 16),)
+    scales = torch.empty((G, *tail), dtype=torch.uint8, device=dev)
+    st = load_library().moe_quantize_nvfp4(px, G, R, H, pg, layout, codes.data_ptr(), scales.data_ptr(), _on(stream))
+    _check(st, "moe_quantize_nvfp4")
     return NVFP4Rows(codes, scales, scale_layout)
 
 
 def dequantize_nvfp4(q: NVFP4Rows, global_scales: torch.Tensor, stream=None) -> torch.Tensor:
     """The bf16 values that q stands for."""
     codes, scales, scale_layout = q
-    if codes.dim() == 2:
+    shape = codes.shape
+    if len(shape) == 2:
         return dequantize_nvfp4(NVFP4Rows(codes.unsqueeze(0), scales, scale_layout), global_scales, stream)[0]
-    G, R, C = codes.shape
+    G, R, C = shape
+    layout = _layout(scale_layout)
+    pc, ps, pg = _pointers((codes, 0, "codes", torch.uint8),
+                           (scales, G * nvfp4_scale_bytes(R, 2 * C, scale_layout), "scales", torch.uint8),
+                           (global_scales, 4 * G, "global_scales", torch.float32))
     out = torch.empty((G, R, 2 * C), dtype=torch.bfloat16, device=codes.device)
-    moe_dequantize_nvfp4(codes, scales, global_scales, out, scale_layout, stream)
+    st = load_library().moe_dequantize_nvfp4(pc, ps, G, R, 2 * C, pg, layout, out.data_ptr(), _on(stream))
+    _check(st, "moe_dequantize_nvfp4")
     return out
 
 
