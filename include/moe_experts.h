@@ -124,10 +124,13 @@ size_t moe_layer_workspace_size(int64_t num_tokens, int topk, int hidden, int in
  * moe_layer_few_tokens -- the layer's experts and their weighted sum, straight from token rows:
  *   h(t, e) = silu(alpha13[e] * W13[e][:inter] x_t) * (alpha13[e] * W13[e][inter:] x_t)
  *   out[t]  = bf16_rn( sum_{k valid} topk_weights[t, k] * alpha2[e] * (W2[e] h(t, e)) ),  e = topk_ids[t, k]
- * Weights only are quantised (NVFP4 or bf16); activations stay bf16 and h keeps 16 bits of
- * mantissa (the chain of moe_expert_gemm_swiglu and moe_expert_gemm quantises both). fp32 sums in an order that
- * depends on the arguments alone. A token without a valid slot gets zeros; a slot that names an
+ * Weights are NVFP4 or bf16; activations are not quantised (the chain of moe_expert_gemm_swiglu and
+ * moe_expert_gemm quantises x and h to NVFP4). With bf16 weights x enters as it is and h as the sum
+ * of two bf16 values. With NVFP4 weights each block of 16 of x and of h enters as the sum of five
+ * NVFP4 blocks, which leaves at most 2^-12 of the block's largest magnitude, typically 2^-18. fp32
+ * sums in an order that depends on the arguments alone. A token without a valid slot gets zeros; a slot that names an
  * expert twice counts twice. Ids outside [-1, E) are skipped and reported as MOE_ERR_BAD_EXPERT_ID.
+ * A token with infinities or NaNs gets unspecified values and leaves the other tokens' as they are.
  * Arguments:
  *   x                [T, hidden] bf16, 16-byte aligned; 0 <= T <= MOE_LAYER_MAX_TOKENS.
  *   topk_ids, topk_weights  [T, K] int32 / fp32, 1 <= K <= MOE_MAX_TOPK.

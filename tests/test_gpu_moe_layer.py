@@ -110,6 +110,19 @@ def test_same_bits_every_time():
         assert torch.equal(layer.run(torch.cuda.Stream()).view(torch.int16), first)
 
 
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+def test_a_token_that_is_not_finite_leaves_the_others_alone(kind):
+    layer = Layer(9, 320, 192, 4, 2, kind, 0, False)
+    want = layer.run().view(torch.int16)
+    layer.x = layer.x.copy()
+    layer.x[3, 5], layer.x[3, 100], layer.x[3, 319] = 0x7fc0, 0x7f80, 0xff80      # NaN, infinity, -infinity
+    layer.x[7] = 0x7fff
+    got = layer.run().view(torch.int16)
+    assert int(layer.status.item()) == 0
+    finite = [t for t in range(9) if t not in (3, 7)]
+    assert torch.equal(got[finite], want[finite])
+
+
 def test_gates_far_from_zero():
     """silu of gates from -3e38 to 3e38, by one-element dot products: x W13 = (gate, 1), W2 picks h."""
     m = moe()
