@@ -16,8 +16,8 @@
 //
 // Why so, and what it measured (one GB300; 6782 GB/s is the copy bandwidth):
 //   256 experts, k 7168 -> 1024 -> 7168 (SwiGLU and the product after it), weights of 3.1 GB
-//     128 tokens top-8, masked:   466 us, 6.7 TB/s: bound by reading the weights once
-//     8192 tokens top-8:          840 us, 5.2 TB/s and 2.9 TFLOP at 3.4 PFLOP/s
+//     128 tokens top-8, masked:   461 us, 6.8 TB/s: bound by reading the weights once
+//     8192 tokens top-8:          840 to 875 us, 5.1 TB/s and 2.9 TFLOP at 3.4 PFLOP/s, at the power limit
 //   128 experts, k 768 -> 4096, 2048 tokens top-8 skewed: 67 us, 5.5 TB/s
 //   16 experts, k 4096 -> 704 -> 4096, 1501 tokens top-4: 46 us
 // With many rows an expert the bound is what an SM takes in from L2: a tile brings 128 + 256 rows of codes for 128 x 256
@@ -112,7 +112,8 @@ __device__ __forceinline__ bool warp_wait_or_die(const GemmArgs& a, Shared* s, u
 
 template <bool SWIGLU>
 __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t slots, bool sf_bulk,
-                                          const CUtensorMap* map_a, const CUtensorMap* map_w) {
+                                          const CUtensorMap* map_a, const CUtensorMap* map_a32,
+                                          const CUtensorMap* map_w) {
     const int k64 = a.g.k / 64;
     const int np128 = (a.g.n + 127) / 128;  // 128-row blocks of a weight matrix
     int st = 0;
@@ -126,8 +127,14 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t
             const int q = min(4, k64 - 4 * c);  // 64-value steps of this slot
             const int nb = tile.n0 / 128;
             const bool second = SWIGLU || nb + 1 < np128;
-            mbar_expect_tx(bar, kBytesA + kBytesB + q * 512 * ((sf_bulk ? 1 : 0) + (second ? 2 : 1)));
-            tma_load_2d(slot, map_a, c * 128, tile.row0, bar);
+            // Of a tile with up to 32 rows only 32 are read: in a masked layout what follows an expert's rows costs
+            // DRAM bandwidth (256 experts, 4 rows each: 475 us with 128 rows, 461 us with 32). Boxes for 64 and 96 rows
+            // gained nothing (prefill 861 -> 873 us). The slot's other rows keep what they hold: their results
+            // are not looked at.
+            const bool few = tile.rows <= kTileM / 4;
+            mbar_expect_tx(bar, (few ? kBytesA / 4 : kBytesA) + kBytesB +
+                                    q * 512 * ((sf_bulk ? 1 : 0) + (second ? 2 : 1)));
+            tma_load_2d(slot, few ? map_a32 : map_a, c * 128, tile.row0, bar);
             // SwiGLU: dimensions (k, column, half, expert), 128 columns of both halves; else (k, column, 1, expert)
             tma_load_4d(slot + kBytesA, map_w, c * 128, tile.n0, 0, tile.e, bar);
             if (sf_bulk)
@@ -329,7 +336,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, Shared* s, int 
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_w) {
+                       const __grid_constant__ CUtensorMap map_a32, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
 
     if (warp == 0) {
-        if (lane == 0) load_role<SWIGLU>(a, s, slots, sf_bulk, &map_a, &map_w);
+        if (lane == 0) load_role<SWIGLU>(a, s, slots, sf_bulk, &map_a, &map_a32, &map_w);
     } else if (warp == 1) {
         mma_role<SWIGLU>(a, s, slots);
     } else if (warp < 4) {
@@ -406,10 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool SWIGLU>
 cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
     const uint64_t kb = uint64_t(g.k) / 2;
-    CUtensorMap map_a, map_w;
+    CUtensorMap map_a, map_a32, map_w;
     const uint64_t da[2] = {kb, uint64_t(g.rows)}, dw[4] = {kb, uint64_t(g.n), SWIGLU ? 2u : 1u, uint64_t(g.E)};
-    const uint32_t ba[2] = {128, kTileM}, bw[4] = {128, SWIGLU ? kTileN / 2 : kTileN, SWIGLU ? 2u : 1u, 1};
-    if (!make_map(&map_a, g.a, 2, da, ba) || !make_map(&map_w, g.w, 4, dw, bw)) return cudaErrorInvalidValue;
+    const uint32_t ba[2] = {128, kTileM}, ba32[2] = {128, kTileM / 4},
+                   bw[4] = {128, SWIGLU ? kTileN / 2 : kTileN, SWIGLU ? 2u : 1u, 1};
+    if (!make_map(&map_a, g.a, 2, da, ba) || !make_map(&map_a32, g.a, 2, da, ba32) || !make_map(&map_w, g.w, 4, dw, bw))
+        return cudaErrorInvalidValue;
     const int cols = SWIGLU ? kTileN / 2 : kTileN;
     const GemmArgs a{g, (g.k + kChunk - 1) / kChunk, (g.n + cols - 1) / cols,
                      g.scale_layout == MOE_SCALES_SWIZZLED_128X4 && reinterpret_cast<uintptr_t>(g.a_sf) % 16 == 0,
@@ -418,7 +427,7 @@ cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
     auto kern = expert_gemm_kernel<SWIGLU>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (err != cudaSuccess) return err;
-    return launch_pdl(ctx, kern, dim3(unsigned(ctx.num_sms)), dim3(kThreads), smem, a, map_a, map_w);
+    return launch_pdl(ctx, kern, dim3(unsigned(ctx.num_sms)), dim3(kThreads), smem, a, map_a, map_a32, map_w);
 }
 
 }  // namespace
