@@ -4,8 +4,8 @@ Needs a GB300 and the built library (python -m combine_moe_route_meta_gb300.buil
 
     python examples/moe_layer_nvfp4.py [--tokens 1,32,512,4096] [--experts 64] [--hidden 4096] [--inter 1024] [--topk 8]
 
-Batches of up to MOE_LAYER_MAX_TOKENS tokens go through moe_layer_few_tokens; larger ones through route metadata,
-NVFP4 dispatch, gate/up product with SwiGLU, down product and combine. Each is timed and compared with the layer's bf16
+Batches of up to four pairs an expert (and MOE_LAYER_MAX_TOKENS tokens) go through moe_layer_few_tokens; larger ones
+through route metadata, NVFP4 dispatch, gate/up product with SwiGLU, down product and combine. Each is timed and compared with the layer's bf16
 weights in 32-bit arithmetic.
 """
 import argparse
