@@ -68,6 +68,13 @@ def _on(stream):
     return _stream(stream)
 
 
+def _current(stream):
+    """A context with `stream` (a torch stream or a raw handle) current, so that what is allocated in it is its own."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return torch.cuda.stream(stream)
+
+
 # ---------------------------------------------------------------------------
 # thin wrappers with the C names
 # ---------------------------------------------------------------------------
@@ -213,10 +220,14 @@ class NVFP4Rows(NamedTuple):
 
 def quantize_nvfp4(x: torch.Tensor, global_scales: torch.Tensor, scale_layout: str = "swizzled",
                    stream=None) -> NVFP4Rows:
-    """Quantise x [groups, rows, hidden], or one matrix [rows, hidden], with one global scale per group."""
+    """Quantise x [groups, rows, hidden], or one matrix [rows, hidden], with one global scale per group. The result is
+    allocated on `stream`."""
+    if stream is not None:
+        with _current(stream):
+            return quantize_nvfp4(x, global_scales, scale_layout)
     shape = x.shape
     if len(shape) == 2:
-        q = quantize_nvfp4(x.unsqueeze(0), global_scales, scale_layout, stream)
+        q = quantize_nvfp4(x.unsqueeze(0), global_scales, scale_layout)
         return NVFP4Rows(q.codes[0], q.scales[0], scale_layout)
     G, R, H = shape
     layout = _layout(scale_layout)
@@ -225,24 +236,27 @@ def quantize_nvfp4(x: torch.Tensor, global_scales: torch.Tensor, scale_layout: s
     codes = torch.empty((G, R, H // 2), dtype=torch.uint8, device=dev)
     tail = (R, H // 16) if layout == MOE_SCALES_ROW_MAJOR else ((R + 127) // 128 * 128 * (H // 16),)
     scales = torch.empty((G, *tail), dtype=torch.uint8, device=dev)
-    st = load_library().moe_quantize_nvfp4(px, G, R, H, pg, layout, codes.data_ptr(), scales.data_ptr(), _on(stream))
+    st = load_library().moe_quantize_nvfp4(px, G, R, H, pg, layout, codes.data_ptr(), scales.data_ptr(), _on(None))
     _check(st, "moe_quantize_nvfp4")
     return NVFP4Rows(codes, scales, scale_layout)
 
 
 def dequantize_nvfp4(q: NVFP4Rows, global_scales: torch.Tensor, stream=None) -> torch.Tensor:
-    """The bf16 values that q stands for."""
+    """The bf16 values that q stands for, allocated on `stream`."""
+    if stream is not None:
+        with _current(stream):
+            return dequantize_nvfp4(q, global_scales)
     codes, scales, scale_layout = q
     shape = codes.shape
     if len(shape) == 2:
-        return dequantize_nvfp4(NVFP4Rows(codes.unsqueeze(0), scales, scale_layout), global_scales, stream)[0]
+        return dequantize_nvfp4(NVFP4Rows(codes.unsqueeze(0), scales, scale_layout), global_scales)[0]
     G, R, C = shape
     layout = _layout(scale_layout)
     pc, ps, pg = _pointers((codes, 0, "codes", torch.uint8),
                            (scales, G * nvfp4_scale_bytes(R, 2 * C, scale_layout), "scales", torch.uint8),
                            (global_scales, 4 * G, "global_scales", torch.float32))
     out = torch.empty((G, R, 2 * C), dtype=torch.bfloat16, device=codes.device)
-    st = load_library().moe_dequantize_nvfp4(pc, ps, G, R, 2 * C, pg, layout, out.data_ptr(), _on(stream))
+    st = load_library().moe_dequantize_nvfp4(pc, ps, G, R, 2 * C, pg, layout, out.data_ptr(), _on(None))
     _check(st, "moe_dequantize_nvfp4")
     return out
 

@@ -153,3 +153,26 @@ def test_one_matrix():
     one, group = m.quantize_nvfp4(x, g), m.quantize_nvfp4(x[None], g)
     assert one.codes.shape == (5, 64) and torch.equal(one.codes, group.codes[0]) and torch.equal(one.scales, group.scales[0])
     assert torch.equal(m.dequantize_nvfp4(one, g), m.dequantize_nvfp4(group, g)[0])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_belong_to_the_stream_that_writes_them(raw):
+    """Memory that the current stream still works on is not handed to a call on another one."""
+    m = moe()
+    g = torch.ones(1, device="cuda")
+    x = torch.ones(256, 4096, device="cuda", dtype=torch.bfloat16)
+    want = m.quantize_nvfp4(x, g)
+    back = m.dequantize_nvfp4(want, g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(10 ** 7)
+    held = [torch.zeros_like(want.codes), torch.zeros_like(want.scales), torch.zeros_like(back)]
+    at = [t.data_ptr() for t in held]
+    for t in held:
+        t.fill_(7)
+    del held, t                          # free again for the current stream, and not yet written by it
+    q = m.quantize_nvfp4(x, g, stream=side.cuda_stream if raw else side)
+    y = m.dequantize_nvfp4(q, g, stream=side.cuda_stream if raw else side)
+    assert not {q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr()} & set(at)
+    torch.cuda.synchronize()
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales) and torch.equal(y, back)
