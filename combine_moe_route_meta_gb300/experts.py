@@ -350,6 +350,9 @@ class MoELayer:
         T, w = x.shape[0], self.weights
         if T > self.T:
             raise ValueError(f"{T} tokens: the layer was made for {self.T}")
+        if x.shape != (T, self.H) or topk_ids.shape != (T, self.K) or topk_weights.shape != (T, self.K):
+            raise ValueError(f"x, topk_ids, topk_weights: [T, {self.H}], [T, {self.K}] and [T, {self.K}] expected, got "
+                             f"{tuple(x.shape)}, {tuple(topk_ids.shape)} and {tuple(topk_weights.shape)}")
         out = self.out[:T]
         if T <= self.few:
             moe_layer_few_tokens(x, topk_ids, topk_weights, w.w13, w.w2, out, self.few_workspace, self.status,

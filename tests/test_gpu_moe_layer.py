@@ -274,6 +274,23 @@ def test_layer_object_refuses():
         layer(torch.zeros(5, 128, dtype=torch.bfloat16, device="cuda"), None, None)
 
 
+@pytest.mark.parametrize("T", [2, 64])          # both ways
+def test_layer_object_refuses_other_shapes(T):
+    m = moe()
+    w = m.quantize_experts(*(torch.randn(4, *s, device="cuda").bfloat16() for s in ((128, 128), (128, 64))))
+    layer = m.MoELayer(w, 2, 64, input_scale=100.0, inter_scale=100.0)
+    x = torch.zeros(T, 128, device="cuda", dtype=torch.bfloat16)
+    ids = torch.zeros(T, 2, device="cuda", dtype=torch.int32)
+    g = torch.zeros(T, 2, device="cuda")
+    layer(x, ids, g)
+    for bad in ((x[:, :64].contiguous(), ids, g), (x, ids[:, :1].contiguous(), g), (x, ids, g[:-1]),
+                (x, ids[:-1], g), (torch.cat([x, x], 1), ids, g), (x, ids, torch.cat([g, g], 1))):
+        with pytest.raises(ValueError):
+            layer(*bad)
+    torch.cuda.synchronize()
+    layer.check()
+
+
 def test_example_runs():
     import os
     import subprocess
