@@ -18,8 +18,8 @@
 // Both kernels list the routed experts and their pairs (route()) and then work in roles:
 //   warps 0..3   turn accumulators into h, or into the sums of out
 //   warp 4       issues the weight loads of a ring of slots, each 128 bytes of 256 weight rows
-//   warp 5       issues the products
-//   warps 6..13  bring a slot's columns of x or h to shared memory, two warps a slot
+//   warps 5, 6   issue the products, one tile of 128 rows each
+//   warps 7..14  bring a slot's columns of x or h to shared memory, two warps a slot
 // gate_up walks persistently over (pairs of an expert, 128 gate rows and their up rows); where that leaves more than
 // half of the SMs without work, a cluster of blocks shares out the length of a row. In down a cluster owns 256 rows
 // of out and shares out the experts; each block adds up its experts in order. A cluster adds up its blocks in order.
@@ -54,7 +54,7 @@ namespace {
 // A pair of converters takes every kTurns'th slot, or every `stages`th where there are fewer: a slot that it waits
 // for is then at most one round of the ring ahead of the last one it filled, so that the parity that it waits
 // for can only stand for the right phase.
-constexpr int kLoadWarp = 4, kMmaWarp = 5, kConvertWarp = 6, kTurns = 4, kConvertWarps = 2 * kTurns;
+constexpr int kLoadWarp = 4, kMmaWarp = 5, kConvertWarp = 7, kTurns = 4, kConvertWarps = 2 * kTurns;
 constexpr int kThreads = (kConvertWarp + kConvertWarps) * 32;
 constexpr int kRows = 256;                    // weight rows of a slot: two tiles of 128
 constexpr int kColumns = 64;                  // columns of a group of pairs
@@ -63,8 +63,8 @@ constexpr int kMaxStages = 5;
 constexpr int kKept = 32;                      // tasks whose columns' largest magnitudes are kept
 constexpr int kMaxRanks = 8;
 constexpr uint32_t kTmemScales = 4 * kColumns;  // after two accumulators of two tiles
-constexpr uint32_t kTmemScaleSet = 48;          // two tiles' and the columns' scales of a slot, 16 each
-static_assert(kTmemScales + kMaxStages * kTmemScaleSet <= 512, "tensor memory");
+constexpr uint32_t kTmemScaleSet = 64;          // of a slot, for each tile: its scales and the columns', 16 each
+constexpr int max_stages(bool nvfp4) { return nvfp4 ? int((512 - kTmemScales) / kTmemScaleSet) : kMaxStages; }
 
 template <bool NVFP4, bool DOWN>
 struct Shape {
@@ -269,42 +269,35 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     }
 }
 
-// The products of a slot, 32 bytes of a row each: 64 NVFP4 or 16 bf16 values.
+// The products of a slot's tile `t`, 32 bytes of a row each: 64 NVFP4 or 16 bf16 values.
 template <bool NVFP4, bool DOWN>
-__device__ __forceinline__ void multiply_slot(uint32_t slot, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool second,
-                                              bool add) {
+__device__ __forceinline__ void multiply_slot(uint32_t slot, int t, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool add) {
     using S = Shape<NVFP4, DOWN>;
-    const uint64_t a0 = desc_k128(slot), a1 = desc_k128(slot + S::kA / 2), b = desc_k128(slot + S::kA);
+    const uint64_t da = desc_k128(slot + t * (S::kA / 2)), db = desc_k128(slot + S::kA);
     if (NVFP4) {
         const uint32_t sf = slot + S::kA + S::kB;
-        const uint64_t s0 = desc_scales(sf), s1 = desc_scales(sf + S::kSfA / 2), sb = desc_scales(sf + S::kSfA);
+        const uint64_t sa = desc_scales(sf + t * (S::kSfA / 2)), sb = desc_scales(sf + S::kSfA);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             if (j >= q) break;
-            tc_copy_scales(ts + j * 4, s0 + j * 32);
-            tc_copy_scales(ts + 16 + j * 4, s1 + j * 32);
-            tc_copy_scales(ts + 32 + j * 4, sb + j * 32);
+            tc_copy_scales(ts + j * 4, sa + j * 32);
+            tc_copy_scales(ts + 16 + j * 4, sb + j * 32);
         }
     }
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-        if (t == 1 && !second) break;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (j >= q) break;
-            if (NVFP4)
-                tc_mma_nvfp4(d + t * kColumns, (t ? a1 : a0) + 2 * j, b + 2 * j, idesc, ts + t * 16 + j * 4,
-                             ts + 32 + j * 4, add || j > 0);
-            else
-                tc_mma_bf16(d + t * kColumns, (t ? a1 : a0) + 2 * j, b + 2 * j, idesc, add || j > 0);
-        }
+    for (int j = 0; j < 4; j++) {
+        if (j >= q) break;
+        if (NVFP4)
+            tc_mma_nvfp4(d, da + 2 * j, db + 2 * j, idesc, ts + j * 4, ts + 16 + j * 4, add || j > 0);
+        else
+            tc_mma_bf16(d, da + 2 * j, db + 2 * j, idesc, add || j > 0);
     }
 }
 
-// A whole warp; one lane issues.
+// A whole warp, for tile `half` of every slot; one lane issues.
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
-                                         uint32_t slots) {
+                                         uint32_t slots, int half) {
     using S = Shape<NVFP4, DOWN>;
     const int tasks = work.tasks();
     const bool leader = elect_one();
@@ -314,9 +307,9 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         const int buf = i & 1, n = S::columns(t.n);
-        const uint32_t d = tmem + buf * 2 * kColumns;
+        const uint32_t d = tmem + (buf * 2 + half) * kColumns;
         const uint32_t idesc = NVFP4 ? idesc_nvfp4(n) : idesc_bf16(n);
-        const bool second = !DOWN || t.block + 1 < a.blocks;
+        const bool there = !DOWN || t.block + half < a.blocks;
         if (!warp_wait_or_die(a, s, &s->acc_empty[buf], (i >> 1 & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = work.c0; c < work.c1; c++) {
@@ -324,8 +317,9 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
             tc_fence_after();
             const int q = min(4, (a.row_bytes - c * 128) / 32);
             if (leader) {
-                multiply_slot<NVFP4, DOWN>(slots + st * S::kSlot, d, tmem + kTmemScales + st * kTmemScaleSet, idesc, q,
-                                           second, c > work.c0);
+                if (there)
+                    multiply_slot<NVFP4, DOWN>(slots + st * S::kSlot, half, d,
+                                               tmem + kTmemScales + st * kTmemScaleSet + half * 32, idesc, q, c > work.c0);
                 tc_commit(smem_addr(&s->empty[st]));
                 if (c + 1 == work.c1) tc_commit(smem_addr(&s->acc_full[buf]));
             }
@@ -671,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         s->dead = 0;
         for (int i = 0; i < a.stages; i++) {
             mbar_init(smem_addr(&s->full[i]), 3);  // the loads' issuer and two converters
-            mbar_init(smem_addr(&s->empty[i]), 1);
+            mbar_init(smem_addr(&s->empty[i]), 2);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(smem_addr(&s->acc_full[i]), 1);
+            mbar_init(smem_addr(&s->acc_full[i]), 2);
             mbar_init(smem_addr(&s->acc_empty[i]), 4);
         }
         mbar_init(smem_addr(&s->shifts_ready), 2 * min(kTurns, a.stages));
@@ -711,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  shifts);
     else if (warp == kLoadWarp) {
         if (lane == 0) load_role<NVFP4, DOWN>(a, s, r, work, slots, &map);
-    } else if (warp == kMmaWarp) {
-        mma_role<NVFP4, DOWN>(a, s, r, work, slots);
+    } else if (warp < kConvertWarp) {
+        mma_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kMmaWarp);
     } else {
         if (DOWN) pdl_wait();
         convert_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kConvertWarp, shifts);
@@ -815,7 +809,7 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     else if (ranks > 1) a.summed = task_pairs;
     const size_t fixed =
         1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + pairs;
-    a.stages = int(std::min<size_t>(kMaxStages, (kMost - sizeof(Shared) - fixed) / S::kSlot));
+    a.stages = int(std::min<size_t>(max_stages(NVFP4), (kMost - sizeof(Shared) - fixed) / S::kSlot));
 
     auto kern = few_tokens_kernel<NVFP4, DOWN>;
     cudaLaunchConfig_t cfg = {};
