@@ -98,15 +98,15 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, Shared* s, int t) {
 }
 
 // Bounded wait; false (and the CTA marked dead) when it gave up or another role already had.
-__device__ __forceinline__ bool wait_or_die(const GemmArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(smem_addr(bar), parity)) return true;
+__device__ __forceinline__ bool wait_or_die(const GemmArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
+    if (mbar_wait(bar, parity)) return true;
     *const_cast<volatile int*>(&s->dead) = 1;
     set_status(a.g.status, MOE_ERR_TIMEOUT);
     return false;
 }
 
 // The same for a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait_or_die(const GemmArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool warp_wait_or_die(const GemmArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
     return __all_sync(kFullMask, wait_or_die(a, s, bar, parity));
 }
 
@@ -121,7 +121,7 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x) {
         const Tile tile = find_tile<SWIGLU>(a, s, t);
         for (int c = 0; c < a.chunks; c++) {
-            if (!wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+            if (!wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
             const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * kSlot;
             const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
             const int q = min(4, k64 - 4 * c);  // 64-value steps of this slot
@@ -149,46 +149,55 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, Shared* s, uint32_t
     }
 }
 
+// What the products read in the first slot; a slot further, kSlot / 16 more.
+struct Operands {
+    uint64_t a, b, sfa, sfb0, sfb1;
+};
+
 // The products of a slot: q steps of 64 values, their scales first.
-__device__ __forceinline__ void multiply_slot(uint32_t slot, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool add) {
-    const uint32_t sfa = slot + kBytesA + kBytesB, sfb = sfa + kBytesSfA;
-    const uint64_t da = desc_k128(slot), db = desc_k128(slot + kBytesA);
-    const uint64_t sa = desc_scales(sfa), s0 = desc_scales(sfb), s1 = desc_scales(sfb + kBytesSfB / 2);
+__device__ __forceinline__ void multiply_slot(const Operands& o, uint32_t off, uint32_t d, uint32_t ts, uint32_t idesc, int q,
+                                              bool add) {
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         if (j >= q) break;
-        tc_copy_scales(ts + j * 4, sa + j * 32);
-        tc_copy_scales(ts + 16 + j * 8, s0 + j * 32);
-        tc_copy_scales(ts + 16 + j * 8 + 4, s1 + j * 32);
+        tc_copy_scales(ts + j * 4, o.sfa + off + j * 32);
+        tc_copy_scales(ts + 16 + j * 8, o.sfb0 + off + j * 32);
+        tc_copy_scales(ts + 16 + j * 8 + 4, o.sfb1 + off + j * 32);
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         if (j >= q) break;
         // 64 codes: 32 bytes further in the rows, 2 in the descriptor's units
-        tc_mma_nvfp4(d, da + 2 * j, db + 2 * j, idesc, ts + j * 4, ts + 16 + j * 8, add || j > 0);
+        tc_mma_nvfp4(d, o.a + off + 2 * j, o.b + off + 2 * j, idesc, ts + j * 4, ts + 16 + j * 8, add || j > 0);
     }
 }
 
 // A whole warp; one lane issues.
 template <bool SWIGLU>
 __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t slots) {
-    const int k64 = a.g.k / 64;
-    const uint32_t tmem = s->tmem;
+    const uint32_t tmem = s->tmem, sf = slots + kBytesA + kBytesB;
+    const Operands o{desc_k128(slots), desc_k128(slots + kBytesA), desc_scales(sf), desc_scales(sf + kBytesSfA),
+                     desc_scales(sf + kBytesSfA + kBytesSfB / 2)};
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const int q_last = a.g.k / 64 - 4 * (a.chunks - 1);
     const bool leader = elect_one();
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x; t < s->tiles; t += gridDim.x, n_tile++) {
         const Tile tile = find_tile<SWIGLU>(a, s, t);
         const uint32_t idesc = idesc_nvfp4(SWIGLU ? kTileN : min(kTileN, a.g.n - tile.n0));
-        if (!warp_wait_or_die(a, s, &s->acc_empty, (n_tile & 1) ^ 1)) return;
+        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_empty), (n_tile & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = 0; c < a.chunks; c++) {
-            if (!warp_wait_or_die(a, s, &s->full[st], ph)) return;
+            if (!warp_wait_or_die(a, s, full + 8 * st, ph)) return;
             tc_fence_after();
             if (leader) {
-                multiply_slot(slots + st * kSlot, tmem, tmem + kTmemScales + st * kTmemScaleSet, idesc,
-                              min(4, k64 - 4 * c), c > 0);
-                tc_commit(smem_addr(&s->empty[st]));
+                const uint32_t off = st * (kSlot / 16), ts = tmem + kTmemScales + st * kTmemScaleSet;
+                if (c + 1 < a.chunks || q_last == 4)
+                    multiply_slot(o, off, tmem, ts, idesc, 4, c > 0);
+                else
+                    multiply_slot(o, off, tmem, ts, idesc, q_last, c > 0);
+                tc_commit(empty + 8 * st);
                 if (c + 1 == a.chunks) tc_commit(smem_addr(&s->acc_full));
             }
             __syncwarp();
@@ -196,7 +205,7 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, Shared* s, uint32_t 
         }
     }
     // the last slot's arrival is the last that is on its way to this CTA's memory
-    if (n_tile > 0) warp_wait_or_die(a, s, &s->empty[st == 0 ? kStages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
+    if (n_tile > 0) warp_wait_or_die(a, s, empty + 8 * (st == 0 ? kStages - 1 : st - 1), st == 0 ? ph ^ 1 : ph);
 }
 
 // Row scales that are not whole tiles of the layout: a warp brings every second slot's, a lane those of four rows
@@ -248,7 +257,7 @@ __device__ __forceinline__ void scale_role(const GemmArgs& a, Shared* s, uint32_
             }
         }
         if (first) continue;
-        if (!warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+        if (!warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
         const uint32_t to = slots + st * kSlot + kBytesA + kBytesB + lane * 16;
 #pragma unroll
         for (int w = 0; w < 4; w++)
@@ -297,7 +306,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, Shared* s, int 
         const int m = quad * 32 + lane;
         const bool valid = m < tile.rows;
         const int64_t r = int64_t(tile.row0) + m;
-        if (!warp_wait_or_die(a, s, &s->acc_full, n_tile & 1)) return;
+        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_full), n_tile & 1)) return;
         tc_fence_after();
         // the warp's half of the tile to registers at once, so that the next tile's products can begin: 128
         // columns, with SwiGLU 64 gate columns and their up columns

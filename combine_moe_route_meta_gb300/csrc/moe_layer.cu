@@ -199,13 +199,13 @@ struct Shared {
     int largest[kKept][kColumns / 16 * 3];
 };
 
-__device__ __forceinline__ bool wait_or_die(const LayerArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(smem_addr(bar), parity)) return true;
+__device__ __forceinline__ bool wait_or_die(const LayerArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
+    if (mbar_wait(bar, parity)) return true;
     *const_cast<volatile int*>(&s->dead) = 1;
     set_status(a.f.status, MOE_ERR_TIMEOUT);
     return false;
 }
-__device__ __forceinline__ bool warp_wait_or_die(const LayerArgs& a, Shared* s, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool warp_wait_or_die(const LayerArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
     return __all_sync(kFullMask, wait_or_die(a, s, bar, parity));
 }
 
@@ -249,7 +249,7 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
         for (int c = work.c0; c < work.c1; c++) {
-            if (!wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+            if (!wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
             const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * S::kSlot;
             const bool second = !DOWN || t.block + 1 < a.blocks;
             const int q = NVFP4 ? min(4, k64 - 4 * c) : 0;
@@ -269,39 +269,47 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     }
 }
 
-// The products of a slot's tile `t`, 32 bytes of a row each: 64 NVFP4 or 16 bf16 values.
-template <bool NVFP4, bool DOWN>
-__device__ __forceinline__ void multiply_slot(uint32_t slot, int t, uint32_t d, uint32_t ts, uint32_t idesc, int q, bool add) {
-    using S = Shape<NVFP4, DOWN>;
-    const uint64_t da = desc_k128(slot + t * (S::kA / 2)), db = desc_k128(slot + S::kA);
+// What the products of a tile read in the first slot; a slot further, kSlot / 16 more.
+struct Operands {
+    uint64_t a, b, sfa, sfb;
+};
+
+// The products of a slot's tile, 32 bytes of a row each (64 NVFP4 or 16 bf16 values), `q` of them.
+template <bool NVFP4>
+__device__ __forceinline__ void multiply_slot(const Operands& o, uint32_t off, uint32_t d, uint32_t ts, uint32_t idesc, int q,
+                                              bool add) {
     if (NVFP4) {
-        const uint32_t sf = slot + S::kA + S::kB;
-        const uint64_t sa = desc_scales(sf + t * (S::kSfA / 2)), sb = desc_scales(sf + S::kSfA);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             if (j >= q) break;
-            tc_copy_scales(ts + j * 4, sa + j * 32);
-            tc_copy_scales(ts + 16 + j * 4, sb + j * 32);
+            tc_copy_scales(ts + j * 4, o.sfa + off + j * 32);
+            tc_copy_scales(ts + 16 + j * 4, o.sfb + off + j * 32);
         }
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         if (j >= q) break;
         if (NVFP4)
-            tc_mma_nvfp4(d, da + 2 * j, db + 2 * j, idesc, ts + j * 4, ts + 16 + j * 4, add || j > 0);
+            tc_mma_nvfp4(d, o.a + off + 2 * j, o.b + off + 2 * j, idesc, ts + j * 4, ts + 16 + j * 4, add || j > 0);
         else
-            tc_mma_bf16(d, da + 2 * j, db + 2 * j, idesc, add || j > 0);
+            tc_mma_bf16(d, o.a + off + 2 * j, o.b + off + 2 * j, idesc, add || j > 0);
     }
 }
 
-// A whole warp, for tile `half` of every slot; one lane issues.
+// A whole warp, for tile `half` of every slot; one lane issues. A slot costs the warp some hundred cycles beside its
+// products, so what does not change from slot to slot is made before.
 template <bool NVFP4, bool DOWN>
 __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
                                          uint32_t slots, int half) {
     using S = Shape<NVFP4, DOWN>;
     const int tasks = work.tasks();
     const bool leader = elect_one();
-    const uint32_t tmem = s->tmem;
+    const uint32_t sf = slots + S::kA + S::kB;
+    const Operands o{desc_k128(slots + half * (S::kA / 2)), desc_k128(slots + S::kA), desc_scales(sf + half * (S::kSfA / 2)),
+                     desc_scales(sf + S::kSfA)};
+    const uint32_t tmem = s->tmem, scales = tmem + kTmemScales + half * 32;
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const int q_last = (a.row_bytes - (a.chunks - 1) * 128) / 32;
     int st = 0;
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
@@ -310,17 +318,20 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
         const uint32_t d = tmem + (buf * 2 + half) * kColumns;
         const uint32_t idesc = NVFP4 ? idesc_nvfp4(n) : idesc_bf16(n);
         const bool there = !DOWN || t.block + half < a.blocks;
-        if (!warp_wait_or_die(a, s, &s->acc_empty[buf], (i >> 1 & 1) ^ 1)) return;
+        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_empty[buf]), (i >> 1 & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = work.c0; c < work.c1; c++) {
-            if (!warp_wait_or_die(a, s, &s->full[st], ph)) return;
+            if (!warp_wait_or_die(a, s, full + 8 * st, ph)) return;
             tc_fence_after();
-            const int q = min(4, (a.row_bytes - c * 128) / 32);
             if (leader) {
-                if (there)
-                    multiply_slot<NVFP4, DOWN>(slots + st * S::kSlot, half, d,
-                                               tmem + kTmemScales + st * kTmemScaleSet + half * 32, idesc, q, c > work.c0);
-                tc_commit(smem_addr(&s->empty[st]));
+                const uint32_t off = st * (S::kSlot / 16), ts = scales + st * kTmemScaleSet;
+                if (there) {
+                    if (c + 1 < a.chunks || q_last == 4)
+                        multiply_slot<NVFP4>(o, off, d, ts, idesc, 4, c > work.c0);
+                    else
+                        multiply_slot<NVFP4>(o, off, d, ts, idesc, q_last, c > work.c0);
+                }
+                tc_commit(empty + 8 * st);
                 if (c + 1 == work.c1) tc_commit(smem_addr(&s->acc_full[buf]));
             }
             __syncwarp();
@@ -328,7 +339,7 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
         }
     }
     // the last slot's arrival is the last that is on its way to this block's memory
-    if (tasks > 0) warp_wait_or_die(a, s, &s->empty[st == 0 ? a.stages - 1 : st - 1], st == 0 ? ph ^ 1 : ph);
+    if (tasks > 0) warp_wait_or_die(a, s, empty + 8 * (st == 0 ? a.stages - 1 : st - 1), st == 0 ? ph ^ 1 : ph);
 }
 
 // 2^e as fp32, e in [-126, 127]
@@ -466,7 +477,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
-            if (!warp_wait_or_die(a, s, &s->shifts_ready, 0)) return;
+            if (!warp_wait_or_die(a, s, smem_addr(&s->shifts_ready), 0)) return;
         }
         if (NVFP4 && !DOWN) {
             int* largest = s->largest[i % kKept];
@@ -493,7 +504,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             if (v == 0 && lane < kColumns / 16 * 3) s->largest[(i + kKept / 2) % kKept][lane] = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
-            if (!warp_wait_or_die(a, s, &s->shifts_ready, i & 1)) return;
+            if (!warp_wait_or_die(a, s, smem_addr(&s->shifts_ready), i & 1)) return;
         }
         for (int c = work.c0; c < work.c1; c++, seq++) {
             if (seq % turns == turn) {
@@ -513,7 +524,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                         uint32_t sf[kTerms];
 #pragma unroll
                         for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l]);
-                        if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+                        if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
                         free = true;
                         if (j >= t.n) continue;
                         const int row0 = S::column(j);
@@ -546,7 +557,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                                 w[l] = *reinterpret_cast<const uint4*>(from + k);
                             }
                         }
-                        if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+                        if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
                         free = true;
 #pragma unroll
                         for (int l = 0; l < 4; l++) {
@@ -558,7 +569,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                         }
                     }
                 }
-                if (!free && !warp_wait_or_die(a, s, &s->empty[st], ph ^ 1)) return;
+                if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&s->full[st]));
@@ -607,7 +618,7 @@ __device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const
         const int buf = i & 1;
         const float* alphas = DOWN ? a.f.alpha2 : a.f.alpha13;
         const float alpha = alphas ? __ldg(alphas + t.e) : 1.0f;
-        if (!warp_wait_or_die(a, s, &s->acc_full[buf], i >> 1 & 1)) return;
+        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_full[buf]), i >> 1 & 1)) return;
         tc_fence_after();
         for (int j0 = 0, c = 0; j0 < t.n; j0 += kPairs, c += 16) {
             float v0[16], v1[16];
