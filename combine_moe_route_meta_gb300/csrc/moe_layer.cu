@@ -369,9 +369,15 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return row * 
 // that of 8^i f.
 __device__ __forceinline__ uint2 split_term(float (&f)[16], int i, uint32_t* sf) {
     const float up = float(1 << 3 * i);
-    float amax = 0.0f;
+    float m[8];  // by halves: a chain of 16 is in the way of the next term
 #pragma unroll
-    for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(f[j]));
+    for (int j = 0; j < 8; j++) m[j] = fmaxf(fabsf(f[j]), fabsf(f[j + 8]));
+#pragma unroll
+    for (int h = 4; h; h /= 2)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < h) m[j] = fmaxf(m[j], m[j + h]);
+    const float amax = m[0];
     *sf = e4m3x2(amax * (up / 6.0f), 0.0f) & 0xffu;
     const float s = e4m3_value(*sf) * (1.0f / up);
     float r;
@@ -447,7 +453,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
     const int lane = threadIdx.x & 31, tasks = work.tasks();
     const int turns = min(kTurns, a.stages), turn = v / 2, half = v % 2;
     if (turn >= turns) return;
-    int seq = 0, st = 0;  // slots so far, over all tasks; their place in the ring
+    int skip = turn, st = turn;  // slots of the next task before this warp's first one; its place in the ring
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
@@ -462,7 +468,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             const bool ok = c < work.c1 && j < t.n && k < a.k;
             now.load(a, list[ok ? j : 0], k, ok);
         };
-        if (NVFP4) load(work.c0 + (turn + turns - seq % turns) % turns, pair);
+        if (NVFP4) load(work.c0 + skip, pair);
         if (NVFP4 && DOWN && i == 0) {  // of every pair of the list, a thread a pair
             const int parts = h_parts(a.k);
             for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
@@ -506,76 +512,77 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
             if (!warp_wait_or_die(a, s, smem_addr(&s->shifts_ready), i & 1)) return;
         }
-        for (int c = work.c0; c < work.c1; c++, seq++) {
-            if (seq % turns == turn) {
-                const uint32_t to = slots + st * S::kSlot + S::kA;
-                bool free = false;  // the slot: the first values are ready before it is waited for
-                if (NVFP4) {
-                    const uint32_t sf_to = to + S::kB + S::kSfA;
+        int c = work.c0 + skip;
+        for (; c < work.c1; c += turns) {
+            const uint32_t to = slots + st * S::kSlot + S::kA;
+            bool free = false;  // the slot: the first values are ready before it is waited for
+            if (NVFP4) {
+                const uint32_t sf_to = to + S::kB + S::kSfA;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < t.n; j0 += 4) {
-                        const int j = j0 + pair, at = min(j, t.n - 1);
-                        float f[16];
-                        now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
-                                   f);
-                        load(j0 + 4 < t.n ? c : c + turns, j0 + 4 < t.n ? j + 4 : pair);
-                        if (j0 + half * 2 >= t.n) continue;
-                        uint2 q[kTerms];
-                        uint32_t sf[kTerms];
+                for (int j0 = 0; j0 < t.n; j0 += 4) {
+                    const int j = j0 + pair, at = min(j, t.n - 1);
+                    float f[16];
+                    now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
+                               f);
+                    load(j0 + 4 < t.n ? c : c + turns, j0 + 4 < t.n ? j + 4 : pair);
+                    if (j0 + half * 2 >= t.n) continue;
+                    uint2 q[kTerms];
+                    uint32_t sf[kTerms];
 #pragma unroll
-                        for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l]);
-                        if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
-                        free = true;
-                        if (j >= t.n) continue;
-                        const int row0 = S::column(j);
+                    for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l]);
+                    if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
+                    free = true;
+                    if (j >= t.n) continue;
+                    const int row0 = S::column(j);
 #pragma unroll
-                        for (int l = 0; l < kTerms; l++) {
-                            const int row = row0 + l;
-                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + swizzled(row, block >> 1) +
-                                                                                  (block & 1) * 8),
-                                         "r"(q[l].x), "r"(q[l].y)
-                                         : "memory");
-                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
-                                                                        row / 32 * 4 + (block & 3)),
-                                         "r"(sf[l])
-                                         : "memory");
-                        }
-                    }
-                } else {
-                    const int parts = DOWN ? 2 : 1;
-                    for (int u0 = half * 128; u0 < t.n * parts * 8; u0 += 256) {  // pieces of 8 values: row u / 8, piece u % 8
-                        uint4 w[4];
-#pragma unroll
-                        for (int l = 0; l < 4; l++) {
-                            const int u = u0 + l * 32 + lane, row = u / 8, k = c * S::kChunk + u % 8 * 8;
-                            w[l] = make_uint4(0, 0, 0, 0);
-                            if (row < t.n * parts && k < a.k) {
-                                const int p = list[row / parts];
-                                const uint16_t* from =
-                                    DOWN ? static_cast<const uint16_t*>(a.f.workspace) + (int64_t(p) * 2 + row % 2) * a.k
-                                         : a.f.x + int64_t(p / a.f.K) * a.k;
-                                w[l] = *reinterpret_cast<const uint4*>(from + k);
-                            }
-                        }
-                        if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
-                        free = true;
-#pragma unroll
-                        for (int l = 0; l < 4; l++) {
-                            const int u = u0 + l * 32 + lane, row = u / 8;
-                            if (row < t.n * parts)
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + swizzled(row, u % 8)),
-                                             "r"(w[l].x), "r"(w[l].y), "r"(w[l].z), "r"(w[l].w)
-                                             : "memory");
-                        }
+                    for (int l = 0; l < kTerms; l++) {
+                        const int row = row0 + l;
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + swizzled(row, block >> 1) +
+                                                                              (block & 1) * 8),
+                                     "r"(q[l].x), "r"(q[l].y)
+                                     : "memory");
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
+                                                                    row / 32 * 4 + (block & 3)),
+                                     "r"(sf[l])
+                                     : "memory");
                     }
                 }
-                if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s->full[st]));
+            } else {
+                const int parts = DOWN ? 2 : 1;
+                for (int u0 = half * 128; u0 < t.n * parts * 8; u0 += 256) {  // pieces of 8 values: row u / 8, piece u % 8
+                    uint4 w[4];
+#pragma unroll
+                    for (int l = 0; l < 4; l++) {
+                        const int u = u0 + l * 32 + lane, row = u / 8, k = c * S::kChunk + u % 8 * 8;
+                        w[l] = make_uint4(0, 0, 0, 0);
+                        if (row < t.n * parts && k < a.k) {
+                            const int p = list[row / parts];
+                            const uint16_t* from =
+                                DOWN ? static_cast<const uint16_t*>(a.f.workspace) + (int64_t(p) * 2 + row % 2) * a.k
+                                     : a.f.x + int64_t(p / a.f.K) * a.k;
+                            w[l] = *reinterpret_cast<const uint4*>(from + k);
+                        }
+                    }
+                    if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
+                    free = true;
+#pragma unroll
+                    for (int l = 0; l < 4; l++) {
+                        const int u = u0 + l * 32 + lane, row = u / 8;
+                        if (row < t.n * parts)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + swizzled(row, u % 8)),
+                                         "r"(w[l].x), "r"(w[l].y), "r"(w[l].z), "r"(w[l].w)
+                                         : "memory");
+                    }
+                }
             }
-            if (++st == a.stages) st = 0, ph ^= 1;
+            if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&s->full[st]));
+            st += turns;
+            if (st >= a.stages) st -= a.stages, ph ^= 1;
         }
+        skip = c - work.c1;
     }
 }
 
