@@ -365,28 +365,55 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 values_of(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+    return p;
+}
+
 // Term i of what is left of a block of 16 values: its codes, the scale, and in f what is left after it. The scale is
 // that of 8^i f.
-__device__ __forceinline__ uint2 split_term(float (&f)[16], int i, uint32_t* sf) {
+__device__ __forceinline__ uint2 split_term(uint64_t (&f)[8], int i, uint32_t* sf) {
     const float up = float(1 << 3 * i);
     float m[8];  // by halves: a chain of 16 is in the way of the next term
 #pragma unroll
-    for (int j = 0; j < 8; j++) m[j] = fmaxf(fabsf(f[j]), fabsf(f[j + 8]));
+    for (int j = 0; j < 8; j++) {
+        const float2 v = values_of(f[j]);
+        m[j] = fmaxf(fabsf(v.x), fabsf(v.y));
+    }
 #pragma unroll
     for (int h = 4; h; h /= 2)
 #pragma unroll
         for (int j = 0; j < 4; j++)
             if (j < h) m[j] = fmaxf(m[j], m[j + h]);
-    const float amax = m[0];
-    *sf = e4m3x2(amax * (up / 6.0f), 0.0f) & 0xffu;
+    *sf = e4m3x2(m[0] * (up / 6.0f), 0.0f) & 0xffu;
     const float s = e4m3_value(*sf) * (1.0f / up);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r = s > 0.0f ? r : 0.0f;
+    const uint64_t r2 = pair_of(r, r), s2 = pair_of(-s, -s);
     uint32_t q[2];
 #pragma unroll
     for (int w = 0; w < 2; w++) {
-        float* v = f + 8 * w;
+        uint64_t* v = f + 4 * w;
+        const float2 y0 = values_of(mul2(v[0], r2)), y1 = values_of(mul2(v[1], r2)), y2 = values_of(mul2(v[2], r2)),
+                     y3 = values_of(mul2(v[3], r2));
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
@@ -394,8 +421,8 @@ __device__ __forceinline__ uint2 split_term(float (&f)[16], int i, uint32_t* sf)
             "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
             "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
             : "=r"(q[w])
-            : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r), "f"(v[5] * r), "f"(v[6] * r),
-              "f"(v[7] * r));
+            : "f"(y0.x), "f"(y0.y), "f"(y1.x), "f"(y1.y), "f"(y2.x), "f"(y2.y), "f"(y3.x), "f"(y3.y));
+        if (i + 1 == kTerms) continue;  // nothing looks at what is left
         uint32_t h[4];
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -407,10 +434,9 @@ __device__ __forceinline__ uint2 split_term(float (&f)[16], int i, uint32_t* sf)
             : "r"(q[w]));
         // the product is exact, and the remainder as exact as fp32 gets
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            v[2 * j] = fmaf(-s, __half2float(__ushort_as_half(uint16_t(h[j]))), v[2 * j]);
-            v[2 * j + 1] = fmaf(-s, __half2float(__ushort_as_half(uint16_t(h[j] >> 16))), v[2 * j + 1]);
-        }
+        for (int j = 0; j < 4; j++)
+            v[j] = fma2(s2, pair_of(__half2float(__ushort_as_half(uint16_t(h[j]))),
+                                    __half2float(__ushort_as_half(uint16_t(h[j] >> 16)))), v[j]);
     }
     return make_uint2(q[0], q[1]);
 }
@@ -429,19 +455,20 @@ struct Sixteen {
             if (ok) w[l] = DOWN ? from[l] : __ldg(from + l);
         }
     }
-    __device__ __forceinline__ void scaled(float scale, float (&f)[16]) const {
+    __device__ __forceinline__ void scaled(float scale, uint64_t (&f)[8]) const {
+        float v[16];
         if constexpr (DOWN) {
 #pragma unroll
             for (int l = 0; l < 4; l++) {
-                f[4 * l] = __uint_as_float(w[l].x), f[4 * l + 1] = __uint_as_float(w[l].y);
-                f[4 * l + 2] = __uint_as_float(w[l].z), f[4 * l + 3] = __uint_as_float(w[l].w);
+                v[4 * l] = __uint_as_float(w[l].x), v[4 * l + 1] = __uint_as_float(w[l].y);
+                v[4 * l + 2] = __uint_as_float(w[l].z), v[4 * l + 3] = __uint_as_float(w[l].w);
             }
         } else {
-            unpack8(w[0], f);
-            unpack8(w[1], f + 8);
+            unpack8(w[0], v);
+            unpack8(w[1], v + 8);
         }
 #pragma unroll
-        for (int l = 0; l < 16; l++) f[l] *= scale;
+        for (int l = 0; l < 8; l++) f[l] = mul2(pair_of(v[2 * l], v[2 * l + 1]), pair_of(scale, scale));
     }
 };
 
@@ -521,7 +548,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
 #pragma unroll 1
                 for (int j0 = 0; j0 < t.n; j0 += 4) {
                     const int j = j0 + pair, at = min(j, t.n - 1);
-                    float f[16];
+                    uint64_t f[8];
                     now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
                                f);
                     load(j0 + 4 < t.n ? c : c + turns, j0 + 4 < t.n ? j + 4 : pair);
