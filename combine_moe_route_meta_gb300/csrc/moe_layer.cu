@@ -19,7 +19,7 @@
 //   warps 0..3   turn accumulators into h, or into the sums of out
 //   warp 4       issues the weight loads of a ring of slots, each 128 bytes of 256 weight rows
 //   warps 5, 6   issue the products, one tile of 128 rows each
-//   warps 7..14  bring a slot's columns of x or h to shared memory, two warps a slot
+//   warps 7..    bring a slot's columns of x or h to shared memory, two or three warps a slot
 // gate_up walks persistently over (pairs of an expert, 128 gate rows and their up rows); where that leaves more than
 // half of the SMs without work, a cluster of blocks shares out the length of a row. In down a cluster owns 256 rows
 // of out and shares out the experts; each block adds up its experts in order. A cluster adds up its blocks in order.
@@ -51,11 +51,12 @@ namespace cg = cooperative_groups;
 namespace moe {
 namespace {
 
-// A pair of converters takes every kTurns'th slot, or every `stages`th where there are fewer: a slot that it waits
+// A team of PER converters takes every kTurns'th slot, or every `stages`th where there are fewer: a slot that it waits
 // for is then at most one round of the ring ahead of the last one it filled, so that the parity that it waits
 // for can only stand for the right phase.
-constexpr int kLoadWarp = 4, kMmaWarp = 5, kConvertWarp = 7, kTurns = 4, kConvertWarps = 2 * kTurns;
-constexpr int kThreads = (kConvertWarp + kConvertWarps) * 32;
+constexpr int kLoadWarp = 4, kMmaWarp = 5, kConvertWarp = 7, kTurns = 4;
+template <int PER>
+constexpr int kThreadsOf = (kConvertWarp + kTurns * PER) * 32;
 constexpr int kRows = 256;                    // weight rows of a slot: two tiles of 128
 constexpr int kColumns = 64;                  // columns of a group of pairs
 constexpr int kTerms = 5;                     // columns of a pair, NVFP4
@@ -113,6 +114,7 @@ __host__ __device__ __forceinline__ size_t routing_bytes(int pairs) {
 // once by warps (match), the experts' prefix sums by threads. `scratch`: E bytes for each chunk, 4 for each pair, 2
 // for each expert (less than a ring of slots), 16-byte aligned, free again afterwards. `report`: write bad ids to the
 // status word.
+template <int kThreads>
 __device__ __forceinline__ Routing route(const FewTokens& a, uint8_t* smem, uint8_t* scratch, int group, bool report) {
     __shared__ int warp_sum[kThreads / 32], n_groups;
     const int pairs = a.T * a.K, chunks = (pairs + 31) / 32, E = a.E;
@@ -473,12 +475,12 @@ struct Sixteen {
 };
 
 // Warp `v` of the converters: half the work of every `turns`th slot. down: `shifts` [pairs in the list].
-template <bool NVFP4, bool DOWN>
+template <bool NVFP4, bool DOWN, int PER>
 __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
                                              uint32_t slots, int v, int8_t* shifts) {
     using S = Shape<NVFP4, DOWN>;
     const int lane = threadIdx.x & 31, tasks = work.tasks();
-    const int turns = min(kTurns, a.stages), turn = v / 2, half = v % 2;
+    const int turns = min(kTurns, a.stages), turn = v / PER, part = v % PER;
     if (turn >= turns) return;
     int skip = turn, st = turn;  // slots of the next task before this warp's first one; its place in the ring
     uint32_t ph = 0;
@@ -488,7 +490,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
         // NVFP4: a lane a block, a warp the sixteen blocks of two pairs, the slot's two warps every other two; the values
         // of the next pairs, or of the next slot's first, are on their way (the task's first ones while the largest are
         // looked for)
-        const int block = lane % 16, pair = half * 2 + lane / 16;
+        const int block = lane % 16, pair = part * 2 + lane / 16;
         Sixteen<DOWN> now;
         auto load = [&](int c, int j) {
             const int k = c * S::kChunk + block * 16;
@@ -498,7 +500,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
         if (NVFP4) load(work.c0 + skip, pair);
         if (NVFP4 && DOWN && i == 0) {  // of every pair of the list, a thread a pair
             const int parts = h_parts(a.k);
-            for (int at = v * 32 + lane; at < r.first[r.groups]; at += 2 * turns * 32) {
+            for (int at = v * 32 + lane; at < r.first[r.groups]; at += PER * turns * 32) {
                 const float4* from = reinterpret_cast<const float4*>(h_largest(a.f) + int64_t(r.list[at]) * parts);
                 float m = 0.0f;
 #pragma unroll 8
@@ -518,11 +520,11 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             for (int j = 0; j < t.n; j++) {
                 const uint16_t* x = a.f.x + int64_t(list[j] / a.f.K) * a.k;
                 uint32_t m = 0;  // two bf16 magnitudes
-                for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * 2 * turns * 256) {
+                for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * PER * turns * 256) {
                     uint4 w[4];
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
-                        const int k = k0 + u * 2 * turns * 256;
+                        const int k = k0 + u * PER * turns * 256;
                         w[u] = k < a.k ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
@@ -546,13 +548,13 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             if (NVFP4) {
                 const uint32_t sf_to = to + S::kB + S::kSfA;
 #pragma unroll 1
-                for (int j0 = 0; j0 < t.n; j0 += 4) {
+                for (int j0 = 0; j0 < t.n; j0 += 2 * PER) {
                     const int j = j0 + pair, at = min(j, t.n - 1);
                     uint64_t f[8];
                     now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
                                f);
-                    load(j0 + 4 < t.n ? c : c + turns, j0 + 4 < t.n ? j + 4 : pair);
-                    if (j0 + half * 2 >= t.n) continue;
+                    load(j0 + 2 * PER < t.n ? c : c + turns, j0 + 2 * PER < t.n ? j + 2 * PER : pair);
+                    if (j0 + part * 2 >= t.n) continue;
                     uint2 q[kTerms];
                     uint32_t sf[kTerms];
 #pragma unroll
@@ -576,7 +578,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                 }
             } else {
                 const int parts = DOWN ? 2 : 1;
-                for (int u0 = half * 128; u0 < t.n * parts * 8; u0 += 256) {  // pieces of 8 values: row u / 8, piece u % 8
+                for (int u0 = part * 128; u0 < t.n * parts * 8; u0 += PER * 128) {  // pieces of 8 values: row u / 8, piece u % 8
                     uint4 w[4];
 #pragma unroll
                     for (int l = 0; l < 4; l++) {
@@ -689,10 +691,11 @@ __device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const
     }
 }
 
-template <bool NVFP4, bool DOWN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool NVFP4, bool DOWN, int PER>
+__global__ void __launch_bounds__(kThreadsOf<PER>, 1)
     few_tokens_kernel(const __grid_constant__ LayerArgs a, const __grid_constant__ CUtensorMap map) {
     using S = Shape<NVFP4, DOWN>;
+    constexpr int kThreads = kThreadsOf<PER>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared shared;
     Shared* s = &shared;
@@ -709,14 +712,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         s->dead = 0;
         for (int i = 0; i < a.stages; i++) {
-            mbar_init(smem_addr(&s->full[i]), 3);  // the loads' issuer and two converters
+            mbar_init(smem_addr(&s->full[i]), 1 + PER);  // the loads' issuer and the converters
             mbar_init(smem_addr(&s->empty[i]), 2);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&s->acc_full[i]), 2);
             mbar_init(smem_addr(&s->acc_empty[i]), 4);
         }
-        mbar_init(smem_addr(&s->shifts_ready), 2 * min(kTurns, a.stages));
+        mbar_init(smem_addr(&s->shifts_ready), PER * min(kTurns, a.stages));
         mbar_fence_init();
     }
     if (DOWN && warp < 4)
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 128;
         if (at < int64_t(a.f.T) * a.f.H * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + at));
     }
-    const Routing r = route(a.f, lists, base, S::kGroup, !DOWN && blockIdx.x == 0);
+    const Routing r = route<kThreads>(a.f, lists, base, S::kGroup, !DOWN && blockIdx.x == 0);
     const Work<DOWN> work(a, r, rank, ranks);
     fence_proxy_async();  // route()'s scratch is where the first loads land
     tc_fence_before();
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kMmaWarp);
     } else {
         if (DOWN) pdl_wait();
-        convert_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kConvertWarp, shifts);
+        convert_role<NVFP4, DOWN, PER>(a, s, r, work, slots, warp - kConvertWarp, shifts);
     }
     if (DOWN) pdl_wait();  // a block without work does not end before gate_up has either
     __syncwarp();
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Whether `owners` clusters of `ranks` blocks can be resident at once (GPCs hold whole clusters), cached per
 // device: it depends on the kernel, its shared memory and the device alone.
-template <typename Kernel>
+template <bool NVFP4, bool DOWN, int PER, typename Kernel>
 bool clusters_fit(const LaunchCtx& ctx, Kernel kern, cudaLaunchConfig_t cfg, int owners, int ranks) {
     constexpr int kDevices = 64;
     static std::mutex mu;
@@ -828,7 +831,7 @@ bool clusters_fit(const LaunchCtx& ctx, Kernel kern, cudaLaunchConfig_t cfg, int
     return owners <= most;
 }
 
-template <bool NVFP4, bool DOWN>
+template <bool NVFP4, bool DOWN, int PER>
 cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     using S = Shape<NVFP4, DOWN>;
     constexpr size_t kMost = 226 * 1024;  // dynamic shared memory beside the static part
@@ -856,9 +859,9 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
         1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + pairs;
     a.stages = int(std::min<size_t>(max_stages(NVFP4), (kMost - sizeof(Shared) - fixed) / S::kSlot));
 
-    auto kern = few_tokens_kernel<NVFP4, DOWN>;
+    auto kern = few_tokens_kernel<NVFP4, DOWN, PER>;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreadsOf<PER>);
     cfg.dynamicSmemBytes = fixed + size_t(a.stages) * S::kSlot;
     cfg.stream = ctx.stream;
     cudaError_t err =
@@ -873,7 +876,7 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     cfg.numAttrs = 1;
     for (;; ranks -= ranks > 2 ? 2 : 1) {
         attr[0].val.clusterDim.x = unsigned(ranks);
-        if (ranks == 1 || clusters_fit(ctx, kern, cfg, int(owners), ranks)) break;
+        if (ranks == 1 || clusters_fit<NVFP4, DOWN, PER>(ctx, kern, cfg, int(owners), ranks)) break;
     }
     cfg.gridDim = dim3(unsigned(owners * ranks));
     cfg.numAttrs = 2;
@@ -886,10 +889,18 @@ size_t few_tokens_workspace(int64_t T, int K, int, int I, int) {
     return size_t(T) * K * (size_t(I) + h_parts(I)) * sizeof(float);
 }
 
+template <bool NVFP4, int PER>
+static cudaError_t launch_layer(const LaunchCtx& ctx, const FewTokens& f) {
+    const cudaError_t err = launch_half<NVFP4, false, PER>(ctx, f);
+    return err != cudaSuccess ? err : launch_half<NVFP4, true, PER>(ctx, f);
+}
+
+// Three converters a slot from two pairs an expert on, two below and with bf16 weights, which are only copied: 64 experts
+// of 4096 x 1024, top-8, 64 tokens 122 us with three, 131 with two and 128 with four (which have fewer registers); 256
+// experts of 7168 x 1024, one token 27.5, 26.9 and 28.5 us (more warps start later), 32 tokens 296, 295 and 298 us.
 cudaError_t launch_few_tokens(const LaunchCtx& ctx, const FewTokens& f) {
-    cudaError_t err = f.nvfp4 ? launch_half<true, false>(ctx, f) : launch_half<false, false>(ctx, f);
-    if (err != cudaSuccess) return err;
-    return f.nvfp4 ? launch_half<true, true>(ctx, f) : launch_half<false, true>(ctx, f);
+    if (!f.nvfp4) return launch_layer<false, 2>(ctx, f);
+    return f.T * f.K > 2 * f.E ? launch_layer<true, 3>(ctx, f) : launch_layer<true, 2>(ctx, f);
 }
 
 }  // namespace moe
