@@ -27,14 +27,14 @@
 // not need, and loads weights until h is there. Every wait is bounded (MOE_ERR_TIMEOUT).
 //
 // Why so, and what it measured (both kernels, one GB300, weights from DRAM; 6782 GB/s is the copy bandwidth):
-//   256 experts of 7168 x 1024, top-8, NVFP4:    32 tokens 301 us (2.0 GB, 6.7 TB/s), 1 token 27.6 us (99 MB, 3.6 TB/s)
-//   128 experts of 4096 x 768, top-8, bf16:      5 tokens 105 us (0.67 GB, 6.3 TB/s)
-//   16 experts of 2112 x 704, top-3, bf16:       61 tokens 39 us (143 MB, 3.6 TB/s)
+//   256 experts of 7168 x 1024, top-8, NVFP4:    32 tokens 292 us (2.0 GB, 6.9 TB/s), 1 token 26.8 us (99 MB, 3.7 TB/s)
+//   128 experts of 4096 x 768, top-8, bf16:      5 tokens 103 us (0.67 GB, 6.5 TB/s)
+//   16 experts of 2112 x 704, top-3, bf16:       61 tokens 39 us (143 MB, 3.7 TB/s)
 // The tensor core takes weights as they are stored, so no instruction is spent on a weight: converting them in
 // registers for mma.sync was bound by those instructions (620 us for the 32 tokens). What is left is the terms of x and
-// h, whose work grows with the pairs of an expert: at four an expert, 64 of these experts and 32 tokens take 104 us,
-// as long as dispatch, products and combine; above that MoELayer takes those. The small cases are bound by latency:
-// two kernels' starts, the list of pairs, the first weights, h and the sums.
+// h, whose work grows with the pairs of an expert: at four an expert, 64 experts of 4096 x 1024, 32 tokens take 90 us,
+// at eight 122 us, the dispatch, products and combine 101 us; MoELayer changes over between them. The small
+// cases are bound by latency: two kernels' starts, the list of pairs, the first weights, h and the sums.
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
