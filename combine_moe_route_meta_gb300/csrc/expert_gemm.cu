@@ -20,11 +20,12 @@
 //     8192 tokens top-8:          840 to 875 us, 5.1 TB/s and 2.9 TFLOP at 3.4 PFLOP/s, at the power limit
 //   128 experts, k 768 -> 4096, 2048 tokens top-8 skewed: 67 us, 5.5 TB/s
 //   16 experts, k 4096 -> 704 -> 4096, 1501 tokens top-4: 46 us
-// With many rows an expert the bound is what an SM takes in from L2: a tile brings 128 + 256 rows of codes for 128 x 256
-// results, 15.6 TB/s over all SMs, while the tensor core is busy for 56 % and DRAM for 62 % of the time. Wider tiles
-// do not fit tensor memory beside the scales; pairs of SMs that share a weight tile were not built (an expert's rows
-// would be rounded up to 256). One lane elected from a converged warp issues the products: issued by a divergent lane
-// they cost 60 ns each, and the first case above took 608 us.
+// With many rows an expert the first product's bound is what an SM takes in from L2: a tile brings 128 + 256 rows of
+// codes for 128 x 256 results, 56 bytes a clock and SM between two tile ends, 15.1 TB/s over a whole launch, while the
+// tensor core is busy for 56 % and DRAM for 62 % of the time. Wider tiles do not fit tensor memory beside the scales;
+// pairs of SMs that share a weight tile were not built (an expert's rows would be rounded up to 256). The second
+// product, with its larger output, is bound by DRAM. One lane elected from a converged warp issues the products:
+// issued by a divergent lane they cost 60 ns each, and the first case above took 608 us.
 #include <cstdint>
 
 #include "expert_rows.cuh"
