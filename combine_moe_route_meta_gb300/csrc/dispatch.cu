@@ -531,7 +531,7 @@ BulkGeom bulk_geometry(int quant, const DispatchArgs& a, bool part) {
     g.in_off = part ? kBulkHeaderPart : kBulkHeader;
     g.out_off = g.in_off + uint32_t(stages) * g.in_bytes;
     const size_t smem = size_t(g.out_off) + (quant == MOE_QUANT_NONE ? 0 : 2 * (g.q_bytes + g.s_bytes)) + seg_bytes;
-    if (smem > 200 * 1024) return g;
+    if (smem > kMostSharedMemory) return g;
     g.stages = stages;
     return g;
 }
@@ -550,7 +550,7 @@ cudaError_t launch_bulk(const LaunchCtx& ctx, const DispatchArgs& a, const BulkG
     if constexpr (QUANT == MOE_QUANT_NONE) {
         auto kern = dispatch_bulk_copy_kernel<MASKED, PART>;
         threads = kBulkCopyThreads;
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        err = allow_shared_memory(kern, kMostSharedMemory);
         if (err == cudaSuccess) err = blocks_per_sm(ctx, kern, threads, smem, &per_sm);
         if (err != cudaSuccess) return err;
         const int grid = int(std::min<int64_t>(a.T, int64_t(ctx.num_sms) * (per_sm > 0 ? per_sm : 1)));
@@ -565,7 +565,7 @@ cudaError_t launch_bulk(const LaunchCtx& ctx, const DispatchArgs& a, const BulkG
         const int nslices = a.H / kLaneElems;
         const int passes = (nslices + kBulkQuantThreads - 1) / kBulkQuantThreads;
         threads = ((nslices + passes - 1) / passes + 31) / 32 * 32;
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        err = allow_shared_memory(kern, kMostSharedMemory);
         if (err == cudaSuccess) err = blocks_per_sm(ctx, kern, threads, smem, &per_sm);
         if (err != cudaSuccess) return err;
         const int grid = int(std::min<int64_t>(a.T, int64_t(ctx.num_sms) * (per_sm > 0 ? per_sm : 1)));

@@ -435,7 +435,7 @@ cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
                      reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
     const size_t smem = 1024 + size_t(kStages) * kSlot + shared_bytes(g.E);
     auto kern = expert_gemm_kernel<SWIGLU>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t err = allow_shared_memory(kern, 1024 + size_t(kStages) * kSlot + shared_bytes(MOE_MAX_EXPERTS));
     if (err != cudaSuccess) return err;
     return launch_pdl(ctx, kern, dim3(unsigned(ctx.num_sms)), dim3(kThreads), smem, a, map_a, map_a32, map_w);
 }

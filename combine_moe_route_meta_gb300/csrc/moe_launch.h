@@ -37,6 +37,15 @@ cudaError_t launch_pdl(const LaunchCtx& ctx, Kernel kern, dim3 grid, dim3 block,
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Lets `kern` be launched with up to `most` bytes of dynamic shared memory. The limit belongs to the kernel, not to a
+// launch: a call that set it to its own size could lower it between another thread's call and that thread's launch, which
+// would then be refused. So `most` is a constant of the kernel, the largest size that any call needs.
+template <typename Kernel>
+cudaError_t allow_shared_memory(Kernel kern, size_t most) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+}
+constexpr size_t kMostSharedMemory = 200 * 1024;  // of the dispatch, interleave and partitioned ring kernels
+
 // Resident blocks per SM of `kern` at (threads, smem), cached per device and kernel: the
 // answer depends only on the compiled kernel and the device, so it is queried once.
 // Kernels that cannot be resident at all report 0.

@@ -864,8 +864,7 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     cfg.blockDim = dim3(kThreadsOf<PER>);
     cfg.dynamicSmemBytes = fixed + size_t(a.stages) * S::kSlot;
     cfg.stream = ctx.stream;
-    cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(cfg.dynamicSmemBytes));
+    const cudaError_t err = allow_shared_memory(kern, kMost - sizeof(Shared));
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

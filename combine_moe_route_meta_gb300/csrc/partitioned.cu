@@ -643,6 +643,9 @@ constexpr int64_t kRingMinTokens = 1024;
 // down, four CTAs per SM, held there by 56 registers x 288 threads); four consumer warps instead
 // of eight 128.0-129.0; a single slot 147.4 us.
 constexpr size_t kRingTargetBytes = 28 * 1024;
+// two of the longest rows, or the target; and two mbarriers a slot
+constexpr size_t kRingMostBytes =
+    std::max<size_t>(kRingMinSlots * 16 * kRingMaxVecs * kRingConsumerWarps * 32, kRingTargetBytes) + 16 * kRingMaxSlots;
 
 // Partitions of the CTA's tokens i0 + lane (stride G from blockIdx.x), one token per lane, as bit
 // masks: every lane loads its token's K ids at once, so a warp pays one round trip for 32 tokens.
@@ -870,10 +873,9 @@ cudaError_t launch_dispatch_partitioned(const LaunchCtx& ctx, int quant, const u
     constexpr bool kDRing = true;
     if (kDRing && quant == MOE_QUANT_NVFP4_B16 && scale_layout == MOE_SCALES_ROW_MAJOR && !by_tiles && T >= 1024 &&
         H % 256 == 0 &&
-        (reinterpret_cast<uintptr_t>(recv_sf) & 15) == 0 && dring_smem(H) <= 200 * 1024) {
+        (reinterpret_cast<uintptr_t>(recv_sf) & 15) == 0 && dring_smem(H) <= kMostSharedMemory) {
         const size_t smem = dring_smem(H);
-        cudaError_t err = cudaFuncSetAttribute(dispatch_partitioned_ring_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t err = allow_shared_memory(dispatch_partitioned_ring_kernel, kMostSharedMemory);
         int per_sm = 0;
         if (err == cudaSuccess) err = blocks_per_sm(ctx, dispatch_partitioned_ring_kernel, kDRingThreads, smem, &per_sm);
         if (err != cudaSuccess) return err;
@@ -916,8 +918,7 @@ cudaError_t launch_combine_partitioned(const LaunchCtx& ctx, const uint16_t* par
     const int NS = int(std::max<size_t>(kRingMinSlots, std::min<size_t>(kRingMaxSlots, kRingTargetBytes / row_bytes)));
     if (T >= kRingMinTokens && H / 8 <= kRingMaxVecs * kRingConsumerWarps * 32) {
         const size_t smem = size_t(NS) * row_bytes + 16 * size_t(NS);
-        cudaError_t err =
-            cudaFuncSetAttribute(combine_partitioned_ring_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t err = allow_shared_memory(combine_partitioned_ring_kernel, kRingMostBytes);
         int per_sm = 0;
         if (err == cudaSuccess) err = blocks_per_sm(ctx, combine_partitioned_ring_kernel, kRingThreads, smem, &per_sm);
         if (err != cudaSuccess) return err;

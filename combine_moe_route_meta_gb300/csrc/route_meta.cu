@@ -405,7 +405,7 @@ cudaError_t launch_single(const LaunchCtx& ctx, const RouteArgs& a, int E) {
     const size_t smem = route_smem_bytes(E);
     auto k = route_meta_single_kernel<RMAX>;
     if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t err = allow_shared_memory(k, route_smem_bytes(MOE_MAX_EXPERTS));
         if (err != cudaSuccess) return err;
     }
     return launch_pdl(ctx, k, dim3(1), dim3(kRouteThreads), smem, a);
@@ -417,7 +417,7 @@ cudaError_t launch_rmax(const LaunchCtx& ctx, const RoutePlan& plan, const Route
     if (plan.single) return launch_single<RMAX>(ctx, a, E);
     auto k1 = route_meta_count_kernel<RMAX>;
     if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t err = allow_shared_memory(k1, route_smem_bytes(MOE_MAX_EXPERTS));
         if (err != cudaSuccess) return err;
     }
     cudaError_t err = launch_pdl(ctx, k1, dim3(plan.blocks), dim3(kRouteThreads), smem, a);

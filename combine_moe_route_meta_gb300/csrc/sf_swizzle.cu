@@ -281,7 +281,7 @@ int64_t sf_grid(const LaunchCtx& ctx, const SfTiles& a, int per_sm) {
 template <typename Kernel>
 cudaError_t launch_sf(const LaunchCtx& ctx, Kernel kern, const SfTiles& a, size_t smem) {
     if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t err = allow_shared_memory(kern, kMostSharedMemory);
         if (err != cudaSuccess) return err;
     }
     int per_sm = 0;
@@ -297,7 +297,7 @@ bool sf_tiles_interleave_zeroes(const SfTiles& a) {
 }
 
 bool sf_tiles_interleavable(const SfTiles& a) {
-    return a.C % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15) == 0 && interleave_smem(a) <= 200 * 1024;
+    return a.C % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15) == 0 && interleave_smem(a) <= kMostSharedMemory;
 }
 
 cudaError_t launch_sf_tiles_clear(const LaunchCtx& ctx, const SfTiles& a) {
