@@ -422,6 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 template <bool SWIGLU>
 cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
+    auto kern = expert_gemm_kernel<SWIGLU>;
+    // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
+    const cudaError_t err = allow_shared_memory(kern, 1024 + size_t(kStages) * kSlot + shared_bytes(MOE_MAX_EXPERTS));
+    if (err != cudaSuccess) return err;
     const uint64_t kb = uint64_t(g.k) / 2;
     CUtensorMap map_a, map_a32, map_w;
     const uint64_t da[2] = {kb, uint64_t(g.rows)}, dw[4] = {kb, uint64_t(g.n), SWIGLU ? 2u : 1u, uint64_t(g.E)};
@@ -434,9 +438,6 @@ cudaError_t launch(const LaunchCtx& ctx, const ExpertGemm& g) {
                      g.scale_layout == MOE_SCALES_SWIZZLED_128X4 && reinterpret_cast<uintptr_t>(g.a_sf) % 16 == 0,
                      reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
     const size_t smem = 1024 + size_t(kStages) * kSlot + shared_bytes(g.E);
-    auto kern = expert_gemm_kernel<SWIGLU>;
-    cudaError_t err = allow_shared_memory(kern, 1024 + size_t(kStages) * kSlot + shared_bytes(MOE_MAX_EXPERTS));
-    if (err != cudaSuccess) return err;
     return launch_pdl(ctx, kern, dim3(unsigned(ctx.num_sms)), dim3(kThreads), smem, a, map_a, map_a32, map_w);
 }
 

@@ -835,6 +835,10 @@ template <bool NVFP4, bool DOWN, int PER>
 cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     using S = Shape<NVFP4, DOWN>;
     constexpr size_t kMost = 226 * 1024;  // dynamic shared memory beside the static part
+    auto kern = few_tokens_kernel<NVFP4, DOWN, PER>;
+    // first: it makes the device's context current in a thread that has made no CUDA call yet, and the map needs one
+    const cudaError_t err = allow_shared_memory(kern, kMost - sizeof(Shared));
+    if (err != cudaSuccess) return err;
     const int rows = DOWN ? f.H : f.I, k = DOWN ? f.I : f.H, pairs = f.T * f.K;
     LayerArgs a{f, 0, 0, NVFP4 ? k / 2 : 2 * k, (rows + 127) / 128, k, 0};
     a.chunks = (a.row_bytes + 127) / 128;
@@ -859,13 +863,10 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
         1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + pairs;
     a.stages = int(std::min<size_t>(max_stages(NVFP4), (kMost - sizeof(Shared) - fixed) / S::kSlot));
 
-    auto kern = few_tokens_kernel<NVFP4, DOWN, PER>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreadsOf<PER>);
     cfg.dynamicSmemBytes = fixed + size_t(a.stages) * S::kSlot;
     cfg.stream = ctx.stream;
-    const cudaError_t err = allow_shared_memory(kern, kMost - sizeof(Shared));
-    if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;

@@ -58,9 +58,9 @@ def _layer_job(m, T, K, status):
 def _product_job(m, E, status):
     """moe_expert_gemm, whose shared memory grows with the number of experts."""
     gen = torch.Generator(device="cuda").manual_seed(E)
-    w = m.quantize_nvfp4(torch.randn(E, 64, 64, device="cuda", generator=gen).bfloat16(), torch.full((E,), 500.0, device="cuda"))
-    a = m.quantize_nvfp4(torch.randn(E * 2, 64, device="cuda", generator=gen).bfloat16(), torch.full((1,), 500.0, device="cuda"),
-                         scale_layout="row")
+    g = torch.full((E,), 500.0, device="cuda")
+    w = m.quantize_nvfp4(torch.randn(E, 64, 64, device="cuda", generator=gen).bfloat16(), g)
+    a = m.quantize_nvfp4(torch.randn(E * 2, 64, device="cuda", generator=gen).bfloat16(), g[:1], scale_layout="row")
     count = torch.full((E,), 2, dtype=torch.int32, device="cuda")
     out = torch.empty((E * 2, 64), dtype=torch.bfloat16, device="cuda")
 
@@ -132,12 +132,41 @@ def test_calls_of_different_sizes_from_several_threads(kind):
 
 def test_no_call_lowers_another_threads_shared_memory(tmp_path):
     """The limit of a kernel's shared memory is the kernel's, not the launch's. Threads without an interpreter between their
-    calls meet inside the entry points often enough (one to three launches in a hundred were refused where each call set the limit to its own size)."""
+    calls meet inside the entry points often enough: where each call set the limit to its own size, one to three launches
+    in a hundred were refused."""
     from combine_moe_route_meta_gb300 import build
     here = os.path.dirname(os.path.abspath(__file__))
     exe, lib = str(tmp_path / "native_threads"), build.LIB_PATH
-    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", f"-I{build.INCLUDE}", os.path.join(here, "native_threads.cpp"), lib,
-                    "-Xlinker", "-rpath", "-Xlinker", os.path.dirname(lib), "-o", exe], check=True, timeout=300)
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", f"-I{build.INCLUDE}", os.path.join(here, "native_threads.cpp"),
+                    lib, "-Xlinker", "-rpath", "-Xlinker", os.path.dirname(lib), "-o", exe], check=True, timeout=300)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == ["product", "0", "layer", "0", "route", "0"], r.stdout
+
+
+@pytest.mark.parametrize("kind", list(JOBS))
+def test_the_first_cuda_call_of_a_thread(kind):
+    """A call may be what makes the device's context current in its thread."""
+    m = moe()
+    status = m.new_status()
+    job, out = JOBS[kind](m, status)[0]
+    job(None)
+    torch.cuda.synchronize()
+    want = out.clone()
+    out.zero_()
+    torch.cuda.synchronize()
+    raised = []
+
+    def work():
+        try:
+            job(0)                            # the legacy default stream
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not raised, raised
+    m.check_status(status)
+    assert torch.equal(out.view(torch.uint8), want.view(torch.uint8))
