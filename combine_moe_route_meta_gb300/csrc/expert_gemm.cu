@@ -360,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ragged = 0;
     for (int e = threadIdx.x; e < a.g.E; e += kThreads) {
         const RowSpan r = expert_rows(a.g, e);
-        s->prefix()[e + 1] = (r.count + kTileM - 1) / kTileM;
+        s->prefix()[e + 1] = int((uint32_t(r.count) + kTileM - 1) / kTileM);
         s->base(a.g.E)[e] = int(r.base);
-        s->last(a.g.E)[e] = uint8_t((r.count + kTileM - 1) % kTileM);
+        s->last(a.g.E)[e] = uint8_t((uint32_t(r.count) + kTileM - 1) % kTileM);
         ragged |= r.count > 0 && r.base % 128 != 0;
     }
     const bool sf_bulk = !__syncthreads_or(ragged) && a.sf_bulk_ok;
     if (warp == 0) {
-        int sum = 0;
+        int64_t sum = 0;
         for (int e0 = 0; e0 < a.g.E; e0 += 32) {
             int v = e0 + lane < a.g.E ? s->prefix()[e0 + lane + 1] : 0;
 #pragma unroll
@@ -375,12 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int u = __shfl_up_sync(kFullMask, v, o);
                 if (lane >= o) v += u;
             }
-            if (e0 + lane < a.g.E) s->prefix()[e0 + lane + 1] = sum + v;
+            if (e0 + lane < a.g.E) s->prefix()[e0 + lane + 1] = int(sum + v);
             sum += __shfl_sync(kFullMask, v, 31);
+        }
+        // Experts that share no row have at most so many row tiles, and their tiles of the output are counted in 31 bits
+        // (checked on the host). Overlapping segments could have any number of both.
+        if (sum > a.g.rows / kTileM + a.g.E) {
+            if (lane == 0) set_status(a.g.status, MOE_ERR_INVALID_ARG);
+            sum = 0;
         }
         if (lane == 0) {
             s->prefix()[0] = 0;
-            s->tiles = sum * a.tiles_n;
+            s->tiles = int(sum) * a.tiles_n;
             s->dead = 0;
             for (int i = 0; i < kStages; i++) {
                 mbar_init(smem_addr(&s->full[i]), sf_bulk ? 1 : 2);

@@ -70,6 +70,8 @@ moe_status_t moe_dequantize_nvfp4(const uint8_t *codes, const uint8_t *scales, i
  *   of out are not written, and what other rows of `a` hold does not matter.
  *   A count above M (masked) or rows beyond `rows` (normal) are cut off and reported as
  *   MOE_ERR_CAPACITY; a negative count or start is skipped and reported as MOE_ERR_INVALID_ARG.
+ *   No row belongs to two experts: segments that overlap so far that they have more than
+ *   rows / 128 + E tiles of 128 rows are reported as MOE_ERR_INVALID_ARG, and nothing is written.
  * Arguments:
  *   num_experts (E)  1..MOE_MAX_EXPERTS.
  *   max_tokens_per_expert (M)  masked: >= 1. Ignored in normal mode.
