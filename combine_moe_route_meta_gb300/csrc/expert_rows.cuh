@@ -69,18 +69,22 @@ __device__ __forceinline__ int64_t act_sf_index(int layout, int64_t r, int c, in
     return layout == MOE_SCALES_SWIZZLED_128X4 ? swizzled_128x4_index(r, c, C) : r * C + c;
 }
 
-// up * gate / (1 + exp(-gate)) to about 2^-21: exp(-gate) = 2^t, t = -gate log2(e), whose rounding error (grown with
-// |gate|) is put back to first order, 2^(t + d) = 2^t (1 + d ln 2); 2^t and the reciprocal by the approximate
-// instructions. Beyond +-80 (where 2^t is still finite) the quotient is gate, or below 10^-31 and taken as 0.
+// up * gate / (1 + exp(-gate)) to 2^-20, with exp(-|gate|) = e c: the quotient is gate / (1 + e c), times e c below 0, so
+// that nothing overflows and no gate's value is lost that a large `up` could make count. e = 2^t, t = -|gate| log2(e), and
+// c = 1 + d ln 2 puts back t's rounding error d (grown with |gate|) to first order. 2^t (subnormal values too) and the
+// reciprocal are the approximate instructions. Beyond 110 e is 0 in binary32.
 __device__ __forceinline__ float swiglu(float gate, float up) {
     constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2(e) = kLog2e + kRest
-    const float g = fminf(fmaxf(gate, -80.0f), 80.0f);
-    const float t = -g * kLog2e;
-    const float d = fmaf(-g, kLog2e, -t) - g * kRest;
+    float g;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(gate), "f"(-110.0f));
+    const float a = fminf(fabsf(g), 110.0f);
+    const float t = -a * kLog2e;
+    const float c = fmaf(fmaf(-a, kLog2e, -t) - a * kRest, kLn2, 1.0f);
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fmaf(e, d * kLn2, e)));
-    return up * (gate < -80.0f ? 0.0f : gate * r);
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, c, 1.0f)));
+    // e by itself: a subnormal e is not rounded twice, nor its small product with gate
+    return g < 0.0f ? (up * e) * (g * r * c) : up * (g * r);
 }
 
 }  // namespace moe

@@ -100,8 +100,10 @@ moe_status_t moe_expert_gemm(moe_mode_t mode, const uint8_t *a_codes, const uint
  * `inter` up rows of expert e:
  *   G = alpha[e] * sum_k a[r, k] * w13[e, i, k],  U = alpha[e] * sum_k a[r, k] * w13[e, inter + i, k]
  *   h[r, i] = U * (G / (1 + exp(-G)))        in fp32, then quantised as moe_quantize_nvfp4 does
- *   with g = out_global_scale. The product's sums and exp are fp32 with their own rounding, so a
- *   code next to a rounding boundary may differ from another evaluation's.
+ *   with g = out_global_scale. The product's sums and exp are fp32 with their own rounding (h is
+ *   within 2^-20 of its value for the G and U that the sums give; within 2^-19 for G below -87, where
+ *   the step of a subnormal exp(G) comes on top), so a code next to a rounding boundary may differ
+ *   from another evaluation's.
  * Arguments as moe_expert_gemm, with inter % 64 == 0 and
  *   w13_codes        [E, 2*inter, k/2]; w13_scales: per expert and half the tiles of its own
  *                    [roundup(inter, 128), k/16] matrix (moe_quantize_nvfp4 with 2*E groups).
