@@ -1,13 +1,13 @@
 // nvfp4_quant.cu -- bf16 rows to NVFP4 codes and block scales, and back.
 //
-//   quantise:    sf = e4m3((amax16 * (1/6)) * g),  q = e2m1(x * (g / sf))   (quantise_block)
+//   quantise:    sf = e4m3((amax16 / 6) * g),  q = e2m1(x * (g / sf))   (quantise_block)
 //   dequantise:  out = bf16((value(q) * value(sf)) / g)
 //
 // A thread takes one block of 16 elements at a time: 32 contiguous bytes of a bf16 row, 8 bytes of codes and
 // one scale byte, so a block's amax needs no shuffle; four neighbouring threads join their scales to a word.
 // A thread block takes kQuantRows rows x 64 CC columns, whose scales lie next to each other in the 512-byte tiles, and
 // issues all its loads before it computes. Bound by DRAM: 2.5625 bytes per element. 32 experts' weights of 2048 x 7168
-// quantised and read back, 2.4 GB, take 363 us (6.6 TB/s, 98 % of the copy bandwidth); 3 x 1001 x 4160 values 13.5 us
+// quantised and read back, 2.4 GB, take 364 us (6.6 TB/s, 97 % of the copy bandwidth); 3 x 1001 x 4160 values 14.2 us
 // and 128 x 7168 values 3.6 us for the two launches, whose starts and ends these are.
 #include <algorithm>
 #include <cstdint>
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 // Rows of a thread block. Smaller ones leave more blocks to an SM: 32 experts' weights (0.94 GB) quantised in
-// 218 us with 128, 193 us with 64.
+// 218 us with 128, 193 us with 64 (before a block's scale took a division).
 constexpr int kQuantRows = 64;
 
 struct QuantArgs {

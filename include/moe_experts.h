@@ -34,10 +34,9 @@ extern "C" {
  * moe_quantize_nvfp4 -- quantise `groups` matrices [rows, hidden] of bf16, each with its own
  * global scale g, per block of 16 consecutive elements, in binary32 with round to nearest even, in
  * the order written:
- *   sf = e4m3_rn_satfinite((amax * (1/6)) * g),  q = e2m1_rn_satfinite(x * (g / sf)), 0 if sf is 0,
- * with 1/6 itself rounded to binary32. moe_dispatch's MOE_QUANT_NVFP4_B16 divides amax by 6 instead:
- * the two give the same blocks but where the scale lies on the boundary between two e4m3 values.
- * The usual g is 448 * 6 / max|x| of the matrix.
+ *   sf = e4m3_rn_satfinite((amax / 6) * g),  q = e2m1_rn_satfinite(x * (g / sf)), 0 if sf is 0:
+ * the codes and scales of moe_dispatch's MOE_QUANT_NVFP4_B16. The usual g is 448 * 6 / max|x| of
+ * the matrix.
  *   x              [groups, rows, hidden] bf16, 16-byte aligned
  *   hidden         > 0, % 16 == 0; % 64 == 0 for MOE_SCALES_SWIZZLED_128X4
  *   global_scales  [groups] fp32
