@@ -7,20 +7,6 @@
 
 namespace moe {
 
-// 8 codes times their block's scale (twice in s), as 4 pairs of fp16
-__device__ __forceinline__ void decode8(uint32_t codes, uint32_t s, uint32_t* out) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
-        : "r"(codes));
-#pragma unroll
-    for (int i = 0; i < 4; i++) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(out[i]) : "r"(s));
-}
-
 // A block of 16 values as NVFP4: its codes, and the scale, in the binary32 steps of the dispatch: sf = e4m3((amax / 6) * g),
 // r = g / value(sf), q = e2m1(x * r); all codes 0 where value(sf) is 0. A product with the rounded 1/6 would give blocks on a
 // boundary another scale than the dispatch gives them (and 32 experts' weights 1 % less time).
