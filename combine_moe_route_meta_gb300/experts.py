@@ -273,7 +273,7 @@ class ExpertWeights(NamedTuple):
     w2: torch.Tensor                       # [E, hidden, inter] bf16, or codes [E, hidden, inter/2]
     w13_scales: Optional[torch.Tensor] = None
     w2_scales: Optional[torch.Tensor] = None
-    alpha13: Optional[torch.Tensor] = None  # [E] fp32: 1 / global scale of w13[e]
+    alpha13: Optional[torch.Tensor] = None  # [E] fp32: 1 / global scale of w13[e]; None: 1
     alpha2: Optional[torch.Tensor] = None
 
     @property
@@ -327,7 +327,9 @@ class MoELayer:
         if not (input_scale > 0 and inter_scale > 0):
             raise ValueError("input_scale, inter_scale: positive scales needed to quantise activations")
         self.input_scale, self.inter_scale = float(input_scale), float(inter_scale)
-        self.alpha13, self.alpha2 = weights.alpha13 / self.input_scale, weights.alpha2 / self.inter_scale
+        one = torch.ones(self.E, dtype=torch.float32, device=dev)
+        self.alpha13 = (one if weights.alpha13 is None else weights.alpha13) / self.input_scale
+        self.alpha2 = (one if weights.alpha2 is None else weights.alpha2) / self.inter_scale
         rows = max_tokens * topk + self.E * (self.ALIGN - 1)
         byte = dict(dtype=torch.uint8, device=dev)
         i32 = dict(dtype=torch.int32, device=dev)
