@@ -12,7 +12,12 @@
 // each of which leaves at most 0.18 of the block's largest value (half of e2m1's widest step, and the rounding of the
 // scale; typically a twelfth): after five, 2^-12 of it (typically 2^-18). So a pair has five columns, whose products
 // are added in fp32 with the weights 8^-i.
-// s, for each column's whole length, brings its largest value to [2^8, 2^9), in the range of e4m3 scales.
+// s is one for a column's whole length, since the products add up along it. It brings the row's largest value to [2^8, 2^9),
+// in the range of e4m3 scales. Five terms are enough while the row's values lie near one another: a block whose largest is
+// 13 binary orders below the row's still keeps normal scales for its last terms, and what a large value leaves, 2^-18 of it,
+// is little against its neighbours. A row in which the largest of some four neighbours lies lower (by an outlier, say) is
+// multiplied in several passes, one for each 13 orders: a pass takes what the passes before it left, 2^13 times larger, in
+// five terms again, and the results of all are added. Where no row of a task is like that, one pass does.
 // With bf16 weights x is a column as it is, and h the sum of two bf16 columns (16 bits).
 //
 // Both kernels list the routed experts and their pairs (route()) and then work in roles:
@@ -27,7 +32,7 @@
 // not need, and loads weights until h is there. Every wait is bounded (MOE_ERR_TIMEOUT).
 //
 // Why so, and what it measured (both kernels, one GB300, weights from DRAM; 6782 GB/s is the copy bandwidth):
-//   256 experts of 7168 x 1024, top-8, NVFP4:    32 tokens 292 us (2.0 GB, 6.9 TB/s), 1 token 26.8 us (99 MB, 3.7 TB/s)
+//   256 experts of 7168 x 1024, top-8, NVFP4:    32 tokens 296 us (2.0 GB, 6.8 TB/s), 1 token 28.8 us (99 MB, 3.4 TB/s)
 //   128 experts of 4096 x 768, top-8, bf16:      5 tokens 103 us (0.67 GB, 6.5 TB/s)
 //   16 experts of 2112 x 704, top-3, bf16:       61 tokens 39 us (143 MB, 3.7 TB/s)
 // The tensor core takes weights as they are stored, so no instruction is spent on a weight: converting them in
@@ -61,7 +66,8 @@ constexpr int kRows = 256;                    // weight rows of a slot: two tile
 constexpr int kColumns = 64;                  // columns of a group of pairs
 constexpr int kTerms = 5;                     // columns of a pair, NVFP4
 constexpr int kMaxStages = 5;
-constexpr int kKept = 32;                      // tasks whose columns' largest magnitudes are kept
+constexpr int kOrders = 13;                   // binary orders of a pass: what five terms take off the largest value of a block
+constexpr int kKept = 32;                     // tasks whose columns' magnitudes and passes are kept
 constexpr int kMaxRanks = 8;
 constexpr uint32_t kTmemScales = 4 * kColumns;  // after two accumulators of two tiles
 constexpr uint32_t kTmemScaleSet = 64;          // of a slot, for each tile: its scales and the columns', 16 each
@@ -91,11 +97,14 @@ struct LayerArgs {
     int summed;          // columns of sums: T in down, in gate_up the pairs of the one task of a cluster
 };
 
-// Workspace: h as fp32 [pairs][I] and the largest magnitude of each 32 of it [pairs][4 ceil(I/128)] (NVFP4), or
-// two bf16 parts [pairs][2][I].
+// Workspace: h as fp32 [pairs][I] and for each 32 of it [pairs][4 ceil(I/128)] two bytes, the exponents of the largest
+// magnitude (high) and of the least largest of four neighbours that is not zero, or 255 (NVFP4); or two bf16 parts
+// [pairs][2][I].
 __device__ __forceinline__ float* h_values(const FewTokens& a) { return static_cast<float*>(a.workspace); }
 __host__ __device__ __forceinline__ int h_parts(int I) { return (I + 127) / 128 * 4; }
-__device__ __forceinline__ float* h_largest(const FewTokens& a) { return h_values(a) + int64_t(a.T) * a.K * a.I; }
+__device__ __forceinline__ uint16_t* h_range(const FewTokens& a) {
+    return reinterpret_cast<uint16_t*>(h_values(a) + int64_t(a.T) * a.K * a.I);
+}
 
 // ---------------------------------------------------------------------------
 // routing: the experts that some pair names, their pairs, and groups of these
@@ -196,10 +205,17 @@ __device__ __forceinline__ Routing route(const FewTokens& a, uint8_t* smem, uint
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], shifts_ready;
     uint32_t tmem;
-    int dead;  // a wait gave up
-    // NVFP4: bits of the largest magnitude of x for the pairs of a task; down has them for all its pairs at once
-    int largest[kKept][kColumns / 16 * 3];
+    int dead;           // a wait gave up
+    int passes[kKept];  // of task i, and 256 (i + 1)
 };
+
+// gate_up with NVFP4: exponents of the largest magnitude of x for the pairs of a task, and 255 minus those of the least largest
+// of four that is not zero. (down has shifts and passes of all its pairs at once.)
+struct Ranges {
+    int largest[kKept][kColumns / 16 * 3], least[kKept][kColumns / 16 * 3];
+};
+template <bool NVFP4, bool DOWN>
+constexpr size_t static_bytes() { return sizeof(Shared) + (NVFP4 && !DOWN ? sizeof(Ranges) : 0); }
 
 __device__ __forceinline__ bool wait_or_die(const LayerArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
     if (mbar_wait(bar, parity)) return true;
@@ -209,6 +225,25 @@ __device__ __forceinline__ bool wait_or_die(const LayerArgs& a, Shared* s, uint3
 }
 __device__ __forceinline__ bool warp_wait_or_die(const LayerArgs& a, Shared* s, uint32_t bar, uint32_t parity) {
     return __all_sync(kFullMask, wait_or_die(a, s, bar, parity));
+}
+
+// The passes of the block's task `i`, which a converter tells when it begins the task; as read before (`seen`), or waited for:
+// 0 when the wait gave up.
+__device__ __forceinline__ int passes_seen(Shared* s, int i) {
+    int n;
+    asm volatile("ld.relaxed.cta.shared::cta.s32 %0, [%1];" : "=r"(n) : "r"(smem_addr(&s->passes[i % kKept])) : "memory");
+    return n;
+}
+__device__ __forceinline__ int await_passes(const LayerArgs& a, Shared* s, int i, int seen) {
+    if (seen >> 8 == i + 1) return seen & 255;
+    const uint64_t t0 = global_ns();
+    for (int polls = 0; polls < kWaitMinPolls || global_ns() - t0 <= kWaitLimitNs; polls++) {
+        seen = passes_seen(s, i);
+        if (seen >> 8 == i + 1) return seen & 255;
+    }
+    *const_cast<volatile int*>(&s->dead) = 1;
+    set_status(a.f.status, MOE_ERR_TIMEOUT);
+    return 0;
 }
 
 // The block's n-th task: a group of pairs and, in gate_up, a 128-row block.
@@ -250,23 +285,26 @@ __device__ __forceinline__ void load_role(const LayerArgs& a, Shared* s, const R
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
-        for (int c = work.c0; c < work.c1; c++) {
-            if (!wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
-            const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * S::kSlot;
-            const bool second = !DOWN || t.block + 1 < a.blocks;
-            const int q = NVFP4 ? min(4, k64 - 4 * c) : 0;
-            mbar_expect_tx(bar, S::kA + q * 512 * (second ? 2 : 1));
-            // dimensions (k, row, half, expert): 128 rows of both halves, or 256 rows
-            tma_load_4d(slot, map, c * 128, t.block * 128, 0, t.e, bar);
-            if (NVFP4) {
-                const int64_t block = DOWN ? int64_t(t.e) * a.blocks + t.block : int64_t(t.e) * 2 * a.blocks + t.block;
-                const uint32_t to = slot + S::kA + S::kB;
-                bulk_load_announced(to, sf + (block * k64 + 4 * c) * 512, q * 512, bar);
-                if (second)
-                    bulk_load_announced(to + S::kSfA / 2,
-                                        sf + ((block + (DOWN ? 1 : a.blocks)) * k64 + 4 * c) * 512, q * 512, bar);
+        for (int pass = 0, passes = 1; pass < passes; pass++) {
+            for (int c = work.c0; c < work.c1; c++) {
+                if (!wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
+                const uint32_t bar = smem_addr(&s->full[st]), slot = slots + st * S::kSlot;
+                const bool second = !DOWN || t.block + 1 < a.blocks;
+                const int q = NVFP4 ? min(4, k64 - 4 * c) : 0;
+                mbar_expect_tx(bar, S::kA + q * 512 * (second ? 2 : 1));
+                // dimensions (k, row, half, expert): 128 rows of both halves, or 256 rows
+                tma_load_4d(slot, map, c * 128, t.block * 128, 0, t.e, bar);
+                if (NVFP4) {
+                    const int64_t block = DOWN ? int64_t(t.e) * a.blocks + t.block : int64_t(t.e) * 2 * a.blocks + t.block;
+                    const uint32_t to = slot + S::kA + S::kB;
+                    bulk_load_announced(to, sf + (block * k64 + 4 * c) * 512, q * 512, bar);
+                    if (second)
+                        bulk_load_announced(to + S::kSfA / 2,
+                                            sf + ((block + (DOWN ? 1 : a.blocks)) * k64 + 4 * c) * 512, q * 512, bar);
+                }
+                if (++st == a.stages) st = 0, ph ^= 1;
             }
-            if (++st == a.stages) st = 0, ph ^= 1;
+            if (NVFP4 && pass == 0 && (passes = await_passes(a, s, i, 0)) == 0) return;
         }
     }
 }
@@ -312,32 +350,38 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
     const uint32_t tmem = s->tmem, scales = tmem + kTmemScales + half * 32;
     const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
     const int q_last = (a.row_bytes - (a.chunks - 1) * 128) / 32;
-    int st = 0;
+    int st = 0, n_pass = 0;  // n_pass: passes of all tasks so far
     uint32_t ph = 0;
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
-        const int buf = i & 1, n = S::columns(t.n);
-        const uint32_t d = tmem + (buf * 2 + half) * kColumns;
+        const int n = S::columns(t.n);
         const uint32_t idesc = NVFP4 ? idesc_nvfp4(n) : idesc_bf16(n);
         const bool there = !DOWN || t.block + half < a.blocks;
-        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_empty[buf]), (i >> 1 & 1) ^ 1)) return;
-        tc_fence_after();
-        for (int c = work.c0; c < work.c1; c++) {
-            if (!warp_wait_or_die(a, s, full + 8 * st, ph)) return;
+        for (int pass = 0, passes = 1; pass < passes; pass++, n_pass++) {
+            const int buf = n_pass & 1;
+            const uint32_t d = tmem + (buf * 2 + half) * kColumns;
+            int seen = 0;
+            if (!warp_wait_or_die(a, s, smem_addr(&s->acc_empty[buf]), (n_pass >> 1 & 1) ^ 1)) return;
             tc_fence_after();
-            if (leader) {
-                const uint32_t off = st * (S::kSlot / 16), ts = scales + st * kTmemScaleSet;
-                if (there) {
-                    if (c + 1 < a.chunks || q_last == 4)
-                        multiply_slot<NVFP4>(o, off, d, ts, idesc, 4, c > work.c0);
-                    else
-                        multiply_slot<NVFP4>(o, off, d, ts, idesc, q_last, c > work.c0);
+            for (int c = work.c0; c < work.c1; c++) {
+                if (!warp_wait_or_die(a, s, full + 8 * st, ph)) return;
+                tc_fence_after();
+                if (NVFP4 && c == work.c0) seen = passes_seen(s, i);
+                if (leader) {
+                    const uint32_t off = st * (S::kSlot / 16), ts = scales + st * kTmemScaleSet;
+                    if (there) {
+                        if (c + 1 < a.chunks || q_last == 4)
+                            multiply_slot<NVFP4>(o, off, d, ts, idesc, 4, c > work.c0);
+                        else
+                            multiply_slot<NVFP4>(o, off, d, ts, idesc, q_last, c > work.c0);
+                    }
+                    tc_commit(empty + 8 * st);
+                    if (c + 1 == work.c1) tc_commit(smem_addr(&s->acc_full[buf]));
                 }
-                tc_commit(empty + 8 * st);
-                if (c + 1 == work.c1) tc_commit(smem_addr(&s->acc_full[buf]));
+                __syncwarp();
+                if (++st == a.stages) st = 0, ph ^= 1;
             }
-            __syncwarp();
-            if (++st == a.stages) st = 0, ph ^= 1;
+            if (NVFP4 && pass == 0 && (passes = __reduce_min_sync(kFullMask, await_passes(a, s, i, seen))) == 0) return;
         }
     }
     // the last slot's arrival is the last that is on its way to this block's memory
@@ -347,21 +391,40 @@ __device__ __forceinline__ void mma_role(const LayerArgs& a, Shared* s, const Ro
 // 2^e as fp32, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// The power of two that brings a largest magnitude to [2^8, 2^9).
-__device__ __forceinline__ int shift_of(float largest) {
-    return largest == 0.0f ? 0 : 8 - max(int(__float_as_uint(largest) >> 23) - 127, -110);
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-    return v;
+// The power of two that brings a row's largest magnitude, by its (biased) exponent, to [2^8, 2^9); at most 2^126, with which
+// a row below 2^-118 is left with what binary32 has of it.
+constexpr int kMostShift = 126;
+__device__ __forceinline__ int shift_of(int exponent) { return min(8 + 127 - exponent, kMostShift); }
+// That of a pass.
+__device__ __forceinline__ int pass_shift(int shift, int pass) { return min(shift + kOrders * pass, kMostShift); }
+// The passes after the first that a row with shift `shift` needs, by the exponent of the least magnitude that counts.
+__device__ __forceinline__ int more_passes(int shift, int exponent) { return max(8 + 127 - shift - exponent - 1, 0) / kOrders; }
+// A pass that comes before any that finds something of a block with this largest magnitude: the last term's scale is 0 where
+// the block's largest is 2^-20 or less in the pass. (In the first pass it may be too small for binary32.)
+__device__ __forceinline__ int first_pass(int shift, float block) {
+    const int below = 8 - shift - (int(__float_as_uint(block) >> 23) - 127);
+    return max(below - 29, 0) / kOrders;
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The largest magnitudes of eight bf16 values by fours.
+__device__ __forceinline__ uint32_t largest_by_fours(const uint4& w) {
+    return max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 }
 
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
@@ -389,10 +452,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return p;
 }
 
-// Term i of what is left of a block of 16 values: its codes, the scale, and in f what is left after it. The scale is
-// that of 8^i f.
-__device__ __forceinline__ uint2 split_term(uint64_t (&f)[8], int i, uint32_t* sf) {
-    const float up = float(1 << 3 * i);
+// Term i of what is left of a block of 16 values: its codes, the scale, and in f what is left after it (`last`: nothing
+// looks at that). The scale is that of 8^i f.
+__device__ __forceinline__ uint2 split_term(uint64_t (&f)[8], int i, uint32_t* sf, bool last) {
+    const float up = pow2(3 * i), down = pow2(-3 * i);
     float m[8];  // by halves: a chain of 16 is in the way of the next term
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -404,8 +467,8 @@ __device__ __forceinline__ uint2 split_term(uint64_t (&f)[8], int i, uint32_t* s
 #pragma unroll
         for (int j = 0; j < 4; j++)
             if (j < h) m[j] = fmaxf(m[j], m[j + h]);
-    *sf = e4m3x2(m[0] * (up / 6.0f), 0.0f) & 0xffu;
-    const float s = e4m3_value(*sf) * (1.0f / up);
+    *sf = e4m3x2(m[0] * (up * (1.0f / 6.0f)), 0.0f) & 0xffu;
+    const float s = e4m3_value(*sf) * down;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r = s > 0.0f ? r : 0.0f;
@@ -424,7 +487,7 @@ __device__ __forceinline__ uint2 split_term(uint64_t (&f)[8], int i, uint32_t* s
             "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
             : "=r"(q[w])
             : "f"(y0.x), "f"(y0.y), "f"(y1.x), "f"(y1.y), "f"(y2.x), "f"(y2.y), "f"(y3.x), "f"(y3.y));
-        if (i + 1 == kTerms) continue;  // nothing looks at what is left
+        if (last) continue;
         uint32_t h[4];
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -457,6 +520,19 @@ struct Sixteen {
             if (ok) w[l] = DOWN ? from[l] : __ldg(from + l);
         }
     }
+    __device__ __forceinline__ float largest() const {
+        if constexpr (DOWN) {
+            float m = 0.0f;
+#pragma unroll
+            for (int l = 0; l < 4; l++)
+                m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(w[l].x)), fabsf(__uint_as_float(w[l].y))),
+                                   fmaxf(fabsf(__uint_as_float(w[l].z)), fabsf(__uint_as_float(w[l].w)))));
+            return m;
+        } else {
+            const uint32_t m = max_bf16x2(largest_by_fours(w[0]), largest_by_fours(w[1]));
+            return fmaxf(bf16_lo(m), bf16_hi(m));
+        }
+    }
     __device__ __forceinline__ void scaled(float scale, uint64_t (&f)[8]) const {
         float v[16];
         if constexpr (DOWN) {
@@ -474,10 +550,82 @@ struct Sixteen {
     }
 };
 
-// Warp `v` of the converters: half the work of every `turns`th slot. down: `shifts` [pairs in the list].
+// A term of a block of 16 in row `row` of a slot's columns.
+__device__ __forceinline__ void store_term(uint32_t to, int row, int block, uint2 q, uint32_t sf) {
+    constexpr uint32_t kSf = Shape<true, false>::kB + Shape<true, false>::kSfA;
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + swizzled(row, block >> 1) + (block & 1) * 8), "r"(q.x), "r"(q.y)
+                 : "memory");
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + kSf + (block >> 2) * 512 + (row % 32) * 16 + row / 32 * 4 + (block & 3)),
+                 "r"(sf)
+                 : "memory");
+}
+
+// The shift of pair j of the block's task i, and the passes after the first that its row needs.
+template <bool DOWN>
+__device__ __forceinline__ int row_shift(const Ranges* ranges, const int8_t* shifts, const Task& t, int i, int j) {
+    return DOWN ? shifts[t.first + j] : shift_of(ranges->largest[i % kKept][j]);
+}
+template <bool DOWN>
+__device__ __forceinline__ int row_more(const LayerArgs& a, const Ranges* ranges, const int8_t* shifts, const Task& t, int i,
+                                        int j) {
+    if (DOWN) return shifts[a.f.T * a.f.K + t.first + j];
+    return more_passes(row_shift<DOWN>(ranges, shifts, t, i, j), 255 - ranges->least[i % kKept][j]);
+}
+
+// The further passes of task i, rarely: what the passes before leave, each block from its first pass on. The warp's place in
+// the ring and its phase before, and after as st | ph << 8 | skip << 9; -1 when a wait gave up. Kept small: a kernel's start
+// takes longer with its size. One token, which has no use for it, takes 28.1 us without it, 28.8 us with it, and 29.4 us with
+// its terms unrolled or as a function of its own.
 template <bool NVFP4, bool DOWN, int PER>
-__device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
-                                             uint32_t slots, int v, int8_t* shifts) {
+__device__ __forceinline__ int convert_more(const LayerArgs& a, Shared* s, const Ranges* ranges, const Routing& r,
+                                            const Work<DOWN>& work, uint32_t slots, int v, const int8_t* shifts, int i,
+                                            int passes, int st, int ph, int skip) {
+    using S = Shape<NVFP4, DOWN>;
+    const int lane = threadIdx.x & 31, turns = min(kTurns, a.stages), part = v % PER;
+    const int block = lane % 16, pair = part * 2 + lane / 16;
+    const Task t = work.task(a, r, i);
+    for (int pass = 1; pass < passes; pass++) {
+        int c = work.c0 + skip;
+        for (; c < work.c1; c += turns) {
+            if (!warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return -1;
+            for (int j0 = 0; j0 + part * 2 < t.n; j0 += 2 * PER) {
+                const int j = j0 + pair, at = min(j, t.n - 1), k = c * S::kChunk + block * 16;
+                const int shift = row_shift<DOWN>(ranges, shifts, t, i, at);
+                Sixteen<DOWN> now;
+                now.load(a, r.list[t.first + at], k, k < a.k);
+                int p = min(pass, first_pass(shift, now.largest()));
+                uint64_t f[8];
+                now.scaled(pass <= row_more<DOWN>(a, ranges, shifts, t, i, at) ? pow2(pass_shift(shift, p)) : 0.0f, f);
+                const int row0 = S::column(at);
+                for (;; p++) {
+#pragma unroll 1
+                    for (int l = 0; l < kTerms; l++) {
+                        uint32_t sf;
+                        const uint2 q = split_term(f, l, &sf, false);
+                        if (p == pass && j < t.n) store_term(slots + st * S::kSlot + S::kA, row0 + l, block, q, sf);
+                    }
+                    if (p == pass) break;
+                    const float up = pow2(pass_shift(shift, p + 1) - pass_shift(shift, p));
+#pragma unroll
+                    for (int l = 0; l < 8; l++) f[l] = mul2(f[l], pair_of(up, up));
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&s->full[st]));
+            st += turns;
+            if (st >= a.stages) st -= a.stages, ph ^= 1;
+        }
+        skip = c - work.c1;
+    }
+    return st | ph << 8 | skip << 9;
+}
+
+// Warp `v` of the converters: its part of every `turns`th slot. down: `shifts` [pairs in the list], and behind them [pairs]
+// the passes after the first that each needs.
+template <bool NVFP4, bool DOWN, int PER>
+__device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, Ranges* ranges, const Routing& r,
+                                             const Work<DOWN>& work, uint32_t slots, int v, int8_t* shifts) {
     using S = Shape<NVFP4, DOWN>;
     const int lane = threadIdx.x & 31, tasks = work.tasks();
     const int turns = min(kTurns, a.stages), turn = v / PER, part = v % PER;
@@ -498,28 +646,34 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             now.load(a, list[ok ? j : 0], k, ok);
         };
         if (NVFP4) load(work.c0 + skip, pair);
+        int passes = 1;
+        int8_t* more = shifts + a.f.T * a.f.K;  // down: passes after the first
+        auto shift_at = [&](int j) { return row_shift<DOWN>(ranges, shifts, t, i, j); };
         if (NVFP4 && DOWN && i == 0) {  // of every pair of the list, a thread a pair
             const int parts = h_parts(a.k);
             for (int at = v * 32 + lane; at < r.first[r.groups]; at += PER * turns * 32) {
-                const float4* from = reinterpret_cast<const float4*>(h_largest(a.f) + int64_t(r.list[at]) * parts);
-                float m = 0.0f;
+                const uint2* from = reinterpret_cast<const uint2*>(h_range(a.f) + int64_t(r.list[at]) * parts);
+                uint32_t most = 0, least = ~0u;  // of two halves
 #pragma unroll 8
                 for (int p = 0; p < parts / 4; p++) {
-                    const float4 w = from[p];
-                    m = fmaxf(m, fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
+                    const uint2 w = from[p];
+                    most = max_u16x2(most, max_u16x2(w.x, w.y));
+                    least = min_u16x2(least, min_u16x2(w.x & 0x00ff00ffu, w.y & 0x00ff00ffu));
                 }
-                shifts[at] = int8_t(shift_of(m));
+                const int shift = shift_of(max(most & 0xffffu, most >> 16) >> 8);
+                shifts[at] = int8_t(shift);
+                more[at] = int8_t(more_passes(shift, min(least & 0xffffu, least >> 16)));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
             if (!warp_wait_or_die(a, s, smem_addr(&s->shifts_ready), 0)) return;
         }
         if (NVFP4 && !DOWN) {
-            int* largest = s->largest[i % kKept];
+            int *largest = ranges->largest[i % kKept], *lowest = ranges->least[i % kKept];
             // every warp looks at its part of the rows
             for (int j = 0; j < t.n; j++) {
                 const uint16_t* x = a.f.x + int64_t(list[j] / a.f.K) * a.k;
-                uint32_t m = 0;  // two bf16 magnitudes
+                uint32_t most = 0, least = ~0u;  // two bf16 magnitudes; least: of those that are not zero, minus one
                 for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * PER * turns * 256) {
                     uint4 w[4];
 #pragma unroll
@@ -528,53 +682,55 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
                         w[u] = k < a.k ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; u++)
-                        m = max_bf16x2(m, max_bf16x2(max_bf16x2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu),
-                                                     max_bf16x2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu)));
+                    for (int u = 0; u < 4; u++) {
+                        const uint32_t m = largest_by_fours(w[u]);
+                        most = max_bf16x2(most, m);
+                        least = min_u16x2(least, ((m | 0x80008000u) - 0x00010001u) ^ 0x80008000u);  // 0 -> 0xffff
+                    }
                 }
-                const float most = warp_max(fmaxf(bf16_lo(m), bf16_hi(m)));
-                if (lane == 0) atomicMax(largest + j, __float_as_int(most));  // non-negative floats
+                const uint32_t high = __reduce_max_sync(kFullMask, max(most & 0xffffu, most >> 16));
+                const uint32_t low = __reduce_min_sync(kFullMask, min(least & 0xffffu, least >> 16));
+                if (lane == 0) {
+                    atomicMax(largest + j, int(high >> 7));
+                    if (low != 0xffffu) atomicMax(lowest + j, 255 - int((low + 1) >> 7));
+                }
             }
             // long done with: a converter is at most 8 tasks ahead of what turns accumulators into results
-            if (v == 0 && lane < kColumns / 16 * 3) s->largest[(i + kKept / 2) % kKept][lane] = 0;
+            if (v == 0 && lane < kColumns / 16 * 3)
+                ranges->largest[(i + kKept / 2) % kKept][lane] = ranges->least[(i + kKept / 2) % kKept][lane] = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s->shifts_ready));
             if (!warp_wait_or_die(a, s, smem_addr(&s->shifts_ready), i & 1)) return;
+        }
+        if (NVFP4) {
+            passes = 1 + __reduce_max_sync(kFullMask, lane < t.n ? row_more<DOWN>(a, ranges, shifts, t, i, lane) : 0);
+            if (v == 0 && lane == 0)
+                asm volatile("st.relaxed.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_addr(&s->passes[i % kKept])),
+                             "r"((i + 1) << 8 | passes)
+                             : "memory");
         }
         int c = work.c0 + skip;
         for (; c < work.c1; c += turns) {
             const uint32_t to = slots + st * S::kSlot + S::kA;
             bool free = false;  // the slot: the first values are ready before it is waited for
             if (NVFP4) {
-                const uint32_t sf_to = to + S::kB + S::kSfA;
 #pragma unroll 1
                 for (int j0 = 0; j0 < t.n; j0 += 2 * PER) {
                     const int j = j0 + pair, at = min(j, t.n - 1);
                     uint64_t f[8];
-                    now.scaled(pow2(DOWN ? shifts[t.first + at] : shift_of(__int_as_float(s->largest[i % kKept][at]))),
-                               f);
+                    now.scaled(pow2(shift_at(at)), f);
                     load(j0 + 2 * PER < t.n ? c : c + turns, j0 + 2 * PER < t.n ? j + 2 * PER : pair);
                     if (j0 + part * 2 >= t.n) continue;
                     uint2 q[kTerms];
                     uint32_t sf[kTerms];
 #pragma unroll
-                    for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l]);
+                    for (int l = 0; l < kTerms; l++) q[l] = split_term(f, l, &sf[l], l + 1 == kTerms);
                     if (!free && !warp_wait_or_die(a, s, smem_addr(&s->empty[st]), ph ^ 1)) return;
                     free = true;
                     if (j >= t.n) continue;
                     const int row0 = S::column(j);
 #pragma unroll
-                    for (int l = 0; l < kTerms; l++) {
-                        const int row = row0 + l;
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + swizzled(row, block >> 1) +
-                                                                              (block & 1) * 8),
-                                     "r"(q[l].x), "r"(q[l].y)
-                                     : "memory");
-                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf_to + (block >> 2) * 512 + (row % 32) * 16 +
-                                                                    row / 32 * 4 + (block & 3)),
-                                     "r"(sf[l])
-                                     : "memory");
-                    }
+                    for (int l = 0; l < kTerms; l++) store_term(to, row0 + l, block, q[l], sf[l]);
                 }
             } else {
                 const int parts = DOWN ? 2 : 1;
@@ -612,6 +768,12 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, cons
             if (st >= a.stages) st -= a.stages, ph ^= 1;
         }
         skip = c - work.c1;
+        if (NVFP4 && passes > 1) {
+            const int next =
+                convert_more<NVFP4, DOWN, PER>(a, s, ranges, r, work, slots, v, shifts, i, passes, st, int(ph), skip);
+            if (next < 0) return;
+            st = next & 0xff, ph = next >> 8 & 1, skip = next >> 9;
+        }
     }
 }
 
@@ -631,8 +793,13 @@ __device__ __forceinline__ void store_h(const FewTokens& f, int p, int row, floa
     const float h = row < f.I ? swiglu(gate, up) : 0.0f;
     if (NVFP4) {
         if (row < f.I) h_values(f)[int64_t(p) * f.I + row] = h;
-        const float m = warp_max(fabsf(h));
-        if (row % 32 == 0) h_largest(f)[int64_t(p) * h_parts(f.I) + row / 32] = m;
+        float m = fmaxf(fabsf(h), __shfl_xor_sync(kFullMask, fabsf(h), 1));
+        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 2));
+        const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(m));
+        const uint32_t least = __reduce_min_sync(kFullMask, __float_as_uint(m) - 1);
+        if (row % 32 == 0)
+            h_range(f)[int64_t(p) * h_parts(f.I) + row / 32] =
+                uint16_t(most >> 23 << 8 | (least == ~0u ? 255u : (least + 1) >> 23));
     } else if (row < f.I) {
         uint16_t* to = static_cast<uint16_t*>(f.workspace) + int64_t(p) * 2 * f.I + row;
         const uint32_t hi = pack_bf16x2(h, 0.0f) & 0xffffu;
@@ -644,47 +811,61 @@ __device__ __forceinline__ void store_h(const FewTokens& f, int p, int row, floa
 // `sums` (of two rows, a thread's own): down's [T][kRows], or this block's [pairs][kRows] in the first block of a cluster
 // of gate_up, which has one task together; null where gate_up's tasks are its own.
 template <bool NVFP4, bool DOWN>
-__device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const Routing& r, const Work<DOWN>& work,
-                                            float* sums, const int8_t* shifts) {
+__device__ __forceinline__ void result_role(const LayerArgs& a, Shared* s, const Ranges* ranges, const Routing& r,
+                                            const Work<DOWN>& work, float* sums, const int8_t* shifts) {
+    using S = Shape<NVFP4, DOWN>;
     constexpr int kPairs = NVFP4 ? 3 : DOWN ? 8 : 16;  // pairs of 16 columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tasks = work.tasks();
     const uint32_t lanes = uint32_t(warp * 32) << 16;
+    int n_pass = 0;  // passes of all tasks so far
     for (int i = 0; i < tasks; i++) {
         const Task t = work.task(a, r, i);
-        const int buf = i & 1;
         const float* alphas = DOWN ? a.f.alpha2 : a.f.alpha13;
         const float alpha = alphas ? __ldg(alphas + t.e) : 1.0f;
-        if (!warp_wait_or_die(a, s, smem_addr(&s->acc_full[buf]), i >> 1 & 1)) return;
-        tc_fence_after();
-        for (int j0 = 0, c = 0; j0 < t.n; j0 += kPairs, c += 16) {
-            float v0[16], v1[16];
-            tmem_load16(s->tmem + lanes + buf * 2 * kColumns + c, v0);
-            tmem_load16(s->tmem + lanes + buf * 2 * kColumns + kColumns + c, v1);
-            if (j0 + kPairs >= t.n) {  // the last columns: the accumulator is free
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty[buf]));
-            }
+        float earlier[2][NVFP4 && !DOWN ? S::kGroup : 1];  // sums of the passes before, where there are several
+        for (int pass = 0, passes = 1; pass < passes; pass++, n_pass++) {
+            const int buf = n_pass & 1;
+            if (!warp_wait_or_die(a, s, smem_addr(&s->acc_full[buf]), n_pass >> 1 & 1)) return;
+            tc_fence_after();
+            const int seen = NVFP4 && pass == 0 ? passes_seen(s, i) : 0;
+            if (NVFP4 && pass == 0 && (passes = __reduce_min_sync(kFullMask, await_passes(a, s, i, seen))) == 0) return;
+            for (int j0 = 0, c = 0; j0 < t.n; j0 += kPairs, c += 16) {
+                float v0[16], v1[16];
+                tmem_load16(s->tmem + lanes + buf * 2 * kColumns + c, v0);
+                tmem_load16(s->tmem + lanes + buf * 2 * kColumns + kColumns + c, v1);
+                if (j0 + kPairs >= t.n) {  // the last columns: the accumulator is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&s->acc_empty[buf]));
+                }
 #pragma unroll
-            for (int j = 0; j < kPairs; j++) {
-                if (j0 + j >= t.n) break;
-                const int p = r.list[t.first + j0 + j];
-                float unscale = alpha;
-                if (NVFP4)
-                    unscale *= pow2(DOWN ? -shifts[t.first + j0 + j]
-                                         : -shift_of(__int_as_float(s->largest[i % kKept][j0 + j])));
-                const float y0 = pair_sum<NVFP4, DOWN>(v0, j) * unscale, y1 = pair_sum<NVFP4, DOWN>(v1, j) * unscale;
-                if (DOWN) {
-                    float* to = sums + (p / a.f.K) * kRows + warp * 32 + lane;
-                    const float f = __ldg(a.f.w + p);
-                    to[0] = fmaf(f, y0, to[0]);
-                    to[128] = fmaf(f, y1, to[128]);
-                } else if (sums) {
-                    float* to = sums + (j0 + j) * kRows + warp * 32 + lane;
-                    to[0] = y0;
-                    to[128] = y1;
-                } else {
-                    store_h<NVFP4>(a.f, p, t.block * 128 + warp * 32 + lane, y0, y1);
+                for (int j = 0; j < kPairs; j++) {
+                    if (j0 + j >= t.n) break;
+                    const int p = r.list[t.first + j0 + j];
+                    float y0 = pair_sum<NVFP4, DOWN>(v0, j) * alpha, y1 = pair_sum<NVFP4, DOWN>(v1, j) * alpha;
+                    if (NVFP4) {
+                        const float unscale = pow2(-pass_shift(row_shift<DOWN>(ranges, shifts, t, i, j0 + j), pass));
+                        y0 *= unscale, y1 *= unscale;
+                    }
+                    if (DOWN) {
+                        float* to = sums + (p / a.f.K) * kRows + warp * 32 + lane;
+                        const float f = __ldg(a.f.w + p);
+                        to[0] = fmaf(f, y0, to[0]);
+                        to[128] = fmaf(f, y1, to[128]);
+                    } else if (sums) {
+                        float* to = sums + (j0 + j) * kRows + warp * 32 + lane;
+                        to[0] = pass == 0 ? y0 : to[0] + y0;
+                        to[128] = pass == 0 ? y1 : to[128] + y1;
+                    } else {
+                        if constexpr (NVFP4 && !DOWN) {
+                            if (pass > 0) y0 += earlier[0][j0 + j], y1 += earlier[1][j0 + j];
+                            if (pass + 1 < passes) {
+                                earlier[0][j0 + j] = y0, earlier[1][j0 + j] = y1;
+                                continue;
+                            }
+                        }
+                        store_h<NVFP4>(a.f, p, t.block * 128 + warp * 32 + lane, y0, y1);
+                    }
                 }
             }
         }
@@ -699,6 +880,11 @@ __global__ void __launch_bounds__(kThreadsOf<PER>, 1)
     extern __shared__ uint8_t raw[];
     __shared__ Shared shared;
     Shared* s = &shared;
+    Ranges* ranges = nullptr;
+    if constexpr (NVFP4 && !DOWN) {
+        __shared__ Ranges of_rows;
+        ranges = &of_rows;
+    }
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
     const cg::cluster_group cluster = cg::this_cluster();
@@ -724,8 +910,10 @@ __global__ void __launch_bounds__(kThreadsOf<PER>, 1)
     }
     if (DOWN && warp < 4)
         for (int i = threadIdx.x; i < kRows * a.f.T; i += 128) sums[i] = 0.0f;  // a thread's own two rows
-    if (NVFP4)
-        for (int i = threadIdx.x; i < kKept * (kColumns / 16 * 3); i += kThreads) s->largest[0][i] = 0;
+    if (NVFP4 && threadIdx.x < kKept) s->passes[threadIdx.x] = 0;
+    if (NVFP4 && !DOWN)
+        for (int i = threadIdx.x; i < kKept * (kColumns / 16 * 3); i += kThreads)
+            ranges->largest[0][i] = ranges->least[0][i] = 0;
     // down is released once every block of gate_up has come past its own wait: what came before gate_up is done, and
     // only h, which the converters wait for, is not
     if (!DOWN) {
@@ -747,7 +935,7 @@ __global__ void __launch_bounds__(kThreadsOf<PER>, 1)
     tc_fence_after();
 
     if (warp < 4)
-        result_role<NVFP4, DOWN>(a, s, r, work, a.summed == 0 ? nullptr
+        result_role<NVFP4, DOWN>(a, s, ranges, r, work, a.summed == 0 ? nullptr
                                                 : DOWN      ? sums
                                                             : cluster.map_shared_rank(sums, 0) + rank * a.summed * kRows,
                                  shifts);
@@ -757,7 +945,7 @@ __global__ void __launch_bounds__(kThreadsOf<PER>, 1)
         mma_role<NVFP4, DOWN>(a, s, r, work, slots, warp - kMmaWarp);
     } else {
         if (DOWN) pdl_wait();
-        convert_role<NVFP4, DOWN, PER>(a, s, r, work, slots, warp - kConvertWarp, shifts);
+        convert_role<NVFP4, DOWN, PER>(a, s, ranges, r, work, slots, warp - kConvertWarp, shifts);
     }
     if (DOWN) pdl_wait();  // a block without work does not end before gate_up has either
     __syncwarp();
@@ -837,7 +1025,7 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     constexpr size_t kMost = 226 * 1024;  // dynamic shared memory beside the static part
     auto kern = few_tokens_kernel<NVFP4, DOWN, PER>;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the map needs one
-    const cudaError_t err = allow_shared_memory(kern, kMost - sizeof(Shared));
+    const cudaError_t err = allow_shared_memory(kern, kMost - static_bytes<NVFP4, DOWN>());
     if (err != cudaSuccess) return err;
     const int rows = DOWN ? f.H : f.I, k = DOWN ? f.I : f.H, pairs = f.T * f.K;
     LayerArgs a{f, 0, 0, NVFP4 ? k / 2 : 2 * k, (rows + 127) / 128, k, 0};
@@ -860,8 +1048,8 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
     if (DOWN) a.summed = f.T;
     else if (ranks > 1) a.summed = task_pairs;
     const size_t fixed =
-        1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + pairs;
-    a.stages = int(std::min<size_t>(max_stages(NVFP4), (kMost - sizeof(Shared) - fixed) / S::kSlot));
+        1024 + sizeof(float) * kRows * a.summed * (DOWN ? 1 : ranks) + routing_bytes(pairs) + 2 * pairs;
+    a.stages = int(std::min<size_t>(max_stages(NVFP4), (kMost - static_bytes<NVFP4, DOWN>() - fixed) / S::kSlot));
 
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreadsOf<PER>);
@@ -886,7 +1074,7 @@ cudaError_t launch_half(const LaunchCtx& ctx, const FewTokens& f) {
 }  // namespace
 
 size_t few_tokens_workspace(int64_t T, int K, int, int I, int) {
-    return size_t(T) * K * (size_t(I) + h_parts(I)) * sizeof(float);
+    return size_t(T) * K * (size_t(I) * sizeof(float) + h_parts(I) * sizeof(uint16_t));
 }
 
 template <bool NVFP4, int PER>
