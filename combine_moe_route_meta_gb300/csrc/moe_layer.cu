@@ -14,10 +14,11 @@
 // are added in fp32 with the weights 8^-i.
 // s is one for a column's whole length, since the products add up along it. It brings the row's largest value to [2^8, 2^9),
 // in the range of e4m3 scales. Five terms are enough while the row's values lie near one another: a block whose largest is
-// 13 binary orders below the row's still keeps normal scales for its last terms, and what a large value leaves, 2^-18 of it,
-// is little against its neighbours. A row in which the largest of some four neighbours lies lower (by an outlier, say) is
-// multiplied in several passes, one for each 13 orders: a pass takes what the passes before it left, 2^13 times larger, in
-// five terms again, and the results of all are added. Where no row of a task is like that, one pass does.
+// 11 binary orders below the row's still has normal scales for its last terms, and what a large value leaves, 2^-18 of it,
+// is little against its neighbours. A row with some eight (h: sixteen) neighbours that lie lower, by an outlier, say, is
+// multiplied in several passes: each takes what the passes before it left, 2^13 times larger, in five terms again, and the
+// results of all are added. Where no row of a task is like that, one pass does. (Four neighbours of h would be as low by
+// chance where gates are large, with silu(gate) about 0 for half of them: with gates of N(0, 50) for every row.)
 // With bf16 weights x is a column as it is, and h the sum of two bf16 columns (16 bits).
 //
 // Both kernels list the routed experts and their pairs (route()) and then work in roles:
@@ -66,7 +67,8 @@ constexpr int kRows = 256;                    // weight rows of a slot: two tile
 constexpr int kColumns = 64;                  // columns of a group of pairs
 constexpr int kTerms = 5;                     // columns of a pair, NVFP4
 constexpr int kMaxStages = 5;
-constexpr int kOrders = 13;                   // binary orders of a pass: what five terms take off the largest value of a block
+constexpr int kOrders = 13;                   // binary orders that five terms take off the largest value of a block at least
+constexpr int kSpread = 11;                   // binary orders below the row's largest at which a row makes do with one pass
 constexpr int kKept = 32;                     // tasks whose columns' magnitudes and passes are kept
 constexpr int kMaxRanks = 8;
 constexpr uint32_t kTmemScales = 4 * kColumns;  // after two accumulators of two tiles
@@ -98,7 +100,7 @@ struct LayerArgs {
 };
 
 // Workspace: h as fp32 [pairs][I] and for each 32 of it [pairs][4 ceil(I/128)] two bytes, the exponents of the largest
-// magnitude (high) and of the least largest of four neighbours that is not zero, or 255 (NVFP4); or two bf16 parts
+// magnitude (high) and of the least largest of 16 neighbours that is not zero, or 255 (NVFP4); or two bf16 parts
 // [pairs][2][I].
 __device__ __forceinline__ float* h_values(const FewTokens& a) { return static_cast<float*>(a.workspace); }
 __host__ __device__ __forceinline__ int h_parts(int I) { return (I + 127) / 128 * 4; }
@@ -210,7 +212,7 @@ struct Shared {
 };
 
 // gate_up with NVFP4: exponents of the largest magnitude of x for the pairs of a task, and 255 minus those of the least largest
-// of four that is not zero. (down has shifts and passes of all its pairs at once.)
+// of eight that is not zero. (down has shifts and passes of all its pairs at once.)
 struct Ranges {
     int largest[kKept][kColumns / 16 * 3], least[kKept][kColumns / 16 * 3];
 };
@@ -398,7 +400,9 @@ __device__ __forceinline__ int shift_of(int exponent) { return min(8 + 127 - exp
 // That of a pass.
 __device__ __forceinline__ int pass_shift(int shift, int pass) { return min(shift + kOrders * pass, kMostShift); }
 // The passes after the first that a row with shift `shift` needs, by the exponent of the least magnitude that counts.
-__device__ __forceinline__ int more_passes(int shift, int exponent) { return max(8 + 127 - shift - exponent - 1, 0) / kOrders; }
+__device__ __forceinline__ int more_passes(int shift, int exponent) {
+    return max(8 + 127 - shift - exponent - kSpread + kOrders - 1, 0) / kOrders;
+}
 // A pass that comes before any that finds something of a block with this largest magnitude: the last term's scale is 0 where
 // the block's largest is 2^-20 or less in the pass. (In the first pass it may be too small for binary32.)
 __device__ __forceinline__ int first_pass(int shift, float block) {
@@ -422,9 +426,11 @@ __device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
     asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// The largest magnitudes of eight bf16 values by fours.
-__device__ __forceinline__ uint32_t largest_by_fours(const uint4& w) {
-    return max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+// The largest magnitude of eight bf16 values, twice.
+__device__ __forceinline__ uint32_t largest_of(const uint4& w) {
+    const uint32_t m =
+        max_bf16x2(max_bf16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), max_bf16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    return max_bf16x2(m, __byte_perm(m, m, 0x1032));
 }
 
 // Byte offset of 16-byte piece `piece` of row `row` in the 128-byte swizzle.
@@ -529,8 +535,7 @@ struct Sixteen {
                                    fmaxf(fabsf(__uint_as_float(w[l].z)), fabsf(__uint_as_float(w[l].w)))));
             return m;
         } else {
-            const uint32_t m = max_bf16x2(largest_by_fours(w[0]), largest_by_fours(w[1]));
-            return fmaxf(bf16_lo(m), bf16_hi(m));
+            return bf16_hi(max_bf16x2(largest_of(w[0]), largest_of(w[1])));
         }
     }
     __device__ __forceinline__ void scaled(float scale, uint64_t (&f)[8]) const {
@@ -673,7 +678,7 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, Rang
             // every warp looks at its part of the rows
             for (int j = 0; j < t.n; j++) {
                 const uint16_t* x = a.f.x + int64_t(list[j] / a.f.K) * a.k;
-                uint32_t most = 0, least = ~0u;  // two bf16 magnitudes; least: of those that are not zero, minus one
+                uint32_t most = 0, least = ~0u;  // a bf16 magnitude, twice; least: of those that are not zero, minus one
                 for (int k0 = (v * 32 + lane) * 8; k0 < a.k; k0 += 4 * PER * turns * 256) {
                     uint4 w[4];
 #pragma unroll
@@ -683,16 +688,14 @@ __device__ __forceinline__ void convert_role(const LayerArgs& a, Shared* s, Rang
                     }
 #pragma unroll
                     for (int u = 0; u < 4; u++) {
-                        const uint32_t m = largest_by_fours(w[u]);
-                        most = max_bf16x2(most, m);
-                        least = min_u16x2(least, ((m | 0x80008000u) - 0x00010001u) ^ 0x80008000u);  // 0 -> 0xffff
+                        const uint32_t m = largest_of(w[u]);
+                        most = max(most, m), least = min(least, m - 1);
                     }
                 }
-                const uint32_t high = __reduce_max_sync(kFullMask, max(most & 0xffffu, most >> 16));
-                const uint32_t low = __reduce_min_sync(kFullMask, min(least & 0xffffu, least >> 16));
+                most = __reduce_max_sync(kFullMask, most), least = __reduce_min_sync(kFullMask, least);
                 if (lane == 0) {
-                    atomicMax(largest + j, int(high >> 7));
-                    if (low != 0xffffu) atomicMax(lowest + j, 255 - int((low + 1) >> 7));
+                    atomicMax(largest + j, int(most >> 23));
+                    if (least != ~0u) atomicMax(lowest + j, 255 - int((least + 1) >> 23));
                 }
             }
             // long done with: a converter is at most 8 tasks ahead of what turns accumulators into results
@@ -793,8 +796,9 @@ __device__ __forceinline__ void store_h(const FewTokens& f, int p, int row, floa
     const float h = row < f.I ? swiglu(gate, up) : 0.0f;
     if (NVFP4) {
         if (row < f.I) h_values(f)[int64_t(p) * f.I + row] = h;
-        float m = fmaxf(fabsf(h), __shfl_xor_sync(kFullMask, fabsf(h), 1));
-        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 2));
+        float m = fabsf(h);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
         const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(m));
         const uint32_t least = __reduce_min_sync(kFullMask, __float_as_uint(m) - 1);
         if (row % 32 == 0)

@@ -131,10 +131,10 @@ size_t moe_layer_workspace_size(int64_t num_tokens, int topk, int hidden, int in
  * moe_expert_gemm quantises x and h to NVFP4). With bf16 weights x enters as it is and h as the sum
  * of two bf16 values. With NVFP4 weights each block of 16 of x and of h enters as the sum of five
  * NVFP4 blocks, which leaves at most 2^-12 of the block's largest magnitude, typically 2^-18. A row
- * of x or h in which the largest of some four neighbours (and not all are 0) lies more than 13
- * binary orders below the row's largest enters as five such blocks for each 13 orders, each five
- * leaving that much of what the five before left: it keeps the values beside an outlier, and costs
- * its experts a reading of their weights for each. fp32 sums in an order that depends on the
+ * of x (of h) in which the largest of some eight (sixteen) neighbours, not all 0, lies more than 11
+ * binary orders below the row's largest enters as five more such blocks for each 13 orders, each
+ * five leaving that much of what the five before left: it keeps the values beside an outlier, and
+ * costs its experts a reading of their weights for each. fp32 sums in an order that depends on the
  * arguments alone. A token without a valid slot gets zeros; a slot that names an expert twice counts
  * twice. Ids outside [-1, E) are skipped and reported as MOE_ERR_BAD_EXPERT_ID.
  * A token with infinities or NaNs gets unspecified values and leaves the other tokens' as they are.

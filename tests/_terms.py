@@ -6,21 +6,22 @@ import oracle
 from _experts import E2M1, E4M3, interleave, silu
 from workloads import bf16_bits_to_f32, f32_to_bf16_bits
 
-ORDERS = 13   # binary orders of a pass
+ORDERS, SPREAD = 13, 11   # binary orders of a further pass, and of the first
 
 
 def split(x, terms=5):
     """The sums of NVFP4 blocks for each 16 values of the rows x [R, K] (binary32): `terms` a pass, with the row's largest at
-    [2^8, 2^9) in the first and 2^13 times what is left in each further one; as many passes as 13 binary orders lie between
-    the row's largest and the least largest of four neighbours that is not zero."""
+    [2^8, 2^9) in the first and 2^13 times what is left in each further one, of which there is one for each 13 binary orders
+    after the first 11 between the row's largest and the least largest of eight neighbours that is not zero."""
     x = np.asarray(x, np.float64)
     R = len(x)
     exponent = lambda v: np.frexp(v)[1] - 1  # noqa: E731
     top = np.abs(x).max(1)
-    fours = np.abs(x).reshape(R, -1, 4).max(2)
-    least = np.where(fours > 0, fours, np.inf).min(1)
+    eights = np.abs(x).reshape(R, -1, 8).max(2)
+    least = np.where(eights > 0, eights, np.inf).min(1)
     row = exponent(np.where(top > 0, top, 256.0))
-    passes = 1 + np.maximum(row - exponent(np.where(np.isfinite(least), least, top)) - 1, 0) // ORDERS
+    below = row - exponent(np.where(np.isfinite(least), least, top))
+    passes = 1 + np.maximum(below - SPREAD + ORDERS - 1, 0) // ORDERS
     left = np.ldexp(x, (8 - row)[:, None]).reshape(R, -1, 16)
     total = np.zeros_like(left)
     for p in range(passes.max()):

@@ -23,7 +23,7 @@ def test_five_terms_leave_at_most_2_to_the_minus_12_of_a_block(below):
 @pytest.mark.parametrize("below", [11, 14, 17, 20, 30, 60])
 def test_the_neighbours_of_an_outlier_keep_their_values(below):
     """In the block of an outlier 2^below times its neighbours: 2^-18 of the outlier is left by a pass, 2^-36 by two, and so
-    on, and rows of more than 13 orders have another pass: about 2^-5 of the neighbours is left at the most."""
+    on, and rows of more than 11 orders have another pass: less than 2^-5 of the neighbours is left."""
     rng = np.random.default_rng(below)
     x = rng.standard_normal((400, 64)).astype(np.float32)
     x[:, 21] = 2.0 ** below
