@@ -17,14 +17,15 @@
 // Why so, and what it measured (one GB300; 6782 GB/s is the copy bandwidth):
 //   256 experts, k 7168 -> 1024 -> 7168 (SwiGLU and the product after it), weights of 3.1 GB
 //     128 tokens top-8, masked:   461 us, 6.8 TB/s: bound by reading the weights once
-//     8192 tokens top-8:          840 to 875 us, 5.1 TB/s and 2.9 TFLOP at 3.4 PFLOP/s, at the power limit
+//     8192 tokens top-8:          840 to 880 us, 5.1 TB/s and 2.9 TFLOP at 3.4 PFLOP/s, at the power limit
 //   128 experts, k 768 -> 4096, 2048 tokens top-8 skewed: 67 us, 5.5 TB/s
 //   16 experts, k 4096 -> 704 -> 4096, 1501 tokens top-4: 46 us
 // With many rows an expert the first product's bound is what an SM takes in from L2: a tile brings 128 + 256 rows of
-// codes for 128 x 256 results, 56 bytes a clock and SM between two tile ends, 15.1 TB/s over a whole launch, while the
-// tensor core is busy for 56 % and DRAM for 62 % of the time. Wider tiles do not fit tensor memory beside the scales;
-// pairs of SMs that share a weight tile were not built (an expert's rows would be rounded up to 256). The second
-// product, with its larger output, is bound by DRAM. One lane elected from a converged warp issues the products:
+// codes for 128 x 256 results, 56 bytes a clock and SM between two tile ends, 15.0 TB/s over a whole launch, while the
+// tensor core is busy for 55 % and DRAM for 61 % of the time. Three ways to take in less were not built: wider tiles (the
+// scales of the four slots fill the half of tensor memory beside the accumulator, but two sets in turn would leave 384
+// columns for it), two products of 128 rows on one slot's weights, and pairs of SMs that share a weight tile (which round
+// an expert's rows up to 256). The second product, with its larger output, is bound by DRAM. One lane elected from a converged warp issues the products:
 // issued by a divergent lane they cost 60 ns each, and the first case above took 608 us.
 #include <cstdint>
 

@@ -19,9 +19,10 @@ struct LaunchCtx {
 };
 
 // Launch `kern` as a programmatic dependent of the previous kernel in the stream: its
-// launch may overlap that kernel's execution, and every kernel of this library executes
+// launch may overlap that kernel's execution, and every kernel that is launched so executes
 // griddepcontrol.wait before its first global-memory access, so it still sees all of the
-// previous kernel's writes.
+// previous kernel's writes. (The few-token layer's kernels have a launch of their own: its second one
+// reads ids, factors and weights before its wait, when the first one's wait is over everywhere.)
 template <typename Kernel, typename... Args>
 cudaError_t launch_pdl(const LaunchCtx& ctx, Kernel kern, dim3 grid, dim3 block, size_t smem, Args... args) {
     cudaLaunchConfig_t cfg = {};

@@ -38,7 +38,7 @@
 //   16 experts of 2112 x 704, top-3, bf16:       61 tokens 39 us (143 MB, 3.7 TB/s)
 // The tensor core takes weights as they are stored, so no instruction is spent on a weight: converting them in
 // registers for mma.sync was bound by those instructions (620 us for the 32 tokens). What is left is the terms of x and
-// h, whose work grows with the pairs of an expert: at four an expert, 64 experts of 4096 x 1024, 32 tokens take 90 us,
+// h, whose work grows with the pairs of an expert: at four an expert, 64 experts of 4096 x 1024, 32 tokens take 91 us,
 // at eight 122 us, the dispatch, products and combine 101 us; MoELayer changes over between them. The small
 // cases are bound by latency: two kernels' starts, the list of pairs, the first weights, h and the sums.
 #include <algorithm>

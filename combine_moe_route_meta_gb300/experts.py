@@ -300,8 +300,8 @@ class MoELayer:
     |x| to expect) and ``inter_scale`` (the same of the SwiGLU outputs). Without these scales, or with bf16
     weights, the layer serves few tokens only. ``few_tokens`` defaults to four pairs an expert, about where the
     two ways take the same time: between three pairs (128 experts of 2048 x 768, top-8, 48 tokens: 82 us against
-    81) and eight (16 experts of 4096 x 1024, top-2, 64 tokens: 49 against 47); 64 experts of 4096 x 1024, top-8
-    take 42 us against 60 with 4 tokens, 90 against 101 with 32 and 122 against 102 with 64. No call allocates, so
+    82) and eight (16 experts of 4096 x 1024, top-2, 64 tokens: 49 against 47); 64 experts of 4096 x 1024, top-8
+    take 43 us against 60 with 4 tokens, 91 against 101 with 32 and 122 against 102 with 64. No call allocates, so
     a call of a fixed size can be captured in a CUDA graph. All calls share the layer's buffers: one at a time.
     """
 

@@ -12,7 +12,9 @@
  * The dispatcher pages stop at the experts: FlashinferDispatcher.dispatch ("sglang
  * token_dispatcher/flashinfer.py" page) hands NVFP4 codes and interleaved block scales, and
  * low_latency_dispatch ("sglang token_dispatcher/deepep.py" page) a masked layout, to a MoE GEMM
- * that they do not show. These calls are that consumer; they have no counterpart on the pages.
+ * that they do not show. These calls are that consumer for NVFP4 rows in the contiguous and masked
+ * layouts of moe_dispatch(_ex); the one-row-per-partition layout of moe_dispatch_partitioned(_ex)
+ * is not read by them. They have no counterpart on the pages.
  *
  * Conventions (device pointers, stream order, no allocation, status codes, first error wins in
  * *dev_status) are those of moe_dispatch.h. NVFP4 matrices hold value(code) * value(scale): codes
