@@ -111,7 +111,7 @@ def _rows(mode: str, a_codes: torch.Tensor, K: int, E: int, M: int, seg_indptr) 
         return E * M
     if seg_indptr is None:
         raise ValueError("seg_indptr: needed in normal mode")
-    return a_codes.numel() // a_codes.shape[-1]
+    return a_codes.shape[:-1].numel()
 
 
 def moe_expert_gemm(mode: str, a_codes: torch.Tensor, a_scales: torch.Tensor, masked_m: torch.Tensor,
