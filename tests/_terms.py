@@ -100,6 +100,6 @@ class Differences:
     # at worst 2^-12 of the block's largest for each of two, and of two of h
     MOST = (2.0 ** -11 + 2.0 ** -17, 2.0 ** -10 + 2.0 ** -17)
 
-    def judge(self, out):
+    def holds(self, out):
         rms, most = self.errors(out)
         return all(r <= lim for r, lim in zip(rms, self.RMS)) and all(r <= lim for r, lim in zip(most, self.MOST))

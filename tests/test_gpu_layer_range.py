@@ -158,7 +158,7 @@ def test_differences_of_neighbours():
     T = len(d.x)
     out = _run(_bf16(d.x), np.zeros((T, 1), np.int32), np.ones((T, 1), np.float32), w13, s13, one, d.codes(d.down)[None],
                d.scales(d.down)[None], one)
-    assert d.judge(out), d.errors(out)
+    assert d.holds(out), d.errors(out)
 
 
 def test_wide_rows_leave_the_others_alone():

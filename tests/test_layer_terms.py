@@ -34,8 +34,8 @@ def test_the_neighbours_of_an_outlier_keep_their_values(below):
 
 def test_the_differences_tell_five_terms_from_four():
     d = Differences()
-    assert d.judge(d.output(5)), d.errors(d.output(5))
-    assert not d.judge(d.output(4)), d.errors(d.output(4))
+    assert d.holds(d.output(5)), d.errors(d.output(5))
+    assert not d.holds(d.output(4)), d.errors(d.output(4))
     rms, _ = d.errors(d.output(4))
     assert all(r > 2 * lim for r, lim in zip(rms, d.RMS))
 
@@ -47,4 +47,4 @@ def test_a_lost_fifth_term_of_h_alone_is_told():
     from workloads import bf16_bits_to_f32, f32_to_bf16_bits
     h = ((x @ d.up.T) * silu(x @ d.gate.T)).astype(np.float32)
     out = bf16_bits_to_f32(f32_to_bf16_bits((split(h, 4) @ d.down.T).astype(np.float32))).astype(np.float64)
-    assert not d.judge(out), d.errors(out)
+    assert not d.holds(out), d.errors(out)
