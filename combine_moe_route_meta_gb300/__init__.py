@@ -11,7 +11,8 @@ like the dispatcher pages' outputs (``DeepEPNormalDispatchOutput`` /
 ``DeepEPLLDispatchOutput`` on the "sglang token_dispatcher/deepep.py" page).
 
 The expert operators between dispatch and combine (``include/moe_experts.h``) are bound in
-:mod:`.experts` and reachable from here.
+:mod:`.experts`, those of a block in bf16, with their gradients, and the norm before it
+(``include/moe_block.h``) in :mod:`.block`; all are reachable from here.
 
 There is no CPU fallback: the first call raises when the library has not been built
 (``python -m combine_moe_route_meta_gb300.build``), and every call requires CUDA tensors.
@@ -93,6 +94,15 @@ _SIGNATURES = {
     "moe_layer_workspace_size": (_sz, [_i64, _int, _int, _int, _int]),
     "moe_layer_few_tokens": (_int, [_P, _i64, _int, _int, _P, _P, _int, _int, _int, _P, _P, _P, _P, _P, _P, _P, _P,
                                     _sz, _P, _P]),
+    # include/moe_block.h
+    "moe_expert_gemm_bf16": (_int, [_int, _P, _int, _int, _i64, _int, _int, _P, _P, _int, _P, _P, _P, _P]),
+    "moe_expert_gemm_swiglu_bf16": (_int, [_int, _P, _int, _int, _i64, _int, _int, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_gemm_dswiglu_bf16": (_int, [_int, _P, _int, _int, _i64, _int, _int, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_wgrad_bf16": (_int, [_int, _P, _P, _int, _int, _i64, _int, _int, _P, _P, _int, _int, _P, _P, _P]),
+    "moe_combine_backward": (_int, [_int, _P, _P, _i64, _int, _int, _int, _int, _i64, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_rmsnorm": (_int, [_P, _P, _P, _f32, _i64, _int, _int, _P, _P, _P, _P, _P, _P]),
+    "moe_rmsnorm_backward_workspace_size": (_sz, [_i64, _int]),
+    "moe_rmsnorm_backward": (_int, [_P, _P, _P, _P, _P, _i64, _int, _P, _P, _P, _sz, _P]),
 }
 _lib_handle = None
 
@@ -700,3 +710,4 @@ class MoEDispatcher:
 
 
 from .experts import *  # noqa: E402,F401,F403  (uses the names above)
+from .block import *  # noqa: E402,F401,F403

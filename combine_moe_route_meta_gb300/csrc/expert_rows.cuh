@@ -1,6 +1,7 @@
 // expert_rows.cuh -- device helpers shared by the expert operators.
 #pragma once
 
+#include "block_launch.h"
 #include "dispatch_slice.cuh"
 #include "experts_launch.h"
 #include "moe_device.cuh"
@@ -36,7 +37,7 @@ struct RowSpan {
     int64_t base;
     int count;
 };
-__device__ __forceinline__ RowSpan expert_rows(const ExpertGemm& a, int e) {
+__device__ __forceinline__ RowSpan expert_rows(const RowLayout& a, int e) {
     const int64_t base = a.M > 0 ? int64_t(e) * a.M : __ldg(a.seg + e);
     int64_t count = __ldg(a.count + e);
     if (count < 0 || base < 0) {
@@ -49,6 +50,9 @@ __device__ __forceinline__ RowSpan expert_rows(const ExpertGemm& a, int e) {
         count = most;
     }
     return RowSpan{base, int(count)};
+}
+__device__ __forceinline__ RowSpan expert_rows(const ExpertGemm& a, int e) {
+    return expert_rows(RowLayout{a.E, a.M, a.rows, a.seg, a.count, a.status}, e);
 }
 
 // Byte offset of the scale of block c of row r of an activation matrix with C blocks a row.
@@ -72,6 +76,29 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, c, 1.0f)));
     // e by itself: a subnormal e is not rounded twice, nor its small product with gate
     return g < 0.0f ? (up * e) * (g * r * c) : up * (g * r);
+}
+
+// p = 1 / (1 + exp(-g)) and q = 1 - p, each to 2^-20 (2^-19 where exp(-|g|) is subnormal): by e = exp(-|g|), made as in
+// swiglu(), one is 1 / (1 + e) and the other e / (1 + e), so neither is a difference.
+__device__ __forceinline__ void sigmoids(float g, float* p, float* q) {
+    constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float a = fminf(fabsf(g), 110.0f);
+    const float t = -a * kLog2e;
+    const float c = fmaf(fmaf(-a, kLog2e, -t) - a * kRest, kLn2, 1.0f);
+    float e, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e *= c;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
+    *p = g < 0.0f ? e * r : r;
+    *q = g < 0.0f ? r : e * r;
+}
+// The gradients of h = up * silu(gate) with respect to gate and up, times dh. Factors near the ends of the range are
+// multiplied by the small ones first: dh * up alone could overflow where the result does not.
+__device__ __forceinline__ void dswiglu(float gate, float up, float dh, float* dgate, float* dup) {
+    float p, q;
+    sigmoids(gate, &p, &q);
+    *dgate = (dh * p) * (up * fmaf(gate, q, 1.0f));
+    *dup = (dh * p) * gate;
 }
 
 }  // namespace moe

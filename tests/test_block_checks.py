@@ -1,0 +1,222 @@
+"""A MoE block's bf16 operators refuse bad arguments on the host: the C entry points by their status, the binding before
+any launch. CPU only: no call gets as far as a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import combine_moe_route_meta_gb300 as moe
+
+P = ctypes.c_void_p
+FAKE, ODD, TWO = P(0x1000), P(0x1008), P(0x1002)    # never dereferenced: validation fails first
+INVALID, UNSUPPORTED = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
+
+
+def _gemm(op, **kw):
+    a = dict(mode=1, a=FAKE, E=4, M=8, rows=0, n=64, k=128, seg=None, count=FAKE, weights=0, w=FAKE, out=FAKE, gu=FAKE,
+             st=FAKE)
+    a.update(kw)
+    lib = moe.load_library()
+    head = (a["mode"], a["a"], a["E"], a["M"], a["rows"], a["n"], a["k"], a["seg"], a["count"])
+    if op == "plain":
+        return lib.moe_expert_gemm_bf16(*head, a["weights"], a["w"], a["out"], a["st"], None)
+    if op == "swiglu":
+        return lib.moe_expert_gemm_swiglu_bf16(*head, a["w"], a["out"], a["gu"], a["st"], None)
+    return lib.moe_expert_gemm_dswiglu_bf16(*head, a["w"], a["gu"], a["out"], a["st"], None)
+
+
+@pytest.mark.parametrize("op", ["plain", "swiglu", "dswiglu"])
+def test_product_arguments(op):
+    for kw in (dict(mode=2), dict(E=0), dict(M=0), dict(n=0), dict(n=-8), dict(n=12), dict(k=0), dict(k=4), dict(k=100),
+               dict(count=None), dict(st=None), dict(a=None), dict(w=None), dict(out=None), dict(a=ODD), dict(w=ODD),
+               dict(out=ODD), dict(mode=0, rows=8), dict(mode=0, rows=-1, seg=FAKE), dict(seg=P(0x1004)), dict(count=TWO),
+               dict(st=TWO)):
+        assert _gemm(op, **kw) == INVALID, kw
+    assert _gemm(op, E=1025) == UNSUPPORTED and _gemm(op, M=1 << 30) == UNSUPPORTED
+    assert _gemm(op, mode=0, rows=1 << 31, seg=FAKE) == UNSUPPORTED
+    assert _gemm(op, n=1 << 25) == UNSUPPORTED and _gemm(op, k=1 << 25) == UNSUPPORTED
+    assert _gemm(op, mode=0, rows=(1 << 31) - 1, seg=FAKE, n=1 << 24) == UNSUPPORTED       # tiles beyond 31 bits
+    assert _gemm(op, mode=0, rows=0, seg=FAKE) == 0
+    if op == "plain":
+        assert _gemm(op, weights=2) == INVALID
+    elif op == "swiglu":
+        assert _gemm(op, gu=ODD) == INVALID and _gemm(op, n=1 << 24) == UNSUPPORTED
+    else:
+        assert _gemm(op, gu=None) == INVALID and _gemm(op, gu=ODD) == INVALID
+
+
+def _wgrad(**kw):
+    a = dict(mode=1, a=FAKE, b=FAKE, E=4, M=8, rows=0, m=64, n=128, seg=None, count=FAKE, grad=1, acc=0, out=FAKE, st=FAKE)
+    a.update(kw)
+    return moe.load_library().moe_expert_wgrad_bf16(a["mode"], a["a"], a["b"], a["E"], a["M"], a["rows"], a["m"], a["n"],
+                                                    a["seg"], a["count"], a["grad"], a["acc"], a["out"], a["st"], None)
+
+
+def test_weight_gradient_arguments():
+    for kw in (dict(mode=5), dict(E=0), dict(M=0), dict(m=0), dict(m=4), dict(n=0), dict(n=129), dict(count=None),
+               dict(st=None), dict(a=None), dict(b=None), dict(out=None), dict(a=ODD), dict(b=ODD), dict(out=ODD),
+               dict(grad=2), dict(acc=2), dict(mode=0, rows=4), dict(mode=0, rows=0, seg=FAKE, out=None), dict(st=TWO)):
+        assert _wgrad(**kw) == INVALID, kw
+    assert _wgrad(E=1025) == UNSUPPORTED and _wgrad(m=1 << 25) == UNSUPPORTED
+    assert _wgrad(m=1 << 24, n=1 << 24) == UNSUPPORTED
+
+
+def _combine(**kw):
+    a = dict(mode=0, g=FAKE, eo=FAKE, T=4, H=64, K=2, E=4, M=8, rows=0, ids=FAKE, s2d=FAKE, seg=FAKE, w=FAKE, ge=FAKE, gw=FAKE,
+             st=FAKE)
+    a.update(kw)
+    return moe.load_library().moe_combine_backward(a["mode"], a["g"], a["eo"], a["T"], a["H"], a["K"], a["E"], a["M"],
+                                                   a["rows"], a["ids"], a["s2d"], a["seg"], a["w"], a["ge"], a["gw"],
+                                                   a["st"], None)
+
+
+def test_combine_gradient_arguments():
+    for kw in (dict(mode=3), dict(T=-1), dict(H=0), dict(H=12), dict(K=0), dict(E=0), dict(mode=1, M=0), dict(rows=7),
+               dict(rows=-1), dict(st=None), dict(st=TWO), dict(ge=None, gw=None), dict(g=None), dict(eo=None), dict(s2d=None),
+               dict(w=None), dict(mode=1, ids=None), dict(mode=1, seg=None), dict(g=ODD), dict(eo=ODD), dict(ge=ODD),
+               dict(gw=TWO), dict(w=TWO), dict(s2d=TWO), dict(ids=TWO), dict(seg=P(0x1004))):
+        assert _combine(**kw) == INVALID, kw
+    assert _combine(K=17) == UNSUPPORTED and _combine(E=1025) == UNSUPPORTED and _combine(T=1 << 31) == UNSUPPORTED
+    assert _combine(T=0) == 0 and _combine(T=0, g=None, eo=None, s2d=None, w=None) == 0
+
+
+def _norm(**kw):
+    a = dict(x=FAKE, res=FAKE, w=FAKE, eps=1e-6, T=4, H=256, q=1, out=FAKE, c=FAKE, s=FAKE, sum=FAKE, r=FAKE)
+    a.update(kw)
+    return moe.load_library().moe_rmsnorm(a["x"], a["res"], a["w"], a["eps"], a["T"], a["H"], a["q"], a["out"], a["c"], a["s"],
+                                          a["sum"], a["r"], None)
+
+
+def _norm_grad(**kw):
+    a = dict(g=FAKE, s=FAKE, w=FAKE, r=FAKE, gs=None, T=4, H=256, gx=FAKE, gw=FAKE, ws=FAKE, n=1 << 30)
+    a.update(kw)
+    return moe.load_library().moe_rmsnorm_backward(a["g"], a["s"], a["w"], a["r"], a["gs"], a["T"], a["H"], a["gx"], a["gw"],
+                                                   a["ws"], a["n"], None)
+
+
+def test_norm_arguments():
+    for kw in (dict(T=-1), dict(H=0), dict(H=12), dict(H=136), dict(q=2), dict(q=4), dict(q=9), dict(eps=0.0), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(w=None), dict(c=None), dict(s=None),
+               dict(q=0, out=None), dict(x=ODD), dict(res=ODD), dict(w=ODD), dict(out=ODD), dict(c=ODD), dict(sum=ODD),
+               dict(r=TWO), dict(s=TWO)):
+        assert _norm(**kw) == INVALID, kw
+    assert _norm(H=32896) == UNSUPPORTED and _norm(T=1 << 31) == UNSUPPORTED
+    assert _norm(T=0) == 0
+
+
+def test_norm_gradient_arguments():
+    for kw in (dict(T=-1), dict(H=12), dict(g=None), dict(s=None), dict(w=None), dict(r=None), dict(gx=None), dict(gw=None),
+               dict(ws=None), dict(n=moe.moe_rmsnorm_backward_workspace_size(4, 256) - 1), dict(g=ODD), dict(s=ODD), dict(w=ODD), dict(r=TWO), dict(gs=ODD),
+               dict(gx=ODD), dict(gw=ODD), dict(ws=ODD)):
+        assert _norm_grad(**kw) == INVALID, kw
+    assert _norm_grad(H=32776) == UNSUPPORTED
+    assert moe.moe_rmsnorm_backward_workspace_size(4, 12) == 0 and moe.moe_rmsnorm_backward_workspace_size(-1, 8) == 0
+    assert moe.moe_rmsnorm_backward_workspace_size(0, 8) == 0
+    assert moe.moe_rmsnorm_backward_workspace_size(4, 4096) >= 4096 * 4
+
+
+def _operands():
+    bf = dict(dtype=torch.bfloat16)
+    return dict(a=torch.zeros((4, 8, 128), **bf), count=torch.zeros(4, dtype=torch.int32), w=torch.zeros((4, 64, 128), **bf),
+                out=torch.zeros((4, 8, 64), **bf), st=torch.zeros(1, dtype=torch.int32), gu=torch.zeros((4, 8, 128), **bf))
+
+
+def test_binding_checks_products():
+    def plain(mode="masked", seg=None, M=8, transposed=False, **bad):
+        o = _operands() | bad
+        moe.moe_expert_gemm_bf16(mode, o["a"], o["count"], o["w"], o["out"], o["st"], transposed=transposed, seg_indptr=seg,
+                                 max_tokens_per_expert=M)
+
+    def swiglu(**bad):
+        o = _operands() | dict(w=torch.zeros((4, 128, 128), dtype=torch.bfloat16)) | bad
+        moe.moe_expert_gemm_swiglu_bf16("masked", o["a"], o["count"], o["w"], o["out"], o["st"], o["gu"],
+                                        max_tokens_per_expert=8)
+
+    def dswiglu(**bad):
+        o = _operands() | dict(w=torch.zeros((4, 128, 64), dtype=torch.bfloat16),
+                               out=torch.zeros((4, 8, 128), dtype=torch.bfloat16)) | bad
+        moe.moe_expert_gemm_dswiglu_bf16("masked", o["a"], o["count"], o["w"], o["gu"], o["out"], o["st"],
+                                         max_tokens_per_expert=8)
+
+    o = _operands()
+    for f in (plain, swiglu, dswiglu):
+        for bad in (dict(a=o["a"][:3]), dict(a=o["a"].half()), dict(a=o["a"][..., :64]), dict(count=o["count"][1:]),
+                    dict(count=o["count"].long()), dict(w=o["w"].float()), dict(out=o["out"][1:]), dict(out=o["out"].half()),
+                    dict(st=o["st"].float())):
+            with pytest.raises(ValueError):
+                f(**bad)
+        with pytest.raises(ValueError, match="no CPU path"):
+            f()
+    for bad in (dict(M=9), dict(mode="normal"), dict(mode="both"), dict(mode="normal", seg=torch.zeros(4, dtype=torch.int64)),
+                dict(transposed=True)):
+        with pytest.raises(ValueError):
+            plain(**bad)
+    for bad in (dict(gu=o["gu"][1:]), dict(w=torch.zeros((4, 127, 128), dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            swiglu(**bad)
+    with pytest.raises(ValueError):
+        dswiglu(gu=o["gu"][1:])
+
+
+def test_binding_checks_weight_gradient():
+    o = _operands()
+
+    def call(**bad):
+        v = o | dict(b=o["gu"], out=torch.zeros(4, 128, 128)) | bad
+        moe.moe_expert_wgrad_bf16("masked", v["a"], v["b"], v["count"], v["out"], v["st"], max_tokens_per_expert=8)
+
+    for bad in (dict(a=o["a"][:, :7]), dict(b=o["a"].float()), dict(b=o["out"]), dict(out=torch.zeros(4, 64, 128)),
+                dict(out=torch.zeros(4, 128, 128).double()), dict(out=torch.zeros(5, 128, 128)), dict(st=o["st"].long())):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(ValueError, match="no CPU path"):
+        call()
+    with pytest.raises(ValueError, match="rows"):
+        moe.moe_expert_wgrad_bf16("normal", torch.zeros(8, 128).bfloat16(), torch.zeros(9, 128).bfloat16(), o["count"],
+                                  torch.zeros(4, 128, 128), o["st"], seg_indptr=torch.zeros(5, dtype=torch.int64))
+
+
+def test_binding_checks_combine_gradient():
+    T, K, H, E = 3, 2, 64, 4
+    good = dict(g=torch.zeros(T, H).bfloat16(), eo=torch.zeros(6, H).bfloat16(), ids=torch.zeros(T, K, dtype=torch.int32),
+                w=torch.zeros(T, K), s2d=torch.zeros(6, dtype=torch.int32), seg=torch.zeros(E + 1, dtype=torch.int64),
+                ge=torch.zeros(6, H).bfloat16(), gw=torch.zeros(T, K), st=torch.zeros(1, dtype=torch.int32))
+
+    def call(mode="normal", rows=6, M=0, **bad):
+        v = good | bad
+        moe.moe_combine_backward(mode, v["g"], v["eo"], v["ids"], v["w"], E, v["s2d"], v["seg"], v["ge"], v["gw"], v["st"],
+                                 max_tokens_per_expert=M, expert_out_rows=rows)
+
+    for bad in (dict(g=good["g"][1:]), dict(g=good["g"].float()), dict(eo=good["eo"][1:]), dict(eo=None),
+                dict(ids=good["ids"].long()), dict(w=good["w"][1:]), dict(s2d=good["s2d"][1:]), dict(ge=good["ge"][1:]),
+                dict(gw=good["gw"].double()), dict(st=good["st"].float()), dict(mode="masked", M=2), dict(mode="x"),
+                dict(mode="masked", M=1, seg=good["seg"][1:])):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(ValueError, match="no CPU path"):
+        call()
+
+
+def test_binding_checks_norm():
+    T, H = 3, 256
+    x, w = torch.zeros(T, H).bfloat16(), torch.zeros(H).bfloat16()
+    for kw in (dict(x=x.float()), dict(w=w[1:]), dict(residual=x[1:]), dict(quant="fp4"), dict(quant="nvfp4b16")):
+        a = dict(x=x, w=w) | kw
+        with pytest.raises(ValueError):
+            moe.rmsnorm(a.pop("x"), a.pop("w"), **a)
+    codes, scales = torch.zeros(T, H, dtype=torch.uint8), torch.zeros(T, 2)
+    for kw in (dict(codes=codes[1:]), dict(scales=scales[1:]), dict(scales=scales.double()), dict(sum=x[1:]),
+               dict(rstd=torch.zeros(2)), dict(out=x[1:])):
+        a = dict(codes=codes, scales=scales) | kw
+        with pytest.raises(ValueError):
+            moe.moe_rmsnorm(x, w, 1e-6, a.pop("out", None), quant="fp8g128", **a)
+    with pytest.raises(ValueError, match="no CPU path"):
+        moe.moe_rmsnorm(x, w, 1e-6, x)
+    r, ws = torch.zeros(T), torch.zeros(1 << 16, dtype=torch.uint8)
+    for kw in (dict(g=x[1:]), dict(s=x.half()), dict(w=w[1:]), dict(r=r[1:]), dict(gx=x[1:]), dict(gw=torch.zeros(H - 1)),
+               dict(gs=x[1:])):
+        a = dict(g=x, s=x, w=w, r=r, gx=x, gw=torch.zeros(H), gs=None) | kw
+        with pytest.raises(ValueError):
+            moe.moe_rmsnorm_backward(a["g"], a["s"], a["w"], a["r"], a["gx"], a["gw"], ws, a["gs"])
+    with pytest.raises(ValueError, match="no CPU path"):
+        moe.moe_rmsnorm_backward(x, x, w, r, x, torch.zeros(H), ws)
