@@ -4,103 +4,271 @@
 //   SwiGLU    h = up * silu(gate) of two such products
 //   dSwiGLU   the gradient of gate and up from such a product
 //
-// One block takes 64 rows x 64 columns of one expert; a thread 4 x 4 of them, in fp32.
+// Persistent pairs of SMs, each walking over tiles of 256 columns x up to 256 rows of one expert. The weights are the M
+// side of the products, 128 columns in each block (SwiGLU: 64 gate columns and the 64 up columns beside them), and the
+// rows the N side, half of them in each block: N follows the expert's rows in steps of 32, so that few rows, or a few more
+// than a tile, cost little more than they are. Warps have roles:
+//   0      issues the loads of a ring of slots of 64 values of k, by tensor maps in the 128-byte swizzle (out-of-range
+//          rows, columns and k read as zero); weights [E, k, n] are read as they lie and multiplied along their columns
+//   1      of the leading block issues the products of both
+//   4..11  take the accumulator (columns are its lanes) through shared memory to rows, and finish these
+// Tiles run with the row tiles of one column block next to each other, so a weight tile comes from DRAM once. Two
+// accumulators: the next tile's products run beside the epilogue. Every wait is bounded (MOE_ERR_TIMEOUT).
 #include <cstdint>
 
-#include "block_launch.h"
-#include "expert_rows.cuh"
+#include "expert_pair.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kMaxRows = 256;  // of a tile
+constexpr int kCols = 256;
+constexpr int kChunkRows = 16;                               // rows of the accumulator at a time
+constexpr uint32_t kStaged = kChunkRows * 128 * 4;           // ... of a block's 128 columns in fp32
+constexpr uint32_t kStaging = 2 * 2 * kStaged;               // two groups of four epilogue warps, two buffers each
+static_assert(1024 + kPairStages * kPairSlot + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024,
+              "shared memory of an SM");
 
-struct RowTile {
-    int e, rows;
-    int64_t row0;
+struct GemmArgs {
+    RowGemm g;
+    int chunks;   // slots per tile: ceil(k / kPairK)
+    int tiles_n;  // column tiles
 };
 
-// The block's row tile: number t of all experts', found by one thread. e = -1: there is none.
-__device__ RowTile find_row_tile(const RowLayout& l, int t) {
-    int64_t wide = 0;
-    for (int e = 0; e < l.E; e++) wide += (expert_rows(l, e).count + 255) / 256;
-    if (wide > l.rows / 256 + l.E) {
-        set_status(l.status, MOE_ERR_INVALID_ARG);
-        return RowTile{-1, 0, 0};
+struct Tile {
+    int e, n0, row0, rows;  // expert, first column, first row, rows
+    // N of the products; each block loads half of it, in boxes of 16 rows
+    __device__ __forceinline__ int n() const { return (rows + 31) & ~31; }
+};
+
+template <RowOp OP>
+constexpr int kTileCols = OP == RowOp::kSwiglu ? kCols / 2 : kCols;  // columns of the result in a tile
+
+template <RowOp OP>
+__device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int t) {
+    const int E = a.g.rows.E;
+    const int* prefix = s->prefix();
+    int lo = 0, hi = E;  // prefix[lo] * tiles_n <= t < prefix[hi] * tiles_n
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (int64_t(prefix[mid]) * a.tiles_n <= t)
+            lo = mid;
+        else
+            hi = mid;
     }
-    for (int e = 0; e < l.E; e++) {
-        const RowSpan r = expert_rows(l, e);
-        const int tiles = int((int64_t(r.count) + kTile - 1) / kTile);
-        if (t < tiles) return RowTile{e, min(kTile, r.count - t * kTile), r.base + int64_t(t) * kTile};
-        t -= tiles;
-    }
-    return RowTile{-1, 0, 0};
+    const int rows_t = prefix[lo + 1] - prefix[lo];
+    const int i = int(t - int64_t(prefix[lo]) * a.tiles_n);
+    const int m = i % rows_t;
+    // an expert's rows are shared out evenly among its tiles, in steps of 32
+    const int count = s->count(E)[lo], each = (count + rows_t - 1) / rows_t;
+    const int step = (each + 31) & ~31;
+    const int first = min(m * step, count);
+    return Tile{lo, i / rows_t * kTileCols<OP>, s->base(E)[lo] + first, min(step, count - first)};
 }
 
 template <RowOp OP, bool KN>
-__global__ void __launch_bounds__(kThreads) row_gemm_kernel(RowGemm g) {
-    constexpr int kHalves = OP == RowOp::kSwiglu ? 2 : 1;
-    __shared__ float sa[kStep][kTile + 1], sw[kHalves][kStep][kTile + 1];
-    __shared__ RowTile tile;
-    pdl_wait();
-    if (threadIdx.x == 0) tile = find_row_tile(g.rows, blockIdx.y);
-    __syncthreads();
-    if (tile.e < 0) return;
-    const int n0 = blockIdx.x * kTile, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const uint16_t* w = g.w + int64_t(tile.e) * kHalves * g.n * g.k;
-    float acc[kHalves][4][4] = {};
-    for (int k0 = 0; k0 < g.k; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kStep, k = k0 + i % kStep;
-            sa[i % kStep][r] = r < tile.rows && k < g.k ? bf16_lo(g.a[(tile.row0 + r) * g.k + k]) : 0.0f;
-            for (int h = 0; h < kHalves; h++) {
-                const int kk = KN ? i / kTile : i % kStep, j = KN ? i % kTile : i / kStep;
-                const bool in = k0 + kk < g.k && n0 + j < g.n;
-                const int64_t at = KN ? int64_t(k0 + kk) * g.n + n0 + j : (int64_t(h) * g.n + n0 + j) * g.k + k0 + kk;
-                sw[h][kk][j] = in ? bf16_lo(w[at]) : 0.0f;
+__device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank,
+                                          const CUtensorMap* map_a, const CUtensorMap* map_a128,
+                                          const CUtensorMap* map_w) {
+    const int lane = threadIdx.x % 32, pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
+        const Tile tile = find_tile<OP>(a, s, t);
+        const int half = tile.n() / 2, boxes = half / 16;
+        const int row0 = tile.row0 + rank * half;
+        const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
+        for (int c = 0; c < a.chunks; c++) {
+            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->empty[st]), ph ^ 1)) return;
+            const uint32_t own = smem_addr(&s->full[st]), bar = leaders(own), slot = slots + st * kPairSlot;
+            const int k0 = c * kPairK;
+            if (lane == 0) {
+                if (rank == 0) mbar_expect_tx(own, 2 * (kPairBytes + boxes * 2048));
+                if constexpr (KN) {
+                    pair_load_3d(slot, map_w, n0, k0, tile.e, bar);
+                    pair_load_3d(slot + kPairBytes / 2, map_w, n0 + 64, k0, tile.e, bar);
+                } else {
+                    // (k, column, half, expert); SwiGLU: 64 columns of both halves
+                    pair_load_4d(slot, map_w, k0, n0, 0, tile.e, bar);
+                }
+                if (boxes == 8) pair_load_2d(slot + kPairBytes, map_a128, k0, row0, bar);
             }
+            if (boxes < 8 && lane < boxes)
+                pair_load_2d(slot + kPairBytes + lane * 2048, map_a, k0, row0 + lane * 16, bar);
+            __syncwarp();
+            if (++st == kPairStages) st = 0, ph ^= 1;
         }
-        __syncthreads();
-        for (int k = 0; k < kStep; k++)
-            for (int h = 0; h < kHalves; h++)
-                for (int i = 0; i < 4; i++)
-                    for (int j = 0; j < 4; j++)
-                        acc[h][i][j] = fmaf(sa[k][ty * 4 + i], sw[h][k][tx * 4 + j], acc[h][i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; i++) {
-        const int64_t r = tile.row0 + ty * 4 + i;
-        if (ty * 4 + i >= tile.rows) break;
-        for (int j = 0; j < 4; j++) {
-            const int c = n0 + tx * 4 + j;
-            if (c >= g.n) break;
-            const float v = acc[0][i][j];
-            if constexpr (OP == RowOp::kPlain) {
-                g.out[r * g.n + c] = uint16_t(pack_bf16x2(v, 0.0f));
-            } else if constexpr (OP == RowOp::kSwiglu) {
-                const float up = acc[kHalves - 1][i][j];
-                g.out[r * g.n + c] = uint16_t(pack_bf16x2(swiglu(v, up), 0.0f));
-                if (g.gate_up) {
-                    g.gate_up[r * 2 * g.n + c] = uint16_t(pack_bf16x2(v, 0.0f));
-                    g.gate_up[(r * 2 + 1) * g.n + c] = uint16_t(pack_bf16x2(up, 0.0f));
+    pair_drain(s, a.g.rows.status, st, ph);
+}
+
+// A whole warp of the leading block; one lane issues.
+template <RowOp OP, bool KN>
+__device__ __forceinline__ void mma_role(const GemmArgs& a, PairShared* s, uint32_t slots) {
+    const uint64_t da = KN ? desc_mn128(slots) : desc_k128(slots), db = desc_k128(slots + kPairBytes);
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
+    const int last = (a.g.k - (a.chunks - 1) * kPairK + 15) / 16;  // steps of 16 in the last slot
+    const bool leader = elect_one();
+    int st = 0, n_tile = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
+        const Tile tile = find_tile<OP>(a, s, t);
+        const uint32_t idesc = pair_idesc_bf16(tile.n(), KN, false);
+        const int acc = n_tile & 1;
+        const uint32_t d = s->tmem + acc * kMaxRows;
+        if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
+        tc_fence_after();
+        for (int c = 0; c < a.chunks; c++) {
+            if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t off = st * (kPairSlot / 16);
+                const int steps = c + 1 < a.chunks ? 4 : last;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if (j >= steps) break;
+                    // 16 values of k: 32 bytes further in the rows; or 16 rows of 128 bytes
+                    pair_mma_bf16(d, da + off + (KN ? 128 : 2) * j, db + off + 2 * j, idesc, c > 0 || j > 0);
+                }
+                pair_commit(empty + 8 * st);
+                if (c + 1 == a.chunks) pair_commit(smem_addr(&s->acc_full[acc]));
+            }
+            __syncwarp();
+            if (++st == kPairStages) st = 0, ph ^= 1;
+        }
+    }
+}
+
+__device__ __forceinline__ uint2 pack4(float4 v) { return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)); }
+__device__ __forceinline__ uint2 ld_v2(const void* p) {  // of what may be written in place
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+template <RowOp OP>
+__device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, float* staging, int rank, int warp) {
+    const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
+    const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
+    const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n, n = a.g.n;
+    float* buffers = staging + group * (2 * kStaged / 4);
+    int n_tile = 0, turn = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
+        const Tile tile = find_tile<OP>(a, s, t);
+        const int acc = n_tile & 1;
+        const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
+        if (!group_all(group, pair_wait(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1))) return;
+        tc_fence_after();
+        const uint32_t done = leaders(smem_addr(&s->acc_empty[acc]));
+        if (group * kChunkRows >= tile.rows) {
+            if (lane == 0) mbar_arrive_cluster(done);
+            continue;
+        }
+        for (int j0 = group * kChunkRows; j0 < tile.rows; j0 += 2 * kChunkRows) {
+            uint2 gate[4], up[4];
+            if constexpr (OP == RowOp::kDswiglu) {
+                // gate and up of the rows and columns that this lane will finish, on their way beside the accumulator
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int j = j0 + quad * 4 + i, col = n0 + lane * 4;
+                    if (j >= tile.rows || col >= n) continue;
+                    const uint16_t* p = a.g.gate_up + (int64_t(tile.row0) + j) * 2 * n + col;
+                    gate[i] = ld_v2(p);
+                    up[i] = ld_v2(p + n);
+                }
+            }
+            __syncwarp();
+            float v[16];
+            tmem_load16(tmem + acc * kMaxRows + j0, v);
+            if (j0 + 2 * kChunkRows >= tile.rows) {  // the warp's last of this accumulator
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(done);
+            }
+            float* stage = buffers + (turn ^= 1) * (kStaged / 4);
+#pragma unroll
+            for (int j = 0; j < kChunkRows; j++) stage[j * 128 + quad * 32 + lane] = v[j];
+            // one barrier for two buffers: who writes this one again has passed the next one's barrier, as has who reads it
+            group_sync(group);
+            if constexpr (OP == RowOp::kSwiglu) {
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int j = quad * 4 + i * 2 + lane / 16, c = lane % 16 * 4, col = n0 + c;
+                    if (j0 + j >= tile.rows || col >= n) continue;
+                    const int64_t r = int64_t(tile.row0) + j0 + j;
+                    const float4 g = *reinterpret_cast<const float4*>(stage + j * 128 + c);
+                    const float4 u = *reinterpret_cast<const float4*>(stage + j * 128 + 64 + c);
+                    st_v2(a.g.out + r * n + col, pack4(make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z),
+                                                                   swiglu(g.w, u.w))));
+                    if (a.g.gate_up) {
+                        st_v2(a.g.gate_up + r * 2 * n + col, pack4(g));
+                        st_v2(a.g.gate_up + (r * 2 + 1) * n + col, pack4(u));
+                    }
                 }
             } else {
-                const int64_t at = r * 2 * g.n + c;
-                float dgate, dup;
-                dswiglu(bf16_lo(g.gate_up[at]), bf16_lo(g.gate_up[at + g.n]), v, &dgate, &dup);
-                g.out[at] = uint16_t(pack_bf16x2(dgate, 0.0f));
-                g.out[at + g.n] = uint16_t(pack_bf16x2(dup, 0.0f));
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int j = quad * 4 + i, col = n0 + lane * 4;
+                    if (j0 + j >= tile.rows || col >= n) continue;
+                    const int64_t r = int64_t(tile.row0) + j0 + j;
+                    const float4 x = *reinterpret_cast<const float4*>(stage + j * 128 + lane * 4);
+                    if constexpr (OP == RowOp::kPlain) {
+                        st_v2(a.g.out + r * n + col, pack4(x));
+                    } else {
+                        float4 dg, du;
+                        dswiglu(bf16_lo(gate[i].x), bf16_lo(up[i].x), x.x, &dg.x, &du.x);
+                        dswiglu(bf16_hi(gate[i].x), bf16_hi(up[i].x), x.y, &dg.y, &du.y);
+                        dswiglu(bf16_lo(gate[i].y), bf16_lo(up[i].y), x.z, &dg.z, &du.z);
+                        dswiglu(bf16_hi(gate[i].y), bf16_hi(up[i].y), x.w, &dg.w, &du.w);
+                        st_v2(a.g.out + r * 2 * n + col, pack4(dg));
+                        st_v2(a.g.out + (r * 2 + 1) * n + col, pack4(du));
+                    }
+                }
             }
         }
     }
+}
+
+template <RowOp OP, bool KN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    row_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap map_a,
+                    const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
+    const uint32_t slots = smem_addr(base);
+    float* staging = reinterpret_cast<float*>(base + kPairStages * kPairSlot);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot + kStaging);
+    const int warp = threadIdx.x / 32, rank = int(cluster_rank());
+    pair_start(s, a.g.rows, kMaxRows, true);
+    if (warp == 0) {
+        load_role<OP, KN>(a, s, slots, rank, &map_a, &map_a128, &map_w);
+    } else if (warp == 1) {
+        if (rank == 0) mma_role<OP, KN>(a, s, slots);
+    } else if (warp >= 4) {
+        epilogue_role<OP>(a, s, staging, rank, warp);
+    }
+    pair_end(s);
 }
 
 template <RowOp OP, bool KN>
 cudaError_t launch(const LaunchCtx& ctx, const RowGemm& g) {
-    const int64_t tiles = g.rows.rows / kTile + g.rows.E;
-    if (tiles > 65535) return cudaErrorInvalidValue;
-    return launch_pdl(ctx, row_gemm_kernel<OP, KN>, dim3(unsigned((g.n + kTile - 1) / kTile), unsigned(tiles)),
-                      dim3(kThreads), 0, g);
+    auto kern = row_gemm_kernel<OP, KN>;
+    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot + kStaging;
+    // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
+    const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
+    if (err != cudaSuccess) return err;
+    constexpr uint64_t halves = OP == RowOp::kSwiglu ? 2 : 1;
+    const uint64_t k = uint64_t(g.k), n = uint64_t(g.n), E = uint64_t(g.rows.E);
+    const uint64_t da[2] = {k, uint64_t(g.rows.rows)}, dnk[4] = {k, n, halves, E}, dkn[3] = {n, k, E};
+    const uint32_t ba[2] = {kPairK, 16}, ba128[2] = {kPairK, 128}, bnk[4] = {kPairK, uint32_t(128 / halves), halves, 1},
+                   bkn[3] = {64, kPairK, 1};
+    CUtensorMap map_a, map_a128, map_w;
+    if (!make_map_bf16(&map_a, g.a, 2, da, ba) || !make_map_bf16(&map_a128, g.a, 2, da, ba128) ||
+        !(KN ? make_map_bf16(&map_w, g.w, 3, dkn, bkn) : make_map_bf16(&map_w, g.w, 4, dnk, bnk)))
+        return cudaErrorInvalidValue;
+    const GemmArgs a{g, (g.k + kPairK - 1) / kPairK, (g.n + kTileCols<OP> - 1) / kTileCols<OP>};
+    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, map_a, map_a128, map_w);
 }
 
 }  // namespace

@@ -1,0 +1,166 @@
+// expert_pair.cuh -- what the bf16 products of pairs of SMs share: the experts' row tiles, the ring's barriers, bounded
+// waits, the start and the end of a kernel.
+#pragma once
+
+#include <cstdint>
+
+#include "block_launch.h"
+#include "expert_rows.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+namespace moe {
+
+constexpr int kPairStages = 5;
+constexpr int kPairK = 64;                                 // values of the summed index in a slot: rows of 128 bytes
+constexpr uint32_t kPairBytes = 128 * 128;                 // one operand's part of a slot in one block
+constexpr uint32_t kPairSlot = 2 * kPairBytes;
+constexpr int kPairEpilogueWarps = 8;
+constexpr int kPairWarps = 4 + kPairEpilogueWarps;         // 0: loads, 1: products, 2, 3: none
+constexpr int kPairThreads = kPairWarps * 32;
+constexpr uint32_t kPairTmemColumns = 512;                 // two accumulators of 256
+
+struct PairShared {
+    // full, acc_empty: the leader's alone are used
+    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int dead;   // a wait gave up
+    int tiles;  // row tiles of all experts
+    // behind: prefix [E + 1], row tiles of the experts before e; base [E], first rows; count [E], rows
+    __device__ __forceinline__ int* prefix() { return reinterpret_cast<int*>(this + 1); }
+    __device__ __forceinline__ int* base(int E) { return prefix() + E + 1; }
+    __device__ __forceinline__ int* count(int E) { return base(E) + E; }
+};
+constexpr size_t pair_shared_bytes(int E) { return sizeof(PairShared) + size_t(3 * E + 1) * 4; }
+
+// Bounded waits, which mark the block dead when they give up.
+__device__ __forceinline__ bool gave_up(PairShared* s, int32_t* status) {
+    *const_cast<volatile int*>(&s->dead) = 1;
+    set_status(status, MOE_ERR_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ bool pair_wait(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {
+    return mbar_wait(bar, parity) || gave_up(s, status);
+}
+// The same for a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool pair_wait_warp(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {
+    return __all_sync(kFullMask, pair_wait(s, status, bar, parity));
+}
+// ... for a phase that threads of the other block complete too
+__device__ __forceinline__ bool pair_wait_cluster(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {
+    bool done = mbar_try_wait_cluster(bar, parity);
+    if (!done) {
+        const uint64_t t0 = global_ns();
+        int polls = 1;
+        while (!(done = mbar_try_wait_cluster(bar, parity))) {
+            if (polls < kWaitMinPolls)
+                polls++;
+            else if (global_ns() - t0 > kWaitLimitNs)
+                break;
+        }
+    }
+    return __all_sync(kFullMask, done || gave_up(s, status));
+}
+
+// True in all 128 threads of an epilogue group if it is in each of them: who gives up does not leave the others at a barrier.
+__device__ __forceinline__ bool group_all(int group, bool mine) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(1 + group), "r"(uint32_t(mine))
+        : "memory");
+    return all != 0;
+}
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+
+// The start of a kernel, by all threads of both blocks: barriers, tensor memory, the experts' rows and their tiles of
+// `tile_rows` rows. `check`: experts that share rows so that there are more tiles than the output could have are refused.
+__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tile_rows, bool check) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
+    if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; i++) {
+            mbar_init(smem_addr(&s->full[i]), 1);
+            mbar_init(smem_addr(&s->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_addr(&s->acc_full[i]), 1);
+            mbar_init(smem_addr(&s->acc_empty[i]), 2 * kPairEpilogueWarps);
+        }
+        mbar_fence_init();
+        s->dead = 0;
+        s->prefix()[0] = 0;
+    }
+    pdl_wait();
+    for (int e = threadIdx.x; e < E; e += kPairThreads) {
+        const RowSpan r = expert_rows(rows, e);
+        s->prefix()[e + 1] = int((uint32_t(r.count) + tile_rows - 1) / tile_rows);
+        s->base(E)[e] = int(r.base);
+        s->count(E)[e] = r.count;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t sum = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            int v = e0 + lane < E ? s->prefix()[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFullMask, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e0 + lane < E) s->prefix()[e0 + lane + 1] = int(sum + v);
+            sum += __shfl_sync(kFullMask, v, 31);
+        }
+        // Experts that share no row have at most so many tiles, and their tiles of the output are counted in 31 bits
+        // (checked on the host). Overlapping segments could have any number of both.
+        if (check && sum > rows.rows / tile_rows + E) {
+            if (lane == 0) set_status(rows.status, MOE_ERR_INVALID_ARG);
+            sum = 0;
+        }
+        if (lane == 0) s->tiles = int(sum);
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+}
+
+// The end of a kernel, by all threads of both blocks.
+__device__ __forceinline__ void pair_end(PairShared* s) {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*const_cast<volatile int*>(&s->dead) && threadIdx.x == 0) {
+        // whatever is still in flight lands in this block's memory: give it time before that is freed
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainLimitNs) __nanosleep(1000);
+    }
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (threadIdx.x / 32 == 1) pair_tmem_free(s->tmem, kPairTmemColumns);
+}
+
+// By the loading warp when it has nothing more to load: every product has read its slot, and no arrival is on its way to
+// this block any more.
+__device__ __forceinline__ void pair_drain(PairShared* s, int32_t* status, int st, uint32_t ph) {
+    for (int i = 0; i < kPairStages; i++) {
+        if (!pair_wait_warp(s, status, smem_addr(&s->empty[st]), ph ^ 1)) return;
+        if (++st == kPairStages) st = 0, ph ^= 1;
+    }
+}
+
+// Launches `kern` on one pair of blocks for every two SMs.
+template <typename Kernel, typename... Args>
+cudaError_t launch_pairs(const LaunchCtx& ctx, Kernel kern, size_t smem, Args... args) {
+    const int pairs = ctx.num_sms / 2 > 0 ? ctx.num_sms / 2 : 1;
+    return launch_pdl(ctx, kern, dim3(unsigned(2 * pairs)), dim3(kPairThreads), smem, args...);
+}
+
+}  // namespace moe

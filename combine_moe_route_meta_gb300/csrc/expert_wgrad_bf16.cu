@@ -1,58 +1,231 @@
 // expert_wgrad_bf16.cu -- the gradient of the experts' weights: out[e, i, j] (+)= sum_r a[r, i] b[r, j] over the rows
 // of each expert.
 //
-// One block takes 64 x 64 of one expert's results; a thread 4 x 4 of them, in fp32.
+// Persistent pairs of SMs, each walking over tiles of 256 x 256 results of one expert: the columns of `a` are the M side of
+// the products, 128 in each block, those of `b` the N side, half of them in each block (128 or 256 by what is left of n).
+// Both operands are read as they lie, rows of the summed index with M or N along them, and multiplied along their columns.
+// Warps have roles as in the row products; the epilogue's lanes have a row of the result each and write 32 columns at a
+// time.
+//
+// The rows behind an expert's last belong to others, or to nobody: they may hold anything, NaNs too, and are summed with.
+// So the last slot of a tile ends with the expert's rows: these come in boxes of 8 rows and of one, and what is missing to
+// 16, the step of a product, in boxes that lie outside of the tensor, which read as zero.
 #include <cstdint>
 
-#include "block_launch.h"
-#include "expert_rows.cuh"
+#include "expert_pair.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kTile = 256;
+static_assert(1024 + kPairStages * kPairSlot + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
 
-__global__ void __launch_bounds__(kThreads) weight_grad_kernel(WeightGrad g, int tiles_n) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    pdl_wait();
-    const int e = blockIdx.y, m0 = int(blockIdx.x) / tiles_n * kTile, n0 = int(blockIdx.x) % tiles_n * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const RowSpan span = expert_rows(g.rows, e);
-    float acc[4][4] = {};
-    for (int r0 = 0; r0 < span.count; r0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kTile, c = i % kTile;
-            const bool in = r0 + r < span.count;
-            sa[r][c] = in && m0 + c < g.m ? bf16_lo(g.a[(span.base + r0 + r) * g.m + m0 + c]) : 0.0f;
-            sb[r][c] = in && n0 + c < g.n ? bf16_lo(g.b[(span.base + r0 + r) * g.n + n0 + c]) : 0.0f;
+struct GradArgs {
+    WeightGrad g;
+    int tiles_m, tiles_n;
+    bool wide;  // out is 32-byte aligned
+};
+struct GradMaps {
+    CUtensorMap a[3], b[3];  // boxes of 64 columns x 64, 8 and 1 rows
+};
+
+struct Tile {
+    int e, m0, n0;
+    int row0, rows;  // the expert's
+    int blocks;      // blocks of 64 columns of b in each of the two
+};
+
+__device__ __forceinline__ Tile find_tile(const GradArgs& a, PairShared* s, int t) {
+    const int per = a.tiles_m * a.tiles_n, E = a.g.rows.E;
+    const int e = t / per, i = t - e * per, n0 = i / a.tiles_m * kTile;
+    return Tile{e, i % a.tiles_m * kTile, n0, s->base(E)[e], s->count(E)[e], a.g.n - n0 > kTile / 2 ? 2 : 1};
+}
+
+__device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint32_t slots, int rank, const GradMaps& maps) {
+    const int lane = threadIdx.x % 32, pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
+        const Tile tile = find_tile(a, s, t);
+        const int blocks = 2 + tile.blocks;  // of a, then of b
+        for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
+            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->empty[st]), ph ^ 1)) return;
+            const uint32_t own = smem_addr(&s->full[st]), bar = leaders(own), slot = slots + st * kPairSlot;
+            const int rem = min(kPairK, tile.rows - r0);
+            if (lane == 0 && rank == 0) mbar_expect_tx(own, 2 * blocks * ((rem + 15) & ~15) * 128);
+            // in pieces: boxes of 64 or 8 rows, then single rows, then (from outside the tensor) single rows to a multiple
+            // of 8 and a box of 8 to one of 16
+            const int eights = rem == kPairK ? 0 : rem / 8, ones = rem % 8, zeros = ones ? 8 - ones : 0;
+            const int groups = eights + (ones > 0), pieces = rem == kPairK ? 1 : eights + ones + zeros + groups % 2;
+            for (int q = lane; q < pieces * blocks; q += 32) {
+                const int piece = q / blocks, block = q % blocks;
+                int kind = 1, at = piece * 8;  // of the map, and the first row in the slot
+                int row = tile.row0 + r0 + at;
+                if (rem == kPairK) {
+                    kind = 0;
+                } else if (piece >= eights && piece < eights + ones + zeros) {
+                    kind = 2;
+                    at = eights * 8 + piece - eights;
+                    row = at < rem ? tile.row0 + r0 + at : -1;
+                } else if (piece >= eights) {
+                    at = groups * 8;
+                    row = -8;
+                }
+                const int col = block < 2 ? tile.m0 + rank * 128 + block * 64
+                                          : tile.n0 + rank * tile.blocks * 64 + (block - 2) * 64;
+                pair_load_2d(slot + block * (kPairBytes / 2) + at * 128, block < 2 ? &maps.a[kind] : &maps.b[kind], col, row,
+                             bar);
+            }
+            __syncwarp();
+            if (++st == kPairStages) st = 0, ph ^= 1;
         }
-        __syncthreads();
-        for (int r = 0; r < kStep; r++)
-            for (int i = 0; i < 4; i++)
-                for (int j = 0; j < 4; j++) acc[i][j] = fmaf(sa[r][ty * 4 + i], sb[r][tx * 4 + j], acc[i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++) {
-            const int r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-            if (r >= g.m || c >= g.n) continue;
-            const int64_t at = (int64_t(e) * g.m + r) * g.n + c;
-            if (g.fp32) {
-                float* out = static_cast<float*>(g.out) + at;
-                *out = g.accumulate ? *out + acc[i][j] : acc[i][j];
-            } else {
-                uint16_t* out = static_cast<uint16_t*>(g.out) + at;
-                *out = uint16_t(pack_bf16x2(g.accumulate ? bf16_lo(*out) + acc[i][j] : acc[i][j], 0.0f));
+    pair_drain(s, a.g.rows.status, st, ph);
+}
+
+// A whole warp of the leading block; one lane issues.
+__device__ __forceinline__ void mma_role(const GradArgs& a, PairShared* s, uint32_t slots) {
+    const uint64_t da = desc_mn128(slots), db = desc_mn128(slots + kPairBytes);
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
+    const bool leader = elect_one();
+    int st = 0, n_tile = 0;
+    uint32_t ph = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
+        const Tile tile = find_tile(a, s, t);
+        if (tile.rows == 0) continue;
+        const uint32_t idesc = pair_idesc_bf16(tile.blocks * 128, true, true);
+        const int acc = n_tile & 1;
+        const uint32_t d = s->tmem + acc * kTile;
+        if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
+        tc_fence_after();
+        n_tile++;
+        for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
+            if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t off = st * (kPairSlot / 16);
+                const int steps = (min(kPairK, tile.rows - r0) + 15) / 16;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if (j >= steps) break;
+                    pair_mma_bf16(d, da + off + 128 * j, db + off + 128 * j, idesc, r0 > 0 || j > 0);
+                }
+                pair_commit(empty + 8 * st);
+                if (r0 + kPairK >= tile.rows) pair_commit(smem_addr(&s->acc_full[acc]));
+            }
+            __syncwarp();
+            if (++st == kPairStages) st = 0, ph ^= 1;
+        }
+    }
+}
+
+// 8 results at element `at` of out.
+__device__ __forceinline__ void store8(const GradArgs& a, int64_t at, float* v) {
+    if (a.g.fp32) {
+        float* p = static_cast<float*>(a.g.out) + at;
+        if (a.g.accumulate) {
+            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = __float_as_uint(v[i]);
+        if (a.wide) {
+            st_v8(p, w);
+        } else {
+            st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+            st_v4(p + 4, make_uint4(w[4], w[5], w[6], w[7]));
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.g.out) + at;
+        if (a.g.accumulate) {
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4*>(p), x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += x[i];
+        }
+        st_v4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                            pack_bf16x2(v[6], v[7])));
+    }
+}
+
+__device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, int rank, int warp) {
+    const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
+    const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
+    const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
+    int n_tile = 0;
+    for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
+        const Tile tile = find_tile(a, s, t);
+        const int m = tile.m0 + rank * 128 + quad * 32 + lane;
+        const int width = tile.blocks * 64, c0 = group * width;  // the group's half of the columns
+        const int64_t line = (int64_t(tile.e) * a.g.m + m) * a.g.n + tile.n0;
+        const bool sums = tile.rows > 0;
+        if (!sums && a.g.accumulate) continue;
+        const int acc = n_tile & 1;
+        if (sums) {
+            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1)) return;
+            tc_fence_after();
+            n_tile++;
+        }
+        for (int c = c0; c < c0 + width; c += 32) {
+            __syncwarp();
+            uint32_t r[32] = {};
+            if (sums) {
+                tmem_load32(tmem + acc * kTile + c, r);
+                tmem_wait(r, 32);
+                if (c + 32 == c0 + width) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
+                }
+            }
+            if (m >= a.g.m) continue;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (tile.n0 + c + i * 8 >= a.g.n) break;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j] = __uint_as_float(r[i * 8 + j]);
+                store8(a, line + c + i * 8, v);
             }
         }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    weight_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ GradMaps maps) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
+    const uint32_t slots = smem_addr(base);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot);
+    const int warp = threadIdx.x / 32, rank = int(cluster_rank());
+    pair_start(s, a.g.rows, kTile, false);
+    if (warp == 0) {
+        load_role(a, s, slots, rank, maps);
+    } else if (warp == 1) {
+        if (rank == 0) mma_role(a, s, slots);
+    } else if (warp >= 4) {
+        epilogue_role(a, s, rank, warp);
+    }
+    pair_end(s);
 }
 
 }  // namespace
 
 cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& g) {
-    const int tiles_m = (g.m + kTile - 1) / kTile, tiles_n = (g.n + kTile - 1) / kTile;
-    return launch_pdl(ctx, weight_grad_kernel, dim3(unsigned(tiles_m * tiles_n), unsigned(g.rows.E)), dim3(kThreads), 0,
-                      g, tiles_n);
+    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot;
+    // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
+    const cudaError_t err = allow_shared_memory(weight_grad_kernel, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
+    if (err != cudaSuccess) return err;
+    GradMaps maps{};
+    const uint64_t rows = uint64_t(g.rows.rows), da[2] = {uint64_t(g.m), rows}, db[2] = {uint64_t(g.n), rows};
+    const uint32_t box[3][2] = {{64, kPairK}, {64, 8}, {64, 1}};
+    for (int i = 0; i < 3 && rows > 0; i++)  // without rows nothing is loaded
+        if (!make_map_bf16(&maps.a[i], g.a, 2, da, box[i]) || !make_map_bf16(&maps.b[i], g.b, 2, db, box[i]))
+            return cudaErrorInvalidValue;
+    const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile, reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
+    return launch_pairs(ctx, weight_grad_kernel, smem + pair_shared_bytes(g.rows.E), a, maps);
 }
 
 }  // namespace moe
