@@ -66,11 +66,14 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
     return Tile{lo, i / rows_t * kTileCols<OP>, s->base(E)[lo] + first, min(step, count - first)};
 }
 
+// A whole warp; one lane issues, with operands that are the same in all lanes.
 template <RowOp OP, bool KN>
 __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank,
                                           const CUtensorMap* map_a, const CUtensorMap* map_a128,
                                           const CUtensorMap* map_w) {
-    const int lane = threadIdx.x % 32, pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
+    const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
+    const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
+    const bool leader = elect_one();
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
@@ -78,12 +81,13 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
         const int half = tile.n() / 2, boxes = half / 16;
         const int row0 = tile.row0 + rank * half;
         const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
+        const uint32_t bytes = 2 * (kPairBytes + boxes * 2048);
         for (int c = 0; c < a.chunks; c++) {
-            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->empty[st]), ph ^ 1)) return;
-            const uint32_t own = smem_addr(&s->full[st]), bar = leaders(own), slot = slots + st * kPairSlot;
-            const int k0 = c * kPairK;
-            if (lane == 0) {
-                if (rank == 0) mbar_expect_tx(own, 2 * (kPairBytes + boxes * 2048));
+            if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
+            if (leader) {
+                const uint32_t bar = counted + 8 * st, slot = slots + st * kPairSlot;
+                const int k0 = c * kPairK;
+                if (rank == 0) mbar_expect_tx(own + 8 * st, bytes);
                 if constexpr (KN) {
                     pair_load_3d(slot, map_w, n0, k0, tile.e, bar);
                     pair_load_3d(slot + kPairBytes / 2, map_w, n0 + 64, k0, tile.e, bar);
@@ -91,10 +95,13 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
                     // (k, column, half, expert); SwiGLU: 64 columns of both halves
                     pair_load_4d(slot, map_w, k0, n0, 0, tile.e, bar);
                 }
-                if (boxes == 8) pair_load_2d(slot + kPairBytes, map_a128, k0, row0, bar);
+                if (boxes == 8) {
+                    pair_load_2d(slot + kPairBytes, map_a128, k0, row0, bar);
+                } else {
+                    for (int i = 0; i < boxes; i++)
+                        pair_load_2d(slot + kPairBytes + i * 2048, map_a, k0, row0 + i * 16, bar);
+                }
             }
-            if (boxes < 8 && lane < boxes)
-                pair_load_2d(slot + kPairBytes + lane * 2048, map_a, k0, row0 + lane * 16, bar);
             __syncwarp();
             if (++st == kPairStages) st = 0, ph ^= 1;
         }

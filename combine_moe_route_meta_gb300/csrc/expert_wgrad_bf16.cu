@@ -41,40 +41,43 @@ __device__ __forceinline__ Tile find_tile(const GradArgs& a, PairShared* s, int 
     return Tile{e, i % a.tiles_m * kTile, n0, s->base(E)[e], s->count(E)[e], a.g.n - n0 > kTile / 2 ? 2 : 1};
 }
 
+// One box of every block of 64 columns: `blocks` of them, of a and then of b, to rows at `to` of the slot.
+__device__ __forceinline__ void load_boxes(const CUtensorMap* a, const CUtensorMap* b, uint32_t to, int blocks, int m, int n,
+                                           int row, uint32_t bar) {
+    pair_load_2d(to, a, m, row, bar);
+    pair_load_2d(to + kPairBytes / 2, a, m + 64, row, bar);
+    pair_load_2d(to + kPairBytes, b, n, row, bar);
+    if (blocks == 4) pair_load_2d(to + kPairBytes + kPairBytes / 2, b, n + 64, row, bar);
+}
+
+// A whole warp; one lane issues, with operands that are the same in all lanes (others cost 60 % more time for a slot).
 __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint32_t slots, int rank, const GradMaps& maps) {
-    const int lane = threadIdx.x % 32, pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
+    const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
+    const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
+    const bool leader = elect_one();
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
         const Tile tile = find_tile(a, s, t);
-        const int blocks = 2 + tile.blocks;  // of a, then of b
+        const int blocks = 2 + tile.blocks, m = tile.m0 + rank * 128, n = tile.n0 + rank * tile.blocks * 64;
         for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
-            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->empty[st]), ph ^ 1)) return;
-            const uint32_t own = smem_addr(&s->full[st]), bar = leaders(own), slot = slots + st * kPairSlot;
-            const int rem = min(kPairK, tile.rows - r0);
-            if (lane == 0 && rank == 0) mbar_expect_tx(own, 2 * blocks * ((rem + 15) & ~15) * 128);
-            // in pieces: boxes of 64 or 8 rows, then single rows, then (from outside the tensor) single rows to a multiple
-            // of 8 and a box of 8 to one of 16
-            const int eights = rem == kPairK ? 0 : rem / 8, ones = rem % 8, zeros = ones ? 8 - ones : 0;
-            const int groups = eights + (ones > 0), pieces = rem == kPairK ? 1 : eights + ones + zeros + groups % 2;
-            for (int q = lane; q < pieces * blocks; q += 32) {
-                const int piece = q / blocks, block = q % blocks;
-                int kind = 1, at = piece * 8;  // of the map, and the first row in the slot
-                int row = tile.row0 + r0 + at;
+            if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
+            if (leader) {
+                const uint32_t bar = counted + 8 * st, slot = slots + st * kPairSlot;
+                const int rem = min(kPairK, tile.rows - r0), row = tile.row0 + r0;
+                if (rank == 0) mbar_expect_tx(own + 8 * st, 2 * blocks * ((rem + 15) & ~15) * 128);
                 if (rem == kPairK) {
-                    kind = 0;
-                } else if (piece >= eights && piece < eights + ones + zeros) {
-                    kind = 2;
-                    at = eights * 8 + piece - eights;
-                    row = at < rem ? tile.row0 + r0 + at : -1;
-                } else if (piece >= eights) {
-                    at = groups * 8;
-                    row = -8;
+                    load_boxes(&maps.a[0], &maps.b[0], slot, blocks, m, n, row, bar);
+                } else {
+                    int at = 0;
+                    for (; at + 8 <= rem; at += 8)
+                        load_boxes(&maps.a[1], &maps.b[1], slot + at * 128, blocks, m, n, row + at, bar);
+                    // the last rows, and zeros from outside the tensor to a multiple of 8, then of 16
+                    if (at < rem)
+                        for (const int end = at + 8; at < end; at++)
+                            load_boxes(&maps.a[2], &maps.b[2], slot + at * 128, blocks, m, n, at < rem ? row + at : -1, bar);
+                    if (at % 16) load_boxes(&maps.a[1], &maps.b[1], slot + at * 128, blocks, m, n, -8, bar);
                 }
-                const int col = block < 2 ? tile.m0 + rank * 128 + block * 64
-                                          : tile.n0 + rank * tile.blocks * 64 + (block - 2) * 64;
-                pair_load_2d(slot + block * (kPairBytes / 2) + at * 128, block < 2 ? &maps.a[kind] : &maps.b[kind], col, row,
-                             bar);
             }
             __syncwarp();
             if (++st == kPairStages) st = 0, ph ^= 1;
