@@ -4,8 +4,8 @@
 // Persistent pairs of SMs, each walking over tiles of 256 x 256 results of one expert: the columns of `a` are the M side of
 // the products, 128 in each block, those of `b` the N side, half of them in each block (128 or 256 by what is left of n).
 // Both operands are read as they lie, rows of the summed index with M or N along them, and multiplied along their columns.
-// Warps have roles as in the row products; the epilogue's lanes have a row of the result each and write 32 columns at a
-// time.
+// Warps have roles as in the row products; the epilogue's warps store 128 bytes of 32
+// rows at a time.
 //
 // The rows behind an expert's last belong to others, or to nobody: they may hold anything, NaNs too, and are summed with.
 // So the last slot of a tile ends with the expert's rows: these come in boxes of 8 rows and of one, and what is missing to
@@ -18,12 +18,13 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256;
-static_assert(1024 + kPairStages * kPairSlot + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
+constexpr uint32_t kStaged = 32 * 128;                              // an epilogue warp's rows on their way out
+constexpr uint32_t kStaging = kPairEpilogueWarps * kStaged;
+static_assert(1024 + kPairStages * kPairSlot + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
 
 struct GradArgs {
     WeightGrad g;
     int tiles_m, tiles_n;
-    bool wide;  // out is 32-byte aligned
 };
 struct GradMaps {
     CUtensorMap a[3], b[3];  // boxes of 64 columns x 64, 8 and 1 rows
@@ -123,85 +124,95 @@ __device__ __forceinline__ void mma_role(const GradArgs& a, PairShared* s, uint3
     }
 }
 
-// 8 results at element `at` of out.
-__device__ __forceinline__ void store8(const GradArgs& a, int64_t at, float* v) {
-    if (a.g.fp32) {
-        float* p = static_cast<float*>(a.g.out) + at;
-        if (a.g.accumulate) {
-            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = __float_as_uint(v[i]);
-        if (a.wide) {
-            st_v8(p, w);
-        } else {
-            st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
-            st_v4(p + 4, make_uint4(w[4], w[5], w[6], w[7]));
-        }
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(a.g.out) + at;
-        if (a.g.accumulate) {
-            float x[8];
-            unpack8(*reinterpret_cast<const uint4*>(p), x);
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] += x[i];
-        }
-        st_v4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                            pack_bf16x2(v[6], v[7])));
-    }
+// The sums of two columns as one word of bf16.
+__device__ __forceinline__ uint32_t pack_sums(const uint32_t* r) {
+    return pack_bf16x2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-__device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, int rank, int warp) {
+// A warp's 32 rows, 128 bytes of each at a time: lanes have a row each, which goes through shared memory in the 128-byte
+// swizzle to a tensor store, so that whole lines reach L2 (written by the lanes themselves, 32 bytes in 32 lines at a time,
+// 128 experts' 1536 x 4096 of 512 rows took 906 us). fp32 sums are added to out by the store itself.
+template <bool FP32>
+__device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, uint32_t staging, int rank, int warp,
+                                              const CUtensorMap* map_out) {
+    constexpr int kCols = FP32 ? 32 : 64;
     const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
+    const uint32_t buffer = staging + (warp - 4) * kStaged, mine = buffer + lane * 128;
     const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
     int n_tile = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
         const Tile tile = find_tile(a, s, t);
-        const int m = tile.m0 + rank * 128 + quad * 32 + lane;
+        const int m0 = tile.m0 + rank * 128 + quad * 32;
         const int width = tile.blocks * 64, c0 = group * width;  // the group's half of the columns
-        const int64_t line = (int64_t(tile.e) * a.g.m + m) * a.g.n + tile.n0;
         const bool sums = tile.rows > 0;
         if (!sums && a.g.accumulate) continue;
         const int acc = n_tile & 1;
         if (sums) {
-            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1)) return;
+            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1)) break;
             tc_fence_after();
             n_tile++;
         }
-        for (int c = c0; c < c0 + width; c += 32) {
-            __syncwarp();
-            uint32_t r[32] = {};
+        for (int c = c0; c < c0 + width; c += kCols) {
+            uint32_t w[32] = {};
             if (sums) {
-                tmem_load32(tmem + acc * kTile + c, r);
-                tmem_wait(r, 32);
-                if (c + 32 == c0 + width) {
+                if constexpr (FP32) {
+                    tmem_load32(tmem + acc * kTile + c, w);
+                    tmem_wait(w, 32);
+                } else {
+                    uint32_t r[64];
+                    tmem_load32(tmem + acc * kTile + c, r);
+                    tmem_load32(tmem + acc * kTile + c + 32, r + 32);
+                    tmem_wait(r, 64);
+                    if (a.g.accumulate && m0 + lane < a.g.m) {
+                        const uint16_t* p = static_cast<const uint16_t*>(a.g.out) +
+                                            (int64_t(tile.e) * a.g.m + m0 + lane) * a.g.n + tile.n0 + c;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            if (tile.n0 + c + i * 8 >= a.g.n) break;
+                            float x[8];
+                            unpack8(*reinterpret_cast<const uint4*>(p + i * 8), x);
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                r[i * 8 + j] = __float_as_uint(__uint_as_float(r[i * 8 + j]) + x[j]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i++) w[i] = pack_sums(r + 2 * i);
+                }
+                if (c + kCols == c0 + width) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
                 }
             }
-            if (m >= a.g.m) continue;
+            if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (tile.n0 + c + i * 8 >= a.g.n) break;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; j++) v[j] = __uint_as_float(r[i * 8 + j]);
-                store8(a, line + c + i * 8, v);
+            for (int i = 0; i < 8; i++)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)),
+                             "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                             : "memory");
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && m0 < a.g.m && tile.n0 + c < a.g.n) {
+                tma_store_3d(map_out, tile.n0 + c, m0, tile.e, buffer, FP32 && a.g.accumulate);
+                bulk_commit();
             }
+            __syncwarp();
         }
     }
+    if (lane == 0) bulk_wait_all();
 }
 
+template <bool FP32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    weight_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ GradMaps maps) {
+    weight_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ GradMaps maps,
+                       const __grid_constant__ CUtensorMap map_out) {
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
-    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, kTile, false);
     if (warp == 0) {
@@ -209,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) mma_role(a, s, slots);
     } else if (warp >= 4) {
-        epilogue_role(a, s, rank, warp);
+        epilogue_role<FP32>(a, s, slots + kPairStages * kPairSlot, rank, warp, &map_out);
     }
     pair_end(s);
 }
@@ -217,18 +228,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }  // namespace
 
 cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& g) {
-    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot;
+    auto kern = g.fp32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
+    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot + kStaging;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
-    const cudaError_t err = allow_shared_memory(weight_grad_kernel, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
+    const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
     if (err != cudaSuccess) return err;
     GradMaps maps{};
+    CUtensorMap map_out;
     const uint64_t rows = uint64_t(g.rows.rows), da[2] = {uint64_t(g.m), rows}, db[2] = {uint64_t(g.n), rows};
-    const uint32_t box[3][2] = {{64, kPairK}, {64, 8}, {64, 1}};
+    const uint64_t dout[3] = {uint64_t(g.n), uint64_t(g.m), uint64_t(g.rows.E)};
+    const uint32_t box[3][2] = {{64, kPairK}, {64, 8}, {64, 1}}, bout[3] = {g.fp32 ? 32u : 64u, 32, 1};
     for (int i = 0; i < 3 && rows > 0; i++)  // without rows nothing is loaded
         if (!make_map_bf16(&maps.a[i], g.a, 2, da, box[i]) || !make_map_bf16(&maps.b[i], g.b, 2, db, box[i]))
             return cudaErrorInvalidValue;
-    const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile, reinterpret_cast<uintptr_t>(g.out) % 32 == 0};
-    return launch_pairs(ctx, weight_grad_kernel, smem + pair_shared_bytes(g.rows.E), a, maps);
+    if (!(g.fp32 ? make_map_fp32(&map_out, g.out, 3, dout, bout) : make_map_bf16(&map_out, g.out, 3, dout, bout)))
+        return cudaErrorInvalidValue;
+    const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile};
+    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, maps, map_out);
 }
 
 }  // namespace moe
