@@ -26,7 +26,7 @@ constexpr int kCols = 256;
 constexpr int kChunkRows = 16;                               // rows of the accumulator at a time
 constexpr uint32_t kStaged = kChunkRows * 128 * 4;           // ... of a block's 128 columns in fp32
 constexpr uint32_t kStaging = 2 * 2 * kStaged;               // two groups of four epilogue warps, two buffers each
-static_assert(1024 + kPairStages * kPairSlot + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024,
+static_assert(1024 + kPairRing + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024,
               "shared memory of an SM");
 
 struct GemmArgs {
@@ -63,17 +63,25 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
     const int count = s->count(E)[lo], each = (count + rows_t - 1) / rows_t;
     const int step = (each + 31) & ~31;
     const int first = min(m * step, count);
-    return Tile{lo, i / rows_t * kTileCols<OP>, s->base(E)[lo] + first, min(step, count - first)};
+    return Tile{uniform(lo), uniform(i / rows_t * kTileCols<OP>), uniform(s->base(E)[lo] + first),
+                uniform(min(step, count - first))};
 }
 
 // A whole warp; one lane issues, with operands that are the same in all lanes.
+// Bytes of a slot, a multiple of the swizzle's atoms, and how many there are: by the largest tile. One token's 8 experts of
+// 2 x 768 x 4096: 18.4 us, with five slots of 32 KB 20.0; 128 experts of 32 rows, 4096 x 2048: 331 and 349 us.
+__device__ __forceinline__ uint32_t slot_bytes(const PairShared* s) { return kPairBytes + uint32_t((s->most + 31) & ~31) * 64; }
+__device__ __forceinline__ int ring_slots(uint32_t slot) { return min(kPairSlots, int(kPairRing / slot)); }
+
 template <RowOp OP, bool KN>
 __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank,
                                           const CUtensorMap* map_a, const CUtensorMap* map_a128,
                                           const CUtensorMap* map_w) {
     const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
     const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
-    const bool leader = elect_one();
+    const uint32_t leader = elect_one();
+    const uint32_t slot_size = uniform(slot_bytes(s));
+    const int stages = uniform(ring_slots(slot_size));
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
@@ -85,7 +93,7 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
         for (int c = 0; c < a.chunks; c++) {
             if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
             if (leader) {
-                const uint32_t bar = counted + 8 * st, slot = slots + st * kPairSlot;
+                const uint32_t bar = counted + 8 * st, slot = slots + st * slot_size;
                 const int k0 = c * kPairK;
                 if (rank == 0) mbar_expect_tx(own + 8 * st, bytes);
                 if constexpr (KN) {
@@ -103,46 +111,45 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
                 }
             }
             __syncwarp();
-            if (++st == kPairStages) st = 0, ph ^= 1;
+            if (++st == stages) st = 0, ph ^= 1;
         }
     }
-    pair_drain(s, a.g.rows.status, st, ph);
+    pair_drain(s, a.g.rows.status, st, ph, stages);
 }
 
 // A whole warp of the leading block; one lane issues.
 template <RowOp OP, bool KN>
 __device__ __forceinline__ void mma_role(const GemmArgs& a, PairShared* s, uint32_t slots) {
     const uint64_t da = KN ? desc_mn128(slots) : desc_k128(slots), db = desc_k128(slots + kPairBytes);
-    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty), tmem = uniform(s->tmem);
     const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
     const int last = (a.g.k - (a.chunks - 1) * kPairK + 15) / 16;  // steps of 16 in the last slot
-    const bool leader = elect_one();
+    const uint32_t leader = elect_one();
+    const uint32_t slot_size = uniform(slot_bytes(s));
+    const int stages = uniform(ring_slots(slot_size));
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
         const Tile tile = find_tile<OP>(a, s, t);
         const uint32_t idesc = pair_idesc_bf16(tile.n(), KN, false);
         const int acc = n_tile & 1;
-        const uint32_t d = s->tmem + acc * kMaxRows;
+        const uint32_t d = tmem + acc * kMaxRows;
         if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
         tc_fence_after();
         for (int c = 0; c < a.chunks; c++) {
             if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return;
             tc_fence_after();
-            if (leader) {
-                const uint32_t off = st * (kPairSlot / 16);
-                const int steps = c + 1 < a.chunks ? 4 : last;
+            const uint32_t off = st * (slot_size / 16);
+            const int steps = c + 1 < a.chunks ? 4 : last;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    if (j >= steps) break;
-                    // 16 values of k: 32 bytes further in the rows; or 16 rows of 128 bytes
-                    pair_mma_bf16(d, da + off + (KN ? 128 : 2) * j, db + off + 2 * j, idesc, c > 0 || j > 0);
-                }
-                pair_commit(empty + 8 * st);
-                if (c + 1 == a.chunks) pair_commit(smem_addr(&s->acc_full[acc]));
+            for (int j = 0; j < 4; j++) {
+                if (j >= steps) break;
+                // 16 values of k: 32 bytes further in the rows; or 16 rows of 128 bytes
+                pair_mma_bf16(leader, d, da + off + (KN ? 128 : 2) * j, db + off + 2 * j, idesc, c > 0 || j > 0);
             }
-            __syncwarp();
-            if (++st == kPairStages) st = 0, ph ^= 1;
+            pair_commit(leader, empty + 8 * st);
+            if (c + 1 == a.chunks) pair_commit(leader, smem_addr(&s->acc_full[acc]));
+            if (++st == stages) st = 0, ph ^= 1;
         }
     }
 }
@@ -244,8 +251,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
-    float* staging = reinterpret_cast<float*>(base + kPairStages * kPairSlot);
-    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot + kStaging);
+    float* staging = reinterpret_cast<float*>(base + kPairRing);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, kMaxRows, true);
     if (warp == 0) {
@@ -261,7 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <RowOp OP, bool KN>
 cudaError_t launch(const LaunchCtx& ctx, const RowGemm& g) {
     auto kern = row_gemm_kernel<OP, KN>;
-    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot + kStaging;
+    constexpr size_t smem = 1024 + size_t(kPairRing) + kStaging;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
     const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
     if (err != cudaSuccess) return err;

@@ -11,10 +11,10 @@
 
 namespace moe {
 
-constexpr int kPairStages = 5;
 constexpr int kPairK = 64;                                 // values of the summed index in a slot: rows of 128 bytes
-constexpr uint32_t kPairBytes = 128 * 128;                 // one operand's part of a slot in one block
-constexpr uint32_t kPairSlot = 2 * kPairBytes;
+constexpr uint32_t kPairBytes = 128 * 128;                 // 128 of these rows: an operand's part of a slot in one block
+constexpr uint32_t kPairRing = 10 * kPairBytes;            // of slots
+constexpr int kPairSlots = 10;                             // at most
 constexpr int kPairEpilogueWarps = 8;
 constexpr int kPairWarps = 4 + kPairEpilogueWarps;         // 0: loads, 1: products, 2, 3: none
 constexpr int kPairThreads = kPairWarps * 32;
@@ -22,16 +22,20 @@ constexpr uint32_t kPairTmemColumns = 512;                 // two accumulators o
 
 struct PairShared {
     // full, acc_empty: the leader's alone are used
-    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
+    uint64_t full[kPairSlots], empty[kPairSlots], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int dead;   // a wait gave up
     int tiles;  // row tiles of all experts
+    int most;   // rows of the largest
     // behind: prefix [E + 1], row tiles of the experts before e; base [E], first rows; count [E], rows
     __device__ __forceinline__ int* prefix() { return reinterpret_cast<int*>(this + 1); }
     __device__ __forceinline__ int* base(int E) { return prefix() + E + 1; }
     __device__ __forceinline__ int* count(int E) { return base(E) + E; }
 };
 constexpr size_t pair_shared_bytes(int E) { return sizeof(PairShared) + size_t(3 * E + 1) * 4; }
+
+// A value that is the same in all lanes, as the compiler then knows.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFullMask, v, 0); }
 
 // Bounded waits, which mark the block dead when they give up.
 __device__ __forceinline__ bool gave_up(PairShared* s, int32_t* status) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kPairStages; i++) {
+        for (int i = 0; i < kPairSlots; i++) {
             mbar_init(smem_addr(&s->full[i]), 1);
             mbar_init(smem_addr(&s->empty[i]), 1);
         }
@@ -107,6 +111,9 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
     __syncthreads();
     if (warp == 0) {
         int64_t sum = 0;
+        int most = 0;
+        for (int e = lane; e < E; e += 32) most = max(most, s->count(E)[e]);
+        most = int(__reduce_max_sync(kFullMask, unsigned(most)));
         for (int e0 = 0; e0 < E; e0 += 32) {
             int v = e0 + lane < E ? s->prefix()[e0 + lane + 1] : 0;
 #pragma unroll
@@ -123,7 +130,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
             if (lane == 0) set_status(rows.status, MOE_ERR_INVALID_ARG);
             sum = 0;
         }
-        if (lane == 0) s->tiles = int(sum);
+        if (lane == 0) s->tiles = int(sum), s->most = min(most, tile_rows);
     }
     __syncwarp();
     tc_fence_before();
@@ -147,12 +154,12 @@ __device__ __forceinline__ void pair_end(PairShared* s) {
     if (threadIdx.x / 32 == 1) pair_tmem_free(s->tmem, kPairTmemColumns);
 }
 
-// By the loading warp when it has nothing more to load: every product has read its slot, and no arrival is on its way to
-// this block any more.
-__device__ __forceinline__ void pair_drain(PairShared* s, int32_t* status, int st, uint32_t ph) {
-    for (int i = 0; i < kPairStages; i++) {
+// By the loading warp when it has nothing more to load, of a ring of `slots`: every product has read its slot, and no arrival
+// is on its way to this block any more.
+__device__ __forceinline__ void pair_drain(PairShared* s, int32_t* status, int st, uint32_t ph, int slots) {
+    for (int i = 0; i < slots; i++) {
         if (!pair_wait_warp(s, status, smem_addr(&s->empty[st]), ph ^ 1)) return;
-        if (++st == kPairStages) st = 0, ph ^= 1;
+        if (++st == slots) st = 0, ph ^= 1;
     }
 }
 

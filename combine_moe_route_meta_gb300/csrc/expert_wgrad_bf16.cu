@@ -18,9 +18,11 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256;
+constexpr uint32_t kSlot = 2 * kPairBytes;  // 64 rows of 128 columns of a, and of b
+constexpr int kStages = kPairRing / kSlot;
 constexpr uint32_t kStaged = 32 * 128;                              // an epilogue warp's rows on their way out
 constexpr uint32_t kStaging = kPairEpilogueWarps * kStaged;
-static_assert(1024 + kPairStages * kPairSlot + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
+static_assert(1024 + kPairRing + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
 
 struct GradArgs {
     WeightGrad g;
@@ -39,7 +41,8 @@ struct Tile {
 __device__ __forceinline__ Tile find_tile(const GradArgs& a, PairShared* s, int t) {
     const int per = a.tiles_m * a.tiles_n, E = a.g.rows.E;
     const int e = t / per, i = t - e * per, n0 = i / a.tiles_m * kTile;
-    return Tile{e, i % a.tiles_m * kTile, n0, s->base(E)[e], s->count(E)[e], a.g.n - n0 > kTile / 2 ? 2 : 1};
+    return Tile{uniform(e), uniform(i % a.tiles_m * kTile), uniform(n0), uniform(s->base(E)[e]), uniform(s->count(E)[e]),
+                uniform(a.g.n - n0 > kTile / 2 ? 2 : 1)};
 }
 
 // One box of every block of 64 columns: `blocks` of them, of a and then of b, to rows at `to` of the slot.
@@ -55,7 +58,7 @@ __device__ __forceinline__ void load_boxes(const CUtensorMap* a, const CUtensorM
 __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint32_t slots, int rank, const GradMaps& maps) {
     const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
     const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
-    const bool leader = elect_one();
+    const uint32_t leader = elect_one();
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
@@ -64,7 +67,7 @@ __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint
         for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
             if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
             if (leader) {
-                const uint32_t bar = counted + 8 * st, slot = slots + st * kPairSlot;
+                const uint32_t bar = counted + 8 * st, slot = slots + st * kSlot;
                 const int rem = min(kPairK, tile.rows - r0), row = tile.row0 + r0;
                 if (rank == 0) mbar_expect_tx(own + 8 * st, 2 * blocks * ((rem + 15) & ~15) * 128);
                 if (rem == kPairK) {
@@ -81,18 +84,18 @@ __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint
                 }
             }
             __syncwarp();
-            if (++st == kPairStages) st = 0, ph ^= 1;
+            if (++st == kStages) st = 0, ph ^= 1;
         }
     }
-    pair_drain(s, a.g.rows.status, st, ph);
+    pair_drain(s, a.g.rows.status, st, ph, kStages);
 }
 
 // A whole warp of the leading block; one lane issues.
 __device__ __forceinline__ void mma_role(const GradArgs& a, PairShared* s, uint32_t slots) {
     const uint64_t da = desc_mn128(slots), db = desc_mn128(slots + kPairBytes);
-    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty);
+    const uint32_t full = smem_addr(s->full), empty = smem_addr(s->empty), tmem = uniform(s->tmem);
     const int pairs = gridDim.x / 2, tiles = a.g.rows.E * a.tiles_m * a.tiles_n;
-    const bool leader = elect_one();
+    const uint32_t leader = elect_one();
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
@@ -100,26 +103,23 @@ __device__ __forceinline__ void mma_role(const GradArgs& a, PairShared* s, uint3
         if (tile.rows == 0) continue;
         const uint32_t idesc = pair_idesc_bf16(tile.blocks * 128, true, true);
         const int acc = n_tile & 1;
-        const uint32_t d = s->tmem + acc * kTile;
+        const uint32_t d = tmem + acc * kTile;
         if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
         tc_fence_after();
         n_tile++;
         for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
             if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return;
             tc_fence_after();
-            if (leader) {
-                const uint32_t off = st * (kPairSlot / 16);
-                const int steps = (min(kPairK, tile.rows - r0) + 15) / 16;
+            const uint32_t off = st * (kSlot / 16);
+            const int steps = (min(kPairK, tile.rows - r0) + 15) / 16;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    if (j >= steps) break;
-                    pair_mma_bf16(d, da + off + 128 * j, db + off + 128 * j, idesc, r0 > 0 || j > 0);
-                }
-                pair_commit(empty + 8 * st);
-                if (r0 + kPairK >= tile.rows) pair_commit(smem_addr(&s->acc_full[acc]));
+            for (int j = 0; j < 4; j++) {
+                if (j >= steps) break;
+                pair_mma_bf16(leader, d, da + off + 128 * j, db + off + 128 * j, idesc, r0 > 0 || j > 0);
             }
-            __syncwarp();
-            if (++st == kPairStages) st = 0, ph ^= 1;
+            pair_commit(leader, empty + 8 * st);
+            if (r0 + kPairK >= tile.rows) pair_commit(leader, smem_addr(&s->acc_full[acc]));
+            if (++st == kStages) st = 0, ph ^= 1;
         }
     }
 }
@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
-    PairShared* s = reinterpret_cast<PairShared*>(base + kPairStages * kPairSlot + kStaging);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, kTile, false);
     if (warp == 0) {
@@ -220,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) mma_role(a, s, slots);
     } else if (warp >= 4) {
-        epilogue_role<FP32>(a, s, slots + kPairStages * kPairSlot, rank, warp, &map_out);
+        epilogue_role<FP32>(a, s, slots + kPairRing, rank, warp, &map_out);
     }
     pair_end(s);
 }
@@ -229,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& g) {
     auto kern = g.fp32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
-    constexpr size_t smem = 1024 + size_t(kPairStages) * kPairSlot + kStaging;
+    constexpr size_t smem = 1024 + size_t(kPairRing) + kStaging;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
     const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
     if (err != cudaSuccess) return err;

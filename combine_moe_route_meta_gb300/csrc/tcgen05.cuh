@@ -240,19 +240,26 @@ __device__ __forceinline__ constexpr uint32_t pair_idesc_bf16(int n, bool a_mn, 
     return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
            (uint32_t(n >> 3) << 17) | (uint32_t(256 >> 4) << 24);
 }
-__device__ __forceinline__ void pair_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Executed by a converged warp and issued by the lane in which `issue` is not 0: without a branch, so that operands which
+// are the same in all lanes stay in uniform registers, where the instructions want them (a branch around four products and a
+// commit costs 70 clocks).
+__device__ __forceinline__ void pair_mma_bf16(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@p tcgen05.mma.cta_group::2.kind::f16 [%1], %2, %3, %4, q;\n\t}" ::"r"(issue),
+        "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
         : "memory");
 }
-// An arrival at `bar` of both blocks when every earlier product of this thread is done.
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
+// An arrival at `bar` of both blocks when every earlier product of the issuing lane is done.
+__device__ __forceinline__ void pair_commit(uint32_t issue, uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(uint16_t(3))
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+        "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"(
+            issue),
+        "r"(bar), "h"(uint16_t(3))
         : "memory");
 }
 
