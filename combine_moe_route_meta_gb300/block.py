@@ -223,16 +223,28 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
         with _current(stream):
             return rmsnorm(x, weight, eps, residual, quant, bf16, keep)
     T, H = x.shape
-    q, dev = _norm_quant(quant), x.device
+    q, n = _norm_quant(quant), 2 * T * H
+    px, pw, pr = _pointers((x, 0, "x", _BF16), (weight, 2 * H, "weight", _BF16), (residual, n, "residual", _BF16))
     if bf16 is None:
         bf16 = not q
-    out = torch.empty((T, H), dtype=_BF16, device=dev) if bf16 else None
-    codes = torch.empty((T, H), dtype=torch.uint8, device=dev) if q else None
-    scales = torch.empty((T, H // 128), dtype=_F32 if q == MOE_QUANT_FP8_G128 else torch.uint8, device=dev) if q else None
-    total = torch.empty((T, H), dtype=_BF16, device=dev) if residual is not None else None
-    rstd = torch.empty(T, dtype=_F32, device=dev) if keep else None
-    moe_rmsnorm(x, weight, eps, out, residual, total, rstd, quant, codes, scales)
-    return NormOutput(out, codes, scales, x if total is None else total, rstd)
+    out = codes = scales = rstd = None
+    total = x
+    if bf16:
+        out = torch.empty_like(x)
+    if residual is not None:
+        total = torch.empty_like(x)
+    if q:
+        codes = torch.empty_like(x, dtype=torch.uint8)
+        scales = torch.empty((T, H // 128), dtype=_F32 if q == MOE_QUANT_FP8_G128 else torch.uint8, device=x.device)
+    if keep:
+        rstd = torch.empty(T, dtype=_F32, device=x.device)
+    # what is allocated here needs no checks
+    st = load_library().moe_rmsnorm(px, pr, pw, float(eps), T, H, q, out.data_ptr() if bf16 else None,
+                                    codes.data_ptr() if q else None, scales.data_ptr() if q else None,
+                                    total.data_ptr() if total is not x else None, rstd.data_ptr() if keep else None,
+                                    _on(None))
+    _check(st, "moe_rmsnorm")
+    return NormOutput(out, codes, scales, total, rstd)
 
 
 def rmsnorm_backward(grad_out: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -243,12 +255,17 @@ def rmsnorm_backward(grad_out: torch.Tensor, s: torch.Tensor, weight: torch.Tens
         with _current(stream):
             return rmsnorm_backward(grad_out, s, weight, rstd, grad_residual)
     T, H = s.shape
-    dev = s.device
-    grad_x = torch.empty((T, H), dtype=_BF16, device=dev)
-    grad_weight = torch.empty(H, dtype=_F32, device=dev)
-    n = moe_rmsnorm_backward_workspace_size(T, H)
-    workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    moe_rmsnorm_backward(grad_out, s, weight, rstd, grad_x, grad_weight, workspace, grad_residual)
+    n = 2 * T * H
+    pg, ps, pw, pr, pgs = _pointers((grad_out, n, "grad_out", _BF16), (s, 0, "s", _BF16), (weight, 2 * H, "weight", _BF16),
+                                    (rstd, 4 * T, "rstd", _F32), (grad_residual, n, "grad_residual", _BF16))
+    lib = load_library()
+    size = lib.moe_rmsnorm_backward_workspace_size(T, H)
+    # what is allocated here needs no checks
+    grad_x, grad_weight = torch.empty_like(s), torch.empty(H, dtype=_F32, device=s.device)
+    workspace = torch.empty(size, dtype=torch.uint8, device=s.device)
+    st = lib.moe_rmsnorm_backward(pg, ps, pw, pr, pgs, T, H, grad_x.data_ptr(), grad_weight.data_ptr(),
+                                  workspace.data_ptr(), size, _on(None))
+    _check(st, "moe_rmsnorm_backward")
     return grad_x, grad_weight
 
 

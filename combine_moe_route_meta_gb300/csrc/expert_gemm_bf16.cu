@@ -67,12 +67,12 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
                 uniform(min(step, count - first))};
 }
 
-// A whole warp; one lane issues, with operands that are the same in all lanes.
 // Bytes of a slot, a multiple of the swizzle's atoms, and how many there are: by the largest tile. One token's 8 experts of
 // 2 x 768 x 4096: 18.4 us, with five slots of 32 KB 20.0; 128 experts of 32 rows, 4096 x 2048: 331 and 349 us.
 __device__ __forceinline__ uint32_t slot_bytes(const PairShared* s) { return kPairBytes + uint32_t((s->most + 31) & ~31) * 64; }
 __device__ __forceinline__ int ring_slots(uint32_t slot) { return min(kPairSlots, int(kPairRing / slot)); }
 
+// A whole warp; one lane issues, with operands that are the same in all lanes.
 template <RowOp OP, bool KN>
 __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank,
                                           const CUtensorMap* map_a, const CUtensorMap* map_a128,

@@ -52,7 +52,7 @@ constexpr size_t kMostSharedMemory = 200 * 1024;  // of the dispatch, interleave
 // Kernels that cannot be resident at all report 0.
 template <typename Kernel>
 cudaError_t blocks_per_sm(const LaunchCtx& ctx, Kernel kern, int threads, size_t smem, int* out) {
-    constexpr int kDevices = 64, kSlots = 16;
+    constexpr int kDevices = 64, kSlots = 64;
     struct Entry {
         const void* fn;
         int threads;

@@ -3,20 +3,34 @@
 //
 // A row stays in registers between its one reading and its one writing. A lane has runs of 8 columns, threads next to
 // each other neighbouring runs, so accesses are of 16 bytes and the 128 values of an FP8 group lie in 16 neighbouring
-// lanes. Rows of up to 1024 columns are a warp's, longer ones a block's. The gradient of the weight is a sum over rows:
-// each of at most kGradBlocks blocks sums its rows in registers and writes one line of partial sums; a second kernel adds
-// the lines in order.
+// lanes. Rows of up to 1024 columns are a warp's, longer ones a block's. As many blocks as fit go from row to row, with the
+// next row's loads on their way beside this one's reduction. The gradient of the weight is a sum over rows: each of at most
+// kGradBlocks blocks sums its rows in registers and writes one line of partial sums; a second kernel adds the lines in order.
+//
+// Bound by DRAM; one GB300, whose copy bandwidth is 6777 GB/s, cold L2:
+//   16384 x 4096, residual:  FP8 72 us (6.5 TB/s), bf16 87 us (6.1), gradient 93 us (5.8)
+//   8192 x 7168:             FP8 65 us (6.4 TB/s), bf16 76 us (6.1), gradient 93 us (5.1)
+//   128 x 7168:              FP8 2.8 us, bf16 2.3 us, gradient 5.4 us (two launches)
+// One row a block, and no loads ahead: 100, 97 and 147 us for the first.
 #include <cstdint>
 
 #include "block_launch.h"
 #include "dispatch_slice.cuh"
+#include "moe_block.h"
 #include "moe_device.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kGradBlocks = 304;
-constexpr int kWarpRows = 4;  // rows of a block whose warps have a row each
+constexpr int kWarpColumns = 1024;  // of a warp's row, at most
+// Warps of a block with a row each: the gradient's blocks are few, so they have more warps where registers allow.
+template <int V, bool GRAD>
+constexpr int kWarpRows = GRAD && V < 4 ? 16 / V : 4;
+// Whether a row is loaded beside the one before and the weight stays in registers: not in blocks of up to 512 or 1024
+// threads with four runs of columns each.
+template <int V, bool WARP>
+constexpr bool kAhead = WARP || V < 4;
 
 __device__ __forceinline__ uint4 ld_v4(const void* p) {  // of what may be written in place
     uint4 v;
@@ -42,135 +56,190 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[32], int turn) {
     return v;
 }
 
-template <int V, int QUANT, bool WARP>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(Norm a) {
-    __shared__ float part[1][32];
+// Where a thread's rows and columns lie: a warp's rows go from warp to warp of the grid, a block's from block to block.
+template <bool WARP>
+struct Place {
+    int lane, lanes;
+    int64_t first, step;
+    __device__ __forceinline__ Place()
+        : lane(WARP ? threadIdx.x % 32 : threadIdx.x),
+          lanes(WARP ? 32 : blockDim.x),
+          first(WARP ? (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32 : blockIdx.x),
+          step(WARP ? int64_t(gridDim.x) * (blockDim.x / 32) : gridDim.x) {}
+    __device__ __forceinline__ int column(int v) const { return (v * lanes + lane) * 8; }
+};
+
+// A thread's part of a row, zeros beyond its end; all zeros for p null.
+template <int V, bool WARP>
+__device__ __forceinline__ void load_row(uint4 (&r)[V], const uint16_t* p, int64_t t, int H, const Place<WARP>& at) {
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        r[v] = p && at.column(v) < H ? ld_v4(p + t * H + at.column(v)) : make_uint4(0, 0, 0, 0);
+}
+
+template <int V, int QUANT, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) rmsnorm_kernel(Norm a) {
+    __shared__ float part[2][32];
     pdl_wait();
-    const int64_t t = WARP ? int64_t(blockIdx.x) * kWarpRows + threadIdx.x / 32 : blockIdx.x;
-    const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, lanes = WARP ? 32 : blockDim.x;
-    if (WARP && t >= a.T) return;
-    const int64_t row = t * a.H;
-    float s[V][8], square = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = (v * lanes + lane) * 8;
-        const bool in = c < a.H;
-        unpack8(in ? ld_v4(a.x + row + c) : make_uint4(0, 0, 0, 0), s[v]);
-        if (a.residual && in) {
-            float r[8];
-            unpack8(ld_v4(a.residual + row + c), r);
-#pragma unroll
-            for (int j = 0; j < 8; j++) s[v][j] += r[j];
-            // the norm is of the sum as it is stored, rounded: what the next layer and the gradient see
-            const uint4 sum = pack8(s[v]);
-            unpack8(sum, s[v]);
-            if (a.sum) st_v4(a.sum + row + c, sum);
+    const Place<WARP> at;
+    uint4 w[V], x[V], res[V];
+    if (kAhead<V, WARP>) load_row(w, a.weight, 0, a.H, at);
+    if (kAhead<V, WARP> && at.first < a.T) {
+        load_row(x, a.x, at.first, a.H, at);
+        load_row(res, a.residual, at.first, a.H, at);
+    }
+    int turn = 0;
+    for (int64_t t = at.first; t < a.T; t += at.step, turn ^= 1) {
+        const int64_t row = t * a.H;
+        float s[V][8], square = 0.0f;
+        if (!kAhead<V, WARP>) {
+            load_row(x, a.x, t, a.H, at);
+            load_row(res, a.residual, t, a.H, at);
         }
 #pragma unroll
-        for (int j = 0; j < 8; j++) square = fmaf(s[v][j], s[v][j], square);
-    }
-    square = row_sum<WARP>(square, part, 0);
-    const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(square, float(a.H)), a.eps)));
-    if (a.rstd && lane == 0) a.rstd[t] = r;
+        for (int v = 0; v < V; v++) {
+            unpack8(x[v], s[v]);
+            if (a.residual) {
+                float r[8];
+                unpack8(res[v], r);
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = (v * lanes + lane) * 8;
-        const bool in = c < a.H;
-        float y[8];
-        unpack8(in ? __ldg(reinterpret_cast<const uint4*>(a.weight + c)) : make_uint4(0, 0, 0, 0), y);
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = __fmul_rn(__fmul_rn(s[v][j], r), y[j]);
-        if (a.out && in) st_v4(a.out + row + c, pack8(y));
-        if constexpr (QUANT != MOE_QUANT_NONE) {
-            // the unrounded values: one rounding to 8 bits, not two
-            float amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(y[j]));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
-            const float sc = __fdiv_rn(fmaxf(amax, 1e-10f), 448.0f);
-            uint32_t q[2];
-            if constexpr (QUANT == MOE_QUANT_FP8_G128) {
-                const float inv = __frcp_rn(sc);
-#pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = div_by_scale(y[j], sc, inv);
-                if (in && lane % 16 == 0) static_cast<float*>(a.scales)[t * (a.H / 128) + c / 128] = sc;
-            } else {
-                const uint32_t bits = __float_as_uint(sc);
-                const uint32_t ex = (bits >> 23) + ((bits & 0x7fffffu) ? 1u : 0u);
-                const float inv = __uint_as_float((254u - ex) << 23);  // of a power of two: exact
-#pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = __fmul_rn(y[j], inv);
-                if (in && lane % 16 == 0) static_cast<uint8_t*>(a.scales)[t * (a.H / 128) + c / 128] = uint8_t(ex);
+                for (int j = 0; j < 8; j++) s[v][j] += r[j];
+                // the norm is of the sum as it is stored, rounded: what the next layer and the gradient see
+                const uint4 sum = pack8(s[v]);
+                unpack8(sum, s[v]);
+                if (a.sum && at.column(v) < a.H) st_v4(a.sum + row + at.column(v), sum);
             }
 #pragma unroll
-            for (int j = 0; j < 2; j++) q[j] = e4m3x2(y[4 * j], y[4 * j + 1]) | e4m3x2(y[4 * j + 2], y[4 * j + 3]) << 16;
-            if (in) st_v2(a.codes + row + c, make_uint2(q[0], q[1]));
+            for (int j = 0; j < 8; j++) square = fmaf(s[v][j], s[v][j], square);
+        }
+        if (!kAhead<V, WARP>) {
+            load_row(w, a.weight, 0, a.H, at);
+        } else if (t + at.step < a.T) {  // the next row, beside this one's reduction
+            load_row(x, a.x, t + at.step, a.H, at);
+            load_row(res, a.residual, t + at.step, a.H, at);
+        }
+        square = row_sum<WARP>(square, part, turn);
+        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(square, float(a.H)), a.eps)));
+        if (a.rstd && at.lane == 0) a.rstd[t] = r;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int c = at.column(v);
+            const bool in = c < a.H;
+            float y[8];
+            unpack8(w[v], y);
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[j] = __fmul_rn(__fmul_rn(s[v][j], r), y[j]);
+            if (a.out && in) st_v4(a.out + row + c, pack8(y));
+            if constexpr (QUANT != MOE_QUANT_NONE) {
+                // the unrounded values: one rounding to 8 bits, not two
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(y[j]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
+                const float sc = __fdiv_rn(fmaxf(amax, 1e-10f), 448.0f);
+                uint32_t q[2];
+                if constexpr (QUANT == MOE_QUANT_FP8_G128) {
+                    const float inv = __frcp_rn(sc);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) y[j] = div_by_scale(y[j], sc, inv);
+                    if (in && at.lane % 16 == 0) static_cast<float*>(a.scales)[t * (a.H / 128) + c / 128] = sc;
+                } else {
+                    const uint32_t bits = __float_as_uint(sc);
+                    const uint32_t ex = (bits >> 23) + ((bits & 0x7fffffu) ? 1u : 0u);
+                    const float inv = __uint_as_float((254u - ex) << 23);  // of a power of two: exact
+#pragma unroll
+                    for (int j = 0; j < 8; j++) y[j] = __fmul_rn(y[j], inv);
+                    if (in && at.lane % 16 == 0) static_cast<uint8_t*>(a.scales)[t * (a.H / 128) + c / 128] = uint8_t(ex);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    q[j] = e4m3x2(y[4 * j], y[4 * j + 1]) | e4m3x2(y[4 * j + 2], y[4 * j + 3]) << 16;
+                if (in) st_v2(a.codes + row + c, make_uint2(q[0], q[1]));
+            }
         }
     }
 }
 
-template <int V, bool WARP>
-__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(NormGrad a) {
+template <int V, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(NormGrad a) {
     __shared__ float part[2][32];
-    extern __shared__ float lines[];  // WARP: [kWarpRows][H]
+    extern __shared__ float lines[];  // WARP: [warps][H]
     pdl_wait();
-    const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, lanes = WARP ? 32 : blockDim.x;
-    const int64_t first = WARP ? int64_t(blockIdx.x) * kWarpRows + threadIdx.x / 32 : blockIdx.x;
-    const int64_t step = WARP ? int64_t(gridDim.x) * kWarpRows : gridDim.x;
-    float acc[V][8] = {};
+    const Place<WARP> at;
+    uint4 w[V], s[V], g[V], more[V];
+    float acc[V][8] = {}, r = 0.0f;
+    if (kAhead<V, WARP>) load_row(w, a.weight, 0, a.H, at);
+    if (kAhead<V, WARP> && at.first < a.T) {
+        load_row(s, a.s, at.first, a.H, at);
+        load_row(g, a.grad, at.first, a.H, at);
+        load_row(more, a.grad_sum, at.first, a.H, at);
+        r = __ldg(a.rstd + at.first);
+    }
     int turn = 0;
-    for (int64_t t = first; t < a.T; t += step, turn ^= 1) {
-        const int64_t row = t * a.H;
-        const float r = __ldg(a.rstd + t);
+    for (int64_t t = at.first; t < a.T; t += at.step, turn ^= 1) {
         float hat[V][8], gw[V][8], dot = 0.0f;
+        uint4 add[V];
+        if (!kAhead<V, WARP>) {
+            load_row(w, a.weight, 0, a.H, at);
+            load_row(s, a.s, t, a.H, at);
+            load_row(g, a.grad, t, a.H, at);
+            r = __ldg(a.rstd + t);
+        }
+        const float r_now = r;
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int c = (v * lanes + lane) * 8;
-            const bool in = c < a.H;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            float w[8];
-            unpack8(in ? ld_v4(a.s + row + c) : zero, hat[v]);
-            unpack8(in ? ld_v4(a.grad + row + c) : zero, gw[v]);
-            unpack8(in ? __ldg(reinterpret_cast<const uint4*>(a.weight + c)) : zero, w);
+            float wv[8];
+            unpack8(s[v], hat[v]);
+            unpack8(g[v], gw[v]);
+            unpack8(w[v], wv);
+            add[v] = more[v];
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                hat[v][j] *= r;
+                hat[v][j] *= r_now;
                 acc[v][j] = fmaf(gw[v][j], hat[v][j], acc[v][j]);
-                gw[v][j] *= w[j];
+                gw[v][j] *= wv[j];
                 dot = fmaf(gw[v][j], hat[v][j], dot);
             }
+        }
+        if (!kAhead<V, WARP>) {
+            load_row(add, a.grad_sum, t, a.H, at);
+        } else if (t + at.step < a.T) {  // the next row, beside this one's reduction
+            load_row(s, a.s, t + at.step, a.H, at);
+            load_row(g, a.grad, t + at.step, a.H, at);
+            load_row(more, a.grad_sum, t + at.step, a.H, at);
+            r = __ldg(a.rstd + t + at.step);
         }
         const float mean = __fdiv_rn(row_sum<WARP>(dot, part, turn), float(a.H));
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int c = (v * lanes + lane) * 8;
-            if (c >= a.H) continue;
-            float d[8], more[8];
-            unpack8(a.grad_sum ? ld_v4(a.grad_sum + row + c) : make_uint4(0, 0, 0, 0), more);
+            if (at.column(v) >= a.H) continue;
+            float d[8], f[8];
+            unpack8(add[v], f);
 #pragma unroll
-            for (int j = 0; j < 8; j++) d[j] = fmaf(r, fmaf(-mean, hat[v][j], gw[v][j]), more[j]);
-            st_v4(a.grad_x + row + c, pack8(d));
+            for (int j = 0; j < 8; j++) d[j] = fmaf(r_now, fmaf(-mean, hat[v][j], gw[v][j]), f[j]);
+            st_v4(a.grad_x + t * a.H + at.column(v), pack8(d));
         }
     }
     float* line = a.partial + int64_t(blockIdx.x) * a.H;
     if constexpr (WARP) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int c = (v * 32 + lane) * 8;
+            const int c = at.column(v);
             if (c >= a.H) continue;
+#pragma unroll
             for (int j = 0; j < 8; j++) lines[threadIdx.x / 32 * a.H + c + j] = acc[v][j];
         }
         __syncthreads();
         for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
             float sum = 0.0f;
-            for (int i = 0; i < kWarpRows; i++) sum += lines[i * a.H + c];
+            for (int i = 0; i < THREADS / 32; i++) sum += lines[i * a.H + c];
             line[c] = sum;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int c = (v * lanes + lane) * 8;
+            const int c = at.column(v);
             if (c >= a.H) continue;
             *reinterpret_cast<float4*>(line + c) = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
             *reinterpret_cast<float4*>(line + c + 4) = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
@@ -195,53 +264,85 @@ __global__ void __launch_bounds__(256) add_lines_kernel(const float* lines, int 
     out[c] = s;
 }
 
-template <int V, bool WARP>
-cudaError_t launch_norm(const LaunchCtx& ctx, const Norm& a, int threads) {
-    const unsigned grid = unsigned(WARP ? (a.T + kWarpRows - 1) / kWarpRows : a.T);
-    if (a.quant == MOE_QUANT_NONE)
-        return launch_pdl(ctx, rmsnorm_kernel<V, MOE_QUANT_NONE, WARP>, dim3(grid), dim3(threads), 0, a);
-    if (a.quant == MOE_QUANT_FP8_G128)
-        return launch_pdl(ctx, rmsnorm_kernel<V, MOE_QUANT_FP8_G128, WARP>, dim3(grid), dim3(threads), 0, a);
-    return launch_pdl(ctx, rmsnorm_kernel<V, MOE_QUANT_FP8_G128_UE8M0, WARP>, dim3(grid), dim3(threads), 0, a);
+template <typename Kernel>
+cudaError_t launch_rows(const LaunchCtx& ctx, Kernel kern, const Norm& a, int rows, int threads) {
+    int per_sm = 0;
+    const cudaError_t err = blocks_per_sm(ctx, kern, threads, 0, &per_sm);
+    if (err != cudaSuccess) return err;
+    const int64_t need = (a.T + rows - 1) / rows;
+    const int64_t most = int64_t(ctx.num_sms) * (per_sm > 0 ? per_sm : 1);
+    return launch_pdl(ctx, kern, dim3(unsigned(need < most ? need : most)), dim3(threads), 0, a);
 }
 
-template <int V, bool WARP>
+template <int V, bool WARP, int THREADS>
+cudaError_t launch_norm(const LaunchCtx& ctx, const Norm& a, int threads) {
+    const int rows = WARP ? threads / 32 : 1;
+    if (a.quant == MOE_QUANT_NONE)
+        return launch_rows(ctx, rmsnorm_kernel<V, MOE_QUANT_NONE, WARP, THREADS>, a, rows, threads);
+    if (a.quant == MOE_QUANT_FP8_G128)
+        return launch_rows(ctx, rmsnorm_kernel<V, MOE_QUANT_FP8_G128, WARP, THREADS>, a, rows, threads);
+    return launch_rows(ctx, rmsnorm_kernel<V, MOE_QUANT_FP8_G128_UE8M0, WARP, THREADS>, a, rows, threads);
+}
+template <int V>
+cudaError_t launch_norm_warps(const LaunchCtx& ctx, const Norm& a) {
+    return launch_norm<V, true, kWarpRows<V, false> * 32>(ctx, a, kWarpRows<V, false> * 32);
+}
+
+template <int V, bool WARP, int THREADS>
 cudaError_t launch_grad(const LaunchCtx& ctx, const NormGrad& a, int threads) {
-    const size_t smem = WARP ? size_t(kWarpRows) * a.H * sizeof(float) : 0;
-    return launch_pdl(ctx, rmsnorm_backward_kernel<V, WARP>, dim3(unsigned(norm_backward_blocks(a.T, a.H))),
+    const size_t smem = WARP ? size_t(threads / 32) * a.H * sizeof(float) : 0;
+    return launch_pdl(ctx, rmsnorm_backward_kernel<V, WARP, THREADS>, dim3(unsigned(norm_backward_blocks(a.T, a.H))),
                       dim3(threads), smem, a);
 }
+template <int V>
+cudaError_t launch_grad_warps(const LaunchCtx& ctx, const NormGrad& a) {
+    return launch_grad<V, true, kWarpRows<V, true> * 32>(ctx, a, kWarpRows<V, true> * 32);
+}
 
+// Runs of 8 columns in a thread of a block that has a row: two, one where that would leave few threads to a block (1003 rows
+// of 2176: 4.5 us with one, 5.0 with two; 16384 rows of 4096 in FP8: 79 and 72 us), four beyond 512 threads.
+int block_runs(int H) { return H < 4096 ? 1 : H <= 8192 ? 2 : 4; }
 int block_threads(int H, int V) { return ((H / 8 + V - 1) / V + 31) / 32 * 32; }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const LaunchCtx& ctx, const Norm& a) {
-    if (a.H <= 256) return launch_norm<1, true>(ctx, a, kWarpRows * 32);
-    if (a.H <= 512) return launch_norm<2, true>(ctx, a, kWarpRows * 32);
-    if (a.H <= 1024) return launch_norm<4, true>(ctx, a, kWarpRows * 32);
-    if (a.H <= 8192) return launch_norm<2, false>(ctx, a, block_threads(a.H, 2));
-    return launch_norm<4, false>(ctx, a, block_threads(a.H, 4));
+    if (a.H <= kWarpColumns / 4) return launch_norm_warps<1>(ctx, a);
+    if (a.H <= kWarpColumns / 2) return launch_norm_warps<2>(ctx, a);
+    if (a.H <= kWarpColumns) return launch_norm_warps<4>(ctx, a);
+    const int V = block_runs(a.H), threads = block_threads(a.H, V);
+    if (V == 1) return launch_norm<1, false, 512>(ctx, a, threads);
+    if (V == 2) return launch_norm<2, false, 512>(ctx, a, threads);
+    return launch_norm<4, false, 1024>(ctx, a, threads);
 }
 
 int norm_backward_blocks(int64_t T, int H) {
-    const int64_t need = H <= 1024 ? (T + kWarpRows - 1) / kWarpRows : T;
+    const int rows = H <= kWarpColumns / 4   ? kWarpRows<1, true>
+                     : H <= kWarpColumns / 2 ? kWarpRows<2, true>
+                     : H <= kWarpColumns     ? kWarpRows<4, true>
+                                             : 1;
+    const int64_t need = (T + rows - 1) / rows;
     return int(need < kGradBlocks ? need : kGradBlocks);
 }
 
 cudaError_t launch_rmsnorm_backward(const LaunchCtx& ctx, const NormGrad& a) {
     cudaError_t err = cudaSuccess;
     if (a.T > 0) {
-        if (a.H <= 256)
-            err = launch_grad<1, true>(ctx, a, kWarpRows * 32);
-        else if (a.H <= 512)
-            err = launch_grad<2, true>(ctx, a, kWarpRows * 32);
-        else if (a.H <= 1024)
-            err = launch_grad<4, true>(ctx, a, kWarpRows * 32);
-        else if (a.H <= 8192)
-            err = launch_grad<2, false>(ctx, a, block_threads(a.H, 2));
+        const int V = block_runs(a.H), threads = block_threads(a.H, V);
+        if (a.H <= kWarpColumns / 4)
+            err = launch_grad_warps<1>(ctx, a);
+        else if (a.H <= kWarpColumns / 2)
+            err = launch_grad_warps<2>(ctx, a);
+        else if (a.H <= kWarpColumns)
+            err = launch_grad_warps<4>(ctx, a);
+        else if (V == 1)
+            err = launch_grad<1, false, 512>(ctx, a, threads);
+        else if (V == 2)
+            err = launch_grad<2, false, 512>(ctx, a, threads);
+        else if (threads <= 512)
+            err = launch_grad<4, false, 512>(ctx, a, threads);
         else
-            err = launch_grad<4, false>(ctx, a, block_threads(a.H, 4));
+            err = launch_grad<4, false, 1024>(ctx, a, threads);
     }
     if (err != cudaSuccess) return err;
     return launch_pdl(ctx, add_lines_kernel, dim3(unsigned((a.H + 31) / 32)), dim3(256), 0,
