@@ -83,9 +83,28 @@ __device__ __forceinline__ void group_sync(int group) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// The start of a kernel, by all threads of both blocks: barriers, tensor memory, the experts' rows and their tiles of
-// `tile_rows` rows. `check`: experts that share rows so that there are more tiles than the output could have are refused.
-__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tile_rows, bool check) {
+// The most rows of a tile: 256, 128 or 64, whichever makes the last pair finish first, if the tiles were all alike: a tile of
+// n rows takes 150 + 0.77 n ns for each 64 values of k (measured: 248 ns for 128 rows, 293 for 192, 346 for 256). Small
+// tiles are for few of them: 16 experts of 356 rows, dSwiGLU 2112 x 704: 29 us with 128 rows, 36 with 256.
+constexpr int kRowChoices = 3;
+// 256 >> the result.
+__device__ __forceinline__ int pick_tile_rows(const uint32_t (&tiles)[kRowChoices], uint32_t rows, int tiles_n, int pairs) {
+    int best = 0;
+    float least = __int_as_float(0x7f800000);
+#pragma unroll
+    for (int i = 0; i < kRowChoices; i++) {
+        const float rounds = __fdividef(float(tiles[i]) * float(tiles_n), float(pairs));
+        if (tiles[i] == 0 || (i > 0 && rounds > 16.0f)) continue;  // many tiles: the last round hardly matters
+        const float cost = ceilf(rounds) * (150.0f + 0.77f * __fdividef(float(rows), float(tiles[i])));
+        if (cost < least) least = cost, best = i;
+    }
+    return best;
+}
+
+// The start of a kernel, by all threads of both blocks: barriers, tensor memory, the experts' rows. tiles_n > 0: their row
+// tiles too, with so many column tiles each; experts that share rows so that there are more tiles than the output could
+// have are refused.
+__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
     if (threadIdx.x == 0) {
@@ -99,38 +118,49 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
         }
         mbar_fence_init();
         s->dead = 0;
+        s->tiles = 0;
         s->prefix()[0] = 0;
     }
     pdl_wait();
     for (int e = threadIdx.x; e < E; e += kPairThreads) {
         const RowSpan r = expert_rows(rows, e);
-        s->prefix()[e + 1] = int((uint32_t(r.count) + tile_rows - 1) / tile_rows);
         s->base(E)[e] = int(r.base);
         s->count(E)[e] = r.count;
     }
     __syncthreads();
-    if (warp == 0) {
-        int64_t sum = 0;
-        int most = 0;
-        for (int e = lane; e < E; e += 32) most = max(most, s->count(E)[e]);
-        most = int(__reduce_max_sync(kFullMask, unsigned(most)));
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            int v = e0 + lane < E ? s->prefix()[e0 + lane + 1] : 0;
+    if (warp == 0 && tiles_n > 0) {
+        uint32_t tiles[kRowChoices] = {}, all = 0, most = 0;
+        for (int e = lane; e < E; e += 32) {
+            const uint32_t c = s->count(E)[e];
+            all += c;
+            most = max(most, c);
+            // kept below what 32 lanes could overflow with, and above what experts that share no row have
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(kFullMask, v, o);
-                if (lane >= o) v += u;
-            }
-            if (e0 + lane < E) s->prefix()[e0 + lane + 1] = int(sum + v);
-            sum += __shfl_sync(kFullMask, v, 31);
+            for (int i = 0; i < kRowChoices; i++) tiles[i] = min(tiles[i] + (c + (256u >> i) - 1) / (256u >> i), 1u << 26);
         }
+        all = __reduce_add_sync(kFullMask, all);
+        most = __reduce_max_sync(kFullMask, most);
+#pragma unroll
+        for (int i = 0; i < kRowChoices; i++) tiles[i] = __reduce_add_sync(kFullMask, tiles[i]);
         // Experts that share no row have at most so many tiles, and their tiles of the output are counted in 31 bits
         // (checked on the host). Overlapping segments could have any number of both.
-        if (check && sum > rows.rows / tile_rows + E) {
+        if (int64_t(tiles[0]) > rows.rows / 256 + E) {
             if (lane == 0) set_status(rows.status, MOE_ERR_INVALID_ARG);
-            sum = 0;
+        } else {
+            const int shift = 8 - pick_tile_rows(tiles, all, tiles_n, gridDim.x / 2);
+            int sum = 0;
+            for (int e0 = 0; e0 < E; e0 += 32) {
+                int v = e0 + lane < E ? int((uint32_t(s->count(E)[e0 + lane]) + (1u << shift) - 1) >> shift) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(kFullMask, v, o);
+                    if (lane >= o) v += u;
+                }
+                if (e0 + lane < E) s->prefix()[e0 + lane + 1] = sum + v;
+                sum += __shfl_sync(kFullMask, v, 31);
+            }
+            if (lane == 0) s->tiles = sum, s->most = int(min(most, 1u << shift));
         }
-        if (lane == 0) s->tiles = int(sum), s->most = min(most, tile_rows);
     }
     __syncwarp();
     tc_fence_before();
