@@ -341,7 +341,7 @@ class BF16MoELayer:
                              f"{tuple(x.shape)}, {tuple(topk_ids.shape)} and {tuple(topk_weights.shape)}")
         out = self.out[:T]
         self.seen = None
-        if T <= self.few:
+        if self.few and T <= self.few:
             moe_layer_few_tokens(x, topk_ids, topk_weights, self.w13, self.w2, out, self.few_workspace, self.status,
                                  stream=stream)
             return out

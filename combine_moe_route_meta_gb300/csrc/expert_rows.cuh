@@ -78,7 +78,7 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
     return g < 0.0f ? (up * e) * (g * r * c) : up * (g * r);
 }
 
-// p = 1 / (1 + exp(-g)) and q = 1 - p, each to 2^-20 (2^-19 where exp(-|g|) is subnormal): by e = exp(-|g|), made as in
+// p = 1 / (1 + exp(-g)) and q = 1 - p, each to 2^-20 and the step of a subnormal exp(-|g|): by e = exp(-|g|), made as in
 // swiglu(), one is 1 / (1 + e) and the other e / (1 + e), so neither is a difference.
 __device__ __forceinline__ void sigmoids(float g, float* p, float* q) {
     constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
@@ -92,13 +92,13 @@ __device__ __forceinline__ void sigmoids(float g, float* p, float* q) {
     *p = g < 0.0f ? e * r : r;
     *q = g < 0.0f ? r : e * r;
 }
-// The gradients of h = up * silu(gate) with respect to gate and up, times dh. Factors near the ends of the range are
-// multiplied by the small ones first: dh * up alone could overflow where the result does not.
+// The gradient of h = up * silu(gate) with respect to gate and up, times dh. In this order no factor overflows, or becomes
+// 0 times infinity, where the result does not: below 0 gate counts after p has made it small.
 __device__ __forceinline__ void dswiglu(float gate, float up, float dh, float* dgate, float* dup) {
     float p, q;
     sigmoids(gate, &p, &q);
-    *dgate = (dh * p) * (up * fmaf(gate, q, 1.0f));
-    *dup = (dh * p) * gate;
+    *dgate = dh * ((up * p) * fmaf(gate, q, 1.0f));
+    *dup = dh * (gate * p);
 }
 
 }  // namespace moe

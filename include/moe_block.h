@@ -85,8 +85,8 @@ moe_status_t moe_expert_gemm_swiglu_bf16(moe_mode_t mode, const uint16_t *a, int
  *   dh = sum_k grad_out[r, k] * w2[e, k, i],  p = 1 / (1 + exp(-G))
  *   grad_gate_up[r, i] = bf16_rn(dh * U * p * (1 + G * (1 - p)))
  *   grad_gate_up[r, inter + i] = bf16_rn(dh * G * p)
- * with G, U = gate_up[r, i], gate_up[r, inter + i], and dh in fp32. The gradients of an infinite or NaN G
- * or U are unspecified.
+ * with G, U = gate_up[r, i], gate_up[r, inter + i], and dh in fp32. p and 1 - p are within 2^-20 (for G below -87
+ * the step of a subnormal exp(G) comes on top). The gradients of an infinite or NaN G or U are unspecified.
  *   grad_out [rows, k], w2 [E, k, inter], gate_up and grad_gate_up [rows, 2*inter]; grad_gate_up may be gate_up
  *   itself, and overlaps it in no other way; else as above.
  */
@@ -102,8 +102,10 @@ moe_status_t moe_expert_gemm_dswiglu_bf16(moe_mode_t mode, const uint16_t *grad_
  *   An expert without rows gets zeros (accumulate: keeps what it has). What rows outside the experts' counts
  *   hold does not matter. Segments may overlap. fp32 sums in an order that depends on the arguments alone.
  *   m, n             columns of a and of b: multiples of 8, at most 2^24
+ *   rows             (masked: max_tokens_per_expert) at most 2^26 here
  *   grad             type of out: MOE_GRAD_BF16 (rounded once) or MOE_GRAD_FP32
- *   accumulate       0: out is overwritten; 1: the sum is added to it in fp32 (MOE_GRAD_BF16: and rounded)
+ *   accumulate       0: out is overwritten; 1: the sum is added to it in fp32 (MOE_GRAD_FP32: where subnormal
+ *                    values may count as 0; MOE_GRAD_BF16: and rounded)
  *   a [rows, m], b [rows, n] bf16; out [E, m, n]; all 16-byte aligned, out overlaps neither; else as above.
  */
 moe_status_t moe_expert_wgrad_bf16(moe_mode_t mode, const uint16_t *a, const uint16_t *b, int num_experts,

@@ -59,6 +59,7 @@ def test_weight_gradient_arguments():
         assert _wgrad(**kw) == INVALID, kw
     assert _wgrad(E=1025) == UNSUPPORTED and _wgrad(m=1 << 25) == UNSUPPORTED
     assert _wgrad(m=1 << 24, n=1 << 24) == UNSUPPORTED
+    assert _wgrad(M=(1 << 26) + 1) == UNSUPPORTED and _wgrad(mode=0, seg=FAKE, rows=(1 << 26) + 1) == UNSUPPORTED
 
 
 def _combine(**kw):

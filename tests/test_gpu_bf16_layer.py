@@ -107,6 +107,24 @@ def test_serving():
         layer.backward(x)
 
 
+def test_no_tokens():
+    """A step without tokens: no output, and weights' gradients of zero."""
+    m = moe()
+    w13, w2, x, ids, w, _ = _case(4, 64, 32, 2, 10, 6)
+    layer = m.BF16MoELayer(w13, w2, 2, 10, train=True)
+    layer(x, ids, w)
+    layer.backward(x)
+    assert layer.grad_w2.any()
+    assert layer(x[:0], ids[:0], w[:0]).shape == (0, 64)
+    kept = layer.grad_w13.clone()
+    grads = layer.backward(x[:0], accumulate=True)
+    assert torch.equal(grads.w13, kept)
+    layer(x[:0], ids[:0], w[:0])
+    grads = layer.backward(x[:0])
+    layer.check()
+    assert grads.x.shape == (0, 64) and not grads.w13.any() and not grads.w2.any()
+
+
 def test_an_expert_twice_in_a_token():
     m = moe()
     w13, w2, x, ids, w, gen = _case(4, 64, 32, 3, 20, 3)

@@ -343,3 +343,86 @@ def test_streams_graphs_and_repetition():
         torch.cuda.synchronize()
         assert torch.equal(got[0][r.used], want[0][r.used]) and torch.equal(got[1], want[1])
     r.ok()
+
+
+def test_dswiglu_of_far_gates():
+    """Gates and ups up to bf16's ends: no infinity or NaN where the gradient has none, and p's own precision."""
+    m = moe()
+    gates = torch.tensor([0.0, 1e-30, 0.5, 3.0, 20.0, 80.0, 88.0, 95.0, 103.0, 110.0, 300.0, 1e5, 1e20, 3e38], device="cuda")
+    gates = torch.cat([gates, -gates]).bfloat16()
+    ups = torch.tensor([0.0, 1.0, -3.0, 1e-20, 1e10, 1e25, 3e38], device="cuda").bfloat16()
+    I, R = gates.numel() + 4, 7 * 3
+    gu = torch.zeros(R, 2 * I, dtype=torch.bfloat16, device="cuda")
+    gu[:, :gates.numel()] = gates
+    gu[:, I:] = ups.repeat_interleave(3)[:, None]
+    dh = torch.tensor([1.0, 1e-15, -2e10], device="cuda").bfloat16().repeat(7)
+    g = torch.zeros(R, 8, dtype=torch.bfloat16, device="cuda")
+    g[:, 0] = dh
+    w2 = torch.zeros(1, 8, I, dtype=torch.bfloat16, device="cuda")
+    w2[:, 0] = 1
+    out, st = torch.zeros_like(gu), torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.moe_expert_gemm_dswiglu_bf16("normal", g, torch.tensor([R], dtype=torch.int32, device="cuda"), w2, gu, out, st,
+                                   seg_indptr=torch.tensor([0, R], device="cuda"))
+    torch.cuda.synchronize()
+    G, U, D = gu[:, :I].double(), gu[:, I:].double(), dh.double()[:, None]
+    p, q = torch.sigmoid(G), torch.sigmoid(-G)
+    tiny = 2.0 ** -149                  # exp(-|G|) may be off by a subnormal step, and p or q with it
+    for got, want, slope, parts in ((out[:, :I], D * U * p * (1 + G * q), U * (1 + G.abs()), U.abs() * p * (1 + G.abs() * q)),
+                                    (out[:, I:], D * G * p, G, (G * p).abs())):
+        # each product of factors may be rounded to a subnormal too, before dh multiplies it
+        bound = (HALF[torch.bfloat16] + 2.0 ** -18) * want.abs() + D.abs() * (2.0 ** -18 * parts + 2 * tiny * (slope.abs() + 2))
+        most = torch.finfo(torch.bfloat16).max
+        fits = want.abs() + bound < most
+        assert not got.isnan().any()
+        close(got[fits], want[fits], bound[fits] + 2.0 ** -133)
+        over = want.abs() - bound > most    # where the bound itself is that large a value says nothing
+        assert bool(over.any()) and bool((got[over].double().abs() >= 0.98 * most).all())
+
+
+def test_threads_with_sizes_of_their_own():
+    """Host threads whose calls differ in experts, sizes and streams, the kernels' first calls among them."""
+    import threading
+    m = moe()
+    jobs = []
+    for i, (E, n, k) in enumerate([(1, 64, 64), (1024, 8, 16), (16, 520, 136), (200, 40, 72)]):
+        r = Rows("normal", [3] * E, seed=20 + i)
+        a, b, w = r.values(k), r.values(n), r.weights(n, k)
+        jobs.append((r, a, w, b, torch.zeros(r.rows, n, device="cuda").bfloat16(), torch.zeros(E, k, n, device="cuda")))
+    want = []
+    for r, a, w, b, out, grad in jobs:
+        x, v = a[r.used].double(), w.double()[r.expert]
+        y = b[r.used].double().view(r.E, 3, -1)
+        x3 = x.view(r.E, 3, -1)
+        want.append((torch.einsum("rk,rnk->rn", x, v), torch.einsum("rk,rnk->rn", x.abs(), v.abs()),
+                     torch.einsum("erk,ern->ekn", x3, y), torch.einsum("erk,ern->ekn", x3.abs(), y.abs())))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(job):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                _both(m, *job, stream=s)
+            s.synchronize()
+        except Exception as e:          # noqa: BLE001 - reported by the test
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    for (r, a, w, b, out, grad), (y, ymag, g, gmag) in zip(jobs, want):
+        r.ok()
+        close(out, y, HALF[torch.bfloat16] * y.abs() + 1.01 * acc(w.shape[2]) * ymag)
+        close(grad, g, HALF[torch.float32] * g.abs() + 1.01 * acc(3) * gmag)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    m = moe()
+    r = Rows("normal", [3], seed=30)
+    a, w, out = r.values(64), r.weights(64, 64), torch.zeros(3, 64, device="cuda").bfloat16()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        m.moe_expert_gemm_bf16("normal", a, r.count, w, out, r.status, **r.where)
