@@ -254,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     float* staging = reinterpret_cast<float*>(base + kPairRing);
     PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
-    pair_start(s, a.g.rows, a.tiles_n);
+    pair_start(s, a.g.rows, a.tiles_n, kPairEpilogueWarps);
     if (warp == 0) {
         load_role<OP, KN>(a, s, slots, rank, &map_a, &map_a128, &map_w);
     } else if (warp == 1) {

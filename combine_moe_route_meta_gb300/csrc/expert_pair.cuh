@@ -101,10 +101,11 @@ __device__ __forceinline__ int pick_tile_rows(const uint32_t (&tiles)[kRowChoice
     return best;
 }
 
-// The start of a kernel, by all threads of both blocks: barriers, tensor memory, the experts' rows. tiles_n > 0: their row
+// The start of a kernel, by all threads of both blocks: barriers (`readers`: warps of a block that read an accumulator),
+// tensor memory, the experts' rows. tiles_n > 0: their row
 // tiles too, with so many column tiles each; experts that share rows so that there are more tiles than the output could
 // have are refused.
-__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n) {
+__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n, int readers) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
     if (threadIdx.x == 0) {
@@ -114,7 +115,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&s->acc_full[i]), 1);
-            mbar_init(smem_addr(&s->acc_empty[i]), 2 * kPairEpilogueWarps);
+            mbar_init(smem_addr(&s->acc_empty[i]), 2 * readers);
         }
         mbar_fence_init();
         s->dead = 0;

@@ -155,7 +155,8 @@ __device__ __forceinline__ uint32_t pack_sums(const uint32_t* r) {
     return pack_bf16x2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// A warp's 32 rows, 128 bytes of each at a time: lanes have a row each, which goes through shared memory in the 128-byte
+// Groups of four warps take tiles in turn, each an accumulator of its own: what one waits for the other's work hides, which
+// counts where experts are short. A warp's 32 rows, 128 bytes of each at a time: lanes have a row each, which goes through shared memory in the 128-byte
 // swizzle to a tensor store, so that whole lines reach L2 (written by the lanes themselves, 32 bytes in 32 lines at a time,
 // 128 experts' 1536 x 4096 of 512 rows took 906 us). fp32 sums are added to out by the store itself.
 template <bool FP32>
@@ -166,20 +167,18 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
     const uint32_t buffer = staging + (warp - 4) * kStaged, mine = buffer + lane * 128;
     const int pairs = gridDim.x / 2;
-    int n_tile = 0;
+    int n_tile = 0, n_empty = 0;
     for (Tiles t(a, blockIdx.x / 2, pairs); t.e < a.g.rows.E; t.next(a)) {
         const Tile tile(a, s, t);
-        const int m0 = tile.m0 + rank * 128 + quad * 32;
-        const int width = tile.blocks * 64, c0 = group * width;  // the group's half of the columns
+        const int m0 = tile.m0 + rank * 128 + quad * 32, width = tile.blocks * 128;
         const bool sums = tile.rows > 0;
-        if (!sums && a.g.accumulate) continue;
-        const int acc = n_tile & 1;
+        const int turn = sums ? n_tile++ : n_empty++, acc = turn & 1;
+        if (acc != group || (!sums && a.g.accumulate)) continue;
         if (sums) {
-            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1)) break;
+            if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), turn >> 1 & 1)) break;
             tc_fence_after();
-            n_tile++;
         }
-        for (int c = c0; c < c0 + width; c += kCols) {
+        for (int c = 0; c < width; c += kCols) {
             uint32_t w[32] = {};
             if (sums) {
                 if constexpr (FP32) {
@@ -206,7 +205,7 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
 #pragma unroll
                     for (int i = 0; i < 32; i++) w[i] = pack_sums(r + 2 * i);
                 }
-                if (c + kCols == c0 + width) {
+                if (c + kCols == width) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
@@ -240,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t slots = smem_addr(base);
     PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
-    pair_start(s, a.g.rows, 0);
+    pair_start(s, a.g.rows, 0, kPairEpilogueWarps / 2);
     if (warp == 0) {
         load_role(a, s, slots, rank, maps);
     } else if (warp == 1) {
