@@ -8,9 +8,9 @@
 // kGradBlocks blocks sums its rows in registers and writes one line of partial sums; a second kernel adds the lines in order.
 //
 // Bound by DRAM; one GB300, whose copy bandwidth is 6777 GB/s, cold L2:
-//   16384 x 4096, residual:  FP8 72 us (6.5 TB/s), bf16 87 us (6.1), gradient 93 us (5.8)
-//   8192 x 7168:             FP8 65 us (6.4 TB/s), bf16 76 us (6.1), gradient 93 us (5.1)
-//   128 x 7168:              FP8 2.8 us, bf16 2.3 us, gradient 5.4 us (two launches)
+//   16384 x 4096, residual:  FP8 72 us (6.5 TB/s), bf16 87 us (6.1), gradient 90 us (5.9)
+//   8192 x 7168:             FP8 64 us (6.4 TB/s), bf16 76 us (6.1), gradient 89 us (5.3)
+//   128 x 7168:              FP8 2.8 us, bf16 2.3 us, gradient 5.7 us (two launches)
 // One row a block, and no loads ahead: 100, 97 and 147 us for the first.
 #include <cstdint>
 
@@ -247,20 +247,22 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(NormGrad a) {
     }
 }
 
-// grad_weight[c] = the sum of `n` lines: 8 threads a column, then these in order.
-__global__ void __launch_bounds__(256) add_lines_kernel(const float* lines, int n, int H, float* out) {
-    __shared__ float sums[8][32];
+// grad_weight[c] = the sum of `n` lines: up to 32 threads a column, each every 32nd line, then these in order.
+constexpr int kParts = 32;
+__global__ void __launch_bounds__(32 * kParts) add_lines_kernel(const float* lines, int n, int H, float* out) {
+    __shared__ float sums[kParts][32];
     pdl_wait();
     const int c = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
     float s = 0.0f;
-    if (c < H)
-#pragma unroll 8
-        for (int i = part; i < n; i += 8) s += lines[int64_t(i) * H + c];
+    if (c < H) {
+#pragma unroll
+        for (int i = 0; i < (kGradBlocks + kParts - 1) / kParts; i++)
+            if (part + i * kParts < n) s += lines[int64_t(part + i * kParts) * H + c];
+    }
     sums[part][threadIdx.x % 32] = s;
     __syncthreads();
     if (part != 0 || c >= H) return;
-#pragma unroll
-    for (int i = 1; i < 8; i++) s += sums[i][threadIdx.x];
+    for (int i = 1; i < int(blockDim.x) / 32; i++) s += sums[i][threadIdx.x];
     out[c] = s;
 }
 
@@ -345,8 +347,9 @@ cudaError_t launch_rmsnorm_backward(const LaunchCtx& ctx, const NormGrad& a) {
             err = launch_grad<4, false, 1024>(ctx, a, threads);
     }
     if (err != cudaSuccess) return err;
-    return launch_pdl(ctx, add_lines_kernel, dim3(unsigned((a.H + 31) / 32)), dim3(256), 0,
-                      static_cast<const float*>(a.partial), norm_backward_blocks(a.T, a.H), a.H, a.grad_weight);
+    const int lines = norm_backward_blocks(a.T, a.H), parts = lines < 1 ? 1 : lines < kParts ? lines : kParts;
+    return launch_pdl(ctx, add_lines_kernel, dim3(unsigned((a.H + 31) / 32)), dim3(32 * parts), 0,
+                      static_cast<const float*>(a.partial), lines, a.H, a.grad_weight);
 }
 
 }  // namespace moe
