@@ -12,6 +12,12 @@
 // has these bits, and what is missing to 16, the step of a product, likewise in boxes that lie outside of the tensor, which
 // read as zero. (128 experts of 512 +- 21 rows, 1536 x 4096 in bf16: 578 us, with
 // boxes of 8 rows and of one alone 594.)
+//
+// What it measured (one GB300, single passes):
+//   8 experts of 8192 rows, 4096 x 4096 in fp32:            1155 us, 1.90 PFLOP/s
+//   128 experts of 512 +- 21 rows, 1536 x 4096 in fp32:     800 us, 3.2 GB of results beside 8 GB of loads from L2
+//   ... in bf16:                                            579 us, 1.43 PFLOP/s
+//   32 experts of one row, 1040 x 1544 in bf16:             32 us, 3.2 TB/s; without a row 21 us
 #include <cstdint>
 
 #include "expert_pair.cuh"

@@ -12,6 +12,19 @@ FAKE, ODD, TWO = P(0x1000), P(0x1008), P(0x1002)    # never dereferenced: valida
 INVALID, UNSUPPORTED = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
 
 
+def test_header_declares_what_the_library_exports():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "moe_block.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(moe_\w+)\s*\(", text))
+    assert len(names) == 8
+    lib = moe.load_library()
+    for n in names:
+        assert getattr(lib, n).argtypes is not None and hasattr(moe, n), n
+
+
 def _gemm(op, **kw):
     a = dict(mode=1, a=FAKE, E=4, M=8, rows=0, n=64, k=128, seg=None, count=FAKE, weights=0, w=FAKE, out=FAKE, gu=FAKE,
              st=FAKE)
