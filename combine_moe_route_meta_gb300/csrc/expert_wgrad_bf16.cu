@@ -4,14 +4,12 @@
 // Persistent pairs of SMs, each walking over tiles of 256 x 256 results of one expert: the columns of `a` are the M side of
 // the products, 128 in each block, those of `b` the N side, half of them in each block (128 or 256 by what is left of n).
 // Both operands are read as they lie, rows of the summed index with M or N along them, and multiplied along their columns.
-// Warps have roles as in the row products; the epilogue's warps store 128 bytes of 32
-// rows at a time.
+// Warps have roles as in the row products; the epilogue's warps store 128 bytes of 32 rows at a time.
 //
-// The rows behind an expert's last belong to others, or to nobody: they may hold anything, NaNs too, and are summed with.
+// The rows behind an expert's last belong to others, or to nobody: they may hold anything, NaNs too, and must not be summed.
 // So the last slot of a tile ends with the expert's rows: these come in boxes of 32, 16, 8, 4, 2 and 1 rows as their number
 // has these bits, and what is missing to 16, the step of a product, likewise in boxes that lie outside of the tensor, which
-// read as zero. (128 experts of 512 +- 21 rows, 1536 x 4096 in bf16: 578 us, with
-// boxes of 8 rows and of one alone 594.)
+// read as zero. (128 experts of 512 +- 21 rows, 1536 x 4096 in bf16: 578 us, with boxes of 8 rows and of one alone 594.)
 //
 // What it measured (one GB300, single passes):
 //   8 experts of 8192 rows, 4096 x 4096 in fp32:            1155 us, 1.90 PFLOP/s
@@ -42,7 +40,8 @@ struct GradMaps {
 };
 
 // The tiles of a pair, one after the other: the column tiles of an expert with the row tiles of each next to each other. A
-// step adds its quotients and remainders, with carries: with divisions it takes longer than the products of a short expert.
+// step adds its quotients and remainders, with carries, where divisions would take a good part of a short expert's time (32
+// experts of one row, 1040 x 1544: 36.6 -> 35.8 us).
 struct Tiles {
     int e, m, n;             // expert, row tile, column tile
     int step_e, step_m, step_n;
