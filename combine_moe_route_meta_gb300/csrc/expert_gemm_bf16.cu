@@ -185,7 +185,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
         if (!group_all(group, pair_wait(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1))) return;
         tc_fence_after();
         const uint32_t done = leaders(smem_addr(&s->acc_empty[acc]));
-        if (group * kChunkRows >= tile.rows) {
+        if (group * kChunkRows >= tile.rows || n0 >= n) {  // nothing to finish
             if (lane == 0) mbar_arrive_cluster(done);
             continue;
         }

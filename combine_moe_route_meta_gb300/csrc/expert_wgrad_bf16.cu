@@ -175,7 +175,8 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
     int n_tile = 0, n_empty = 0;
     for (Tiles t(a, blockIdx.x / 2, pairs); t.e < a.g.rows.E; t.next(a)) {
         const Tile tile(a, s, t);
-        const int m0 = tile.m0 + rank * 128 + quad * 32, width = tile.blocks * 128;
+        const int m0 = tile.m0 + rank * 128 + quad * 32;
+        const int width = m0 < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;  // columns of the warp's rows
         const bool sums = tile.rows > 0;
         const int turn = sums ? n_tile++ : n_empty++, acc = turn & 1;
         if (acc != group || (!sums && a.g.accumulate)) continue;
@@ -183,6 +184,12 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
             if (!pair_wait_warp(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), turn >> 1 & 1)) break;
             tc_fence_after();
         }
+        const auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
+        };
+        if (sums && width == 0) release();
         for (int c = 0; c < width; c += kCols) {
             uint32_t w[32] = {};
             if (sums) {
@@ -210,11 +217,7 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
 #pragma unroll
                     for (int i = 0; i < 32; i++) w[i] = pack_sums(r + 2 * i);
                 }
-                if (c + kCols == width) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
-                }
+                if (c + kCols >= width) release();
             }
             if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
             __syncwarp();
@@ -225,7 +228,7 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
                              : "memory");
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0 && m0 < a.g.m && tile.n0 + c < a.g.n) {
+            if (lane == 0) {
                 tma_store_3d(map_out, tile.n0 + c, m0, tile.e, buffer, FP32 && a.g.accumulate);
                 bulk_commit();
             }
