@@ -27,12 +27,15 @@ constexpr int kTile = 256;
 constexpr uint32_t kSlot = 2 * kPairBytes;  // 64 rows of 128 columns of a, and of b
 constexpr int kStages = kPairRing / kSlot;
 constexpr uint32_t kStaged = 32 * 128;                              // an epilogue warp's rows on their way out
-constexpr uint32_t kStaging = kPairEpilogueWarps * kStaged;
-static_assert(1024 + kPairRing + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of an SM");
+constexpr uint32_t kStaging = kPairEpilogueWarps * kStaged;         // of one buffer a warp
+constexpr size_t shared_bytes(int E, int buffers) { return 1024 + kPairRing + buffers * kStaging + pair_shared_bytes(E); }
+constexpr size_t kSharedMost = 227 * 1024;
+static_assert(shared_bytes(MOE_MAX_EXPERTS, 1) <= kSharedMost, "shared memory of an SM");
 
 struct GradArgs {
     WeightGrad g;
     int tiles_m, tiles_n;
+    int buffers;  // of a warp: 1 or 2
 };
 constexpr int kBoxes = 7;
 struct GradMaps {
@@ -170,7 +173,8 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
     constexpr int kCols = FP32 ? 32 : 64;
     const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
-    const uint32_t buffer = staging + (warp - 4) * kStaged, mine = buffer + lane * 128;
+    const uint32_t first = staging + (warp - 4) * a.buffers * kStaged, other = (a.buffers - 1) * kStaged;
+    uint32_t at = 0;
     const int pairs = gridDim.x / 2;
     int n_tile = 0, n_empty = 0;
     for (Tiles t(a, blockIdx.x / 2, pairs); t.e < a.g.rows.E; t.next(a)) {
@@ -219,8 +223,16 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
                 }
                 if (c + kCols >= width) release();
             }
-            if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+            // the last store from the buffer has read it
+            if (lane == 0) {
+                if (other)
+                    bulk_wait_read<1>();
+                else
+                    bulk_wait_read<0>();
+            }
             __syncwarp();
+            const uint32_t buffer = first + at, mine = buffer + lane * 128;
+            at ^= other;
 #pragma unroll
             for (int i = 0; i < 8; i++)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)),
@@ -245,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
-    PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
+    PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + a.buffers * kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, 0, kPairEpilogueWarps / 2);
     if (warp == 0) {
@@ -262,9 +274,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& g) {
     auto kern = g.fp32 ? weight_grad_kernel<true> : weight_grad_kernel<false>;
-    constexpr size_t smem = 1024 + size_t(kPairRing) + kStaging;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
-    const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
+    const cudaError_t err = allow_shared_memory(kern, kSharedMost);
     if (err != cudaSuccess) return err;
     GradMaps maps{};
     CUtensorMap map_out;
@@ -278,8 +289,9 @@ cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& g) {
     }
     if (!(g.fp32 ? make_map_fp32(&map_out, g.out, 3, dout, bout) : make_map_bf16(&map_out, g.out, 3, dout, bout)))
         return cudaErrorInvalidValue;
-    const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile};
-    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, maps, map_out);
+    const int buffers = shared_bytes(g.rows.E, 2) <= kSharedMost ? 2 : 1;
+    const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile, buffers};
+    return launch_pairs(ctx, kern, shared_bytes(g.rows.E, buffers), a, maps, map_out);
 }
 
 }  // namespace moe
