@@ -170,7 +170,7 @@ __device__ __forceinline__ uint32_t pack_sums(const uint32_t* r) {
 template <bool FP32>
 __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, uint32_t staging, int rank, int warp,
                                               const CUtensorMap* map_out) {
-    constexpr int kCols = FP32 ? 32 : 64;
+    constexpr int kCols = FP32 ? 32 : 64, kPieces = FP32 ? 2 : 2;
     const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
     const uint32_t first = staging + (warp - 4) * a.buffers * kStaged, other = (a.buffers - 1) * kStaged;
@@ -194,12 +194,16 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
             if (lane == 0) mbar_arrive_cluster(leaders(smem_addr(&s->acc_empty[acc])));
         };
         if (sums && width == 0) release();
-        for (int c = 0; c < width; c += kCols) {
-            uint32_t w[32] = {};
-            if (sums) {
+        // bf16: two pieces at a time, so that the accumulator is free a piece earlier
+        for (int c0 = 0; c0 < width; c0 += kPieces * kCols) {
+            uint32_t w[kPieces][32] = {};
+#pragma unroll
+            for (int i = 0; i < kPieces; i++) {
+                const int c = c0 + i * kCols;
+                if (!sums || c >= width) break;
                 if constexpr (FP32) {
-                    tmem_load32(tmem + acc * kTile + c, w);
-                    tmem_wait(w, 32);
+                    tmem_load32(tmem + acc * kTile + c, w[i]);
+                    tmem_wait(w[i], 32);
                 } else {
                     uint32_t r[64];
                     tmem_load32(tmem + acc * kTile + c, r);
@@ -209,42 +213,47 @@ __device__ __forceinline__ void epilogue_role(const GradArgs& a, PairShared* s, 
                         const uint16_t* p = static_cast<const uint16_t*>(a.g.out) +
                                             (int64_t(tile.e) * a.g.m + m0 + lane) * a.g.n + tile.n0 + c;
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            if (tile.n0 + c + i * 8 >= a.g.n) break;
+                        for (int j = 0; j < 8; j++) {
+                            if (tile.n0 + c + j * 8 >= a.g.n) break;
                             float x[8];
-                            unpack8(*reinterpret_cast<const uint4*>(p + i * 8), x);
+                            unpack8(*reinterpret_cast<const uint4*>(p + j * 8), x);
 #pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                r[i * 8 + j] = __float_as_uint(__uint_as_float(r[i * 8 + j]) + x[j]);
+                            for (int l = 0; l < 8; l++)
+                                r[j * 8 + l] = __float_as_uint(__uint_as_float(r[j * 8 + l]) + x[l]);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i++) w[i] = pack_sums(r + 2 * i);
+                    for (int j = 0; j < 32; j++) w[i][j] = pack_sums(r + 2 * j);
                 }
-                if (c + kCols >= width) release();
             }
-            // the last store from the buffer has read it
-            if (lane == 0) {
-                if (other)
-                    bulk_wait_read<1>();
-                else
-                    bulk_wait_read<0>();
-            }
-            __syncwarp();
-            const uint32_t buffer = first + at, mine = buffer + lane * 128;
-            at ^= other;
+            if (sums && c0 + kPieces * kCols >= width) release();
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)),
-                             "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
-                             : "memory");
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_3d(map_out, tile.n0 + c, m0, tile.e, buffer, FP32 && a.g.accumulate);
-                bulk_commit();
+            for (int i = 0; i < kPieces; i++) {
+                const int c = c0 + i * kCols;
+                if (c >= width) break;
+                // the last store from the buffer has read it
+                if (lane == 0) {
+                    if (other)
+                        bulk_wait_read<1>();
+                    else
+                        bulk_wait_read<0>();
+                }
+                __syncwarp();
+                const uint32_t buffer = first + at, mine = buffer + lane * 128;
+                at ^= other;
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((j ^ (lane & 7)) << 4)),
+                                 "r"(w[i][4 * j]), "r"(w[i][4 * j + 1]), "r"(w[i][4 * j + 2]), "r"(w[i][4 * j + 3])
+                                 : "memory");
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(map_out, tile.n0 + c, m0, tile.e, buffer, FP32 && a.g.accumulate);
+                    bulk_commit();
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
     if (lane == 0) bulk_wait_all();
