@@ -47,7 +47,7 @@ struct GemmArgs {
 
 struct Tile {
     int e, n0, row0, rows;  // expert, first column, first row, rows
-    // N of the products; each block loads half of it, in boxes of 16 rows
+    // N of the products; each block loads half of it
     __device__ __forceinline__ int n() const { return (rows + 31) & ~31; }
 };
 
@@ -82,10 +82,14 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
 __device__ __forceinline__ uint32_t slot_bytes(const PairShared* s) { return kPairBytes + uint32_t((s->most + 31) & ~31) * 64; }
 __device__ __forceinline__ int ring_slots(uint32_t slot) { return min(kPairSlots, int(kPairRing / slot)); }
 
+constexpr int kBoxes = 4;
+struct RowMaps {
+    CUtensorMap a[kBoxes];  // boxes of 64 values x 128, 64, 32, 16 rows
+};
+
 // A whole warp; one lane issues, with operands that are the same in all lanes.
 template <RowOp OP, bool KN>
-__device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank,
-                                          const CUtensorMap* map_a, const CUtensorMap* map_a128,
+__device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint32_t slots, int rank, const RowMaps& maps,
                                           const CUtensorMap* map_w) {
     const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n;
     const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
@@ -96,10 +100,10 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
         const Tile tile = find_tile<OP>(a, s, t);
-        const int half = tile.n() / 2, boxes = half / 16;
+        const int half = tile.n() / 2;
         const int row0 = tile.row0 + rank * half;
         const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
-        const uint32_t bytes = 2 * (kPairBytes + boxes * 2048);
+        const uint32_t bytes = 2 * (kPairBytes + half * 128);
         for (int c = 0; c < a.chunks; c++) {
             if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
             if (leader) {
@@ -113,11 +117,14 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
                     // (k, column, half, expert); SwiGLU: 64 columns of both halves
                     pair_load_4d(slot, map_w, k0, n0, 0, tile.e, bar);
                 }
-                if (boxes == 8) {
-                    pair_load_2d(slot + kPairBytes, map_a128, k0, row0, bar);
-                } else {
-                    for (int i = 0; i < boxes; i++)
-                        pair_load_2d(slot + kPairBytes + i * 2048, map_a, k0, row0 + i * 16, bar);
+                int at = 0;
+#pragma unroll
+                for (int i = 0; i < kBoxes; i++) {
+                    const int box = 128 >> i;
+                    if (half & box) {
+                        pair_load_2d(slot + kPairBytes + at * 128, &maps.a[i], k0, row0 + at, bar);
+                        at += box;
+                    }
                 }
             }
             __syncwarp();
@@ -256,8 +263,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
 
 template <RowOp OP, bool KN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    row_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap map_a,
-                    const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_w) {
+    row_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ RowMaps maps,
+                    const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
@@ -266,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, a.tiles_n, kPairEpilogueWarps);
     if (warp == 0) {
-        load_role<OP, KN>(a, s, slots, rank, &map_a, &map_a128, &map_w);
+        load_role<OP, KN>(a, s, slots, rank, maps, &map_w);
     } else if (warp == 1) {
         if (rank == 0) mma_role<OP, KN>(a, s, slots);
     } else if (warp >= 4) {
@@ -285,14 +292,17 @@ cudaError_t launch(const LaunchCtx& ctx, const RowGemm& g) {
     constexpr uint64_t halves = OP == RowOp::kSwiglu ? 2 : 1;
     const uint64_t k = uint64_t(g.k), n = uint64_t(g.n), E = uint64_t(g.rows.E);
     const uint64_t da[2] = {k, uint64_t(g.rows.rows)}, dnk[4] = {k, n, halves, E}, dkn[3] = {n, k, E};
-    const uint32_t ba[2] = {kPairK, 16}, ba128[2] = {kPairK, 128}, bnk[4] = {kPairK, uint32_t(128 / halves), halves, 1},
-                   bkn[3] = {64, kPairK, 1};
-    CUtensorMap map_a, map_a128, map_w;
-    if (!make_map_bf16(&map_a, g.a, 2, da, ba) || !make_map_bf16(&map_a128, g.a, 2, da, ba128) ||
-        !(KN ? make_map_bf16(&map_w, g.w, 3, dkn, bkn) : make_map_bf16(&map_w, g.w, 4, dnk, bnk)))
+    const uint32_t bnk[4] = {kPairK, uint32_t(128 / halves), halves, 1}, bkn[3] = {64, kPairK, 1};
+    RowMaps maps;
+    CUtensorMap map_w;
+    for (int i = 0; i < kBoxes; i++) {
+        const uint32_t box[2] = {kPairK, 128u >> i};
+        if (!make_map_bf16(&maps.a[i], g.a, 2, da, box)) return cudaErrorInvalidValue;
+    }
+    if (!(KN ? make_map_bf16(&map_w, g.w, 3, dkn, bkn) : make_map_bf16(&map_w, g.w, 4, dnk, bnk)))
         return cudaErrorInvalidValue;
     const GemmArgs a{g, (g.k + kPairK - 1) / kPairK, (g.n + kTileCols<OP> - 1) / kTileCols<OP>};
-    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, map_a, map_a128, map_w);
+    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, maps, map_w);
 }
 
 }  // namespace
