@@ -73,17 +73,11 @@ struct Tile {
           blocks(a.g.n - n0 > kTile / 2 ? 2 : 1) {}
 };
 
-// One box of every block of 64 columns: `blocks` of them, of a and then of b, to rows at `to` of the slot.
-__device__ __forceinline__ void load_boxes(const CUtensorMap* a, const CUtensorMap* b, uint32_t to, int blocks, int m, int n,
-                                           int row, uint32_t bar) {
-    pair_load_2d(to, a, m, row, bar);
-    pair_load_2d(to + kPairBytes / 2, a, m + 64, row, bar);
-    pair_load_2d(to + kPairBytes, b, n, row, bar);
-    if (blocks == 4) pair_load_2d(to + kPairBytes + kPairBytes / 2, b, n + 64, row, bar);
-}
-
-// A whole warp; one lane issues, with operands that are the same in all lanes (others cost 60 % more time for a slot).
-__device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint32_t slots, int rank, const GradMaps& maps) {
+// A whole warp for each operand; one lane issues, with operands that are the same in all lanes (others cost 60 % more time
+// for a slot).
+template <bool B>
+__device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint32_t slots, int rank,
+                                          const CUtensorMap* maps) {
     const int pairs = gridDim.x / 2;
     const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
     const uint32_t leader = elect_one();
@@ -91,27 +85,33 @@ __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint
     uint32_t ph = 0;
     for (Tiles t(a, blockIdx.x / 2, pairs); t.e < a.g.rows.E; t.next(a)) {
         const Tile tile(a, s, t);
-        const int blocks = 2 + tile.blocks, m = tile.m0 + rank * 128, n = tile.n0 + rank * tile.blocks * 64;
+        const int blocks = 2 + tile.blocks, x = B ? tile.n0 + rank * tile.blocks * 64 : tile.m0 + rank * 128;
+        const bool second = !B || tile.blocks == 2;
         for (int r0 = 0; r0 < tile.rows; r0 += kPairK) {
             if (!pair_wait_warp(s, a.g.rows.status, empty + 8 * st, ph ^ 1)) return;
             if (leader) {
-                const uint32_t bar = counted + 8 * st, slot = slots + st * kSlot;
+                const uint32_t bar = counted + 8 * st, slot = slots + st * kSlot + (B ? kPairBytes : 0);
                 const int rem = min(kPairK, tile.rows - r0), row = tile.row0 + r0;
-                if (rank == 0) mbar_expect_tx(own + 8 * st, 2 * blocks * ((rem + 15) & ~15) * 128);
+                // one box of each block of 64 columns, to rows at `to` of the slot
+                const auto load = [&](int i, int to, int from) {
+                    pair_load_2d(slot + to * 128, maps + i, x, from, bar);
+                    if (second) pair_load_2d(slot + kPairBytes / 2 + to * 128, maps + i, x + 64, from, bar);
+                };
+                if (!B && rank == 0) mbar_expect_tx(own + 8 * st, 2 * blocks * ((rem + 15) & ~15) * 128);
                 if (rem == kPairK) {
-                    load_boxes(&maps.a[0], &maps.b[0], slot, blocks, m, n, row, bar);
+                    load(0, 0, row);
                 } else {
                     const int gap = -rem & 15;
                     int at = 0;
                     for (int i = 1, rows = 32; i < kBoxes; i++, rows /= 2) {
                         if (rem & rows) {
-                            load_boxes(&maps.a[i], &maps.b[i], slot + at * 128, blocks, m, n, row + at, bar);
+                            load(i, at, row + at);
                             at += rows;
                         }
                     }
                     for (int i = 3, rows = 8; i < kBoxes; i++, rows /= 2) {
                         if (gap & rows) {
-                            load_boxes(&maps.a[i], &maps.b[i], slot + at * 128, blocks, m, n, -rows, bar);
+                            load(i, at, -rows);
                             at += rows;
                         }
                     }
@@ -121,7 +121,7 @@ __device__ __forceinline__ void load_role(const GradArgs& a, PairShared* s, uint
             if (++st == kStages) st = 0, ph ^= 1;
         }
     }
-    pair_drain(s, a.g.rows.status, st, ph, kStages);
+    if (!B) pair_drain(s, a.g.rows.status, st, ph, kStages);
 }
 
 // A whole warp of the leading block; one lane issues.
@@ -270,7 +270,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, 0, kPairEpilogueWarps / 2);
     if (warp == 0) {
-        load_role(a, s, slots, rank, maps);
+        load_role<false>(a, s, slots, rank, maps.a);
+    } else if (warp == 2) {
+        load_role<true>(a, s, slots, rank, maps.b);
     } else if (warp == 1) {
         if (rank == 0) mma_role(a, s, slots);
     } else if (warp >= 4) {
