@@ -41,18 +41,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Stores a box of shared memory (add: adds it, in the type of the map), in the issuing thread's bulk group. What lies outside
-// the tensor is left out; no coordinate is negative.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src, bool add) {
-    if (add)
-        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                         map),
-                     "r"(x), "r"(y), "r"(z), "r"(src)
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                     "r"(x), "r"(y), "r"(z), "r"(src)
-                     : "memory");
+// Stores a box of shared memory, in the issuing thread's bulk group. What lies outside the tensor is left out; no coordinate
+// is negative.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(src)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------------------

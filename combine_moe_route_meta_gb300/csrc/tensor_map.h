@@ -43,12 +43,9 @@ inline bool make_map(CUtensorMap* map, const void* p, int rank, const uint64_t* 
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same of bf16 values, in boxes of 64 values a row, and of fp32 values, in boxes of 32.
+// The same of bf16 values, in boxes of 64 values a row.
 inline bool make_map_bf16(CUtensorMap* map, const void* p, int rank, const uint64_t* dims, const uint32_t* box) {
     return make_map(map, p, rank, dims, box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
-}
-inline bool make_map_fp32(CUtensorMap* map, const void* p, int rank, const uint64_t* dims, const uint32_t* box) {
-    return make_map(map, p, rank, dims, box, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4);
 }
 
 }  // namespace moe
