@@ -279,9 +279,14 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
         const Tile tile(a, s, t);
         const bool sums = tile.rows > 0;
         if (!me.takes(sums) || (!sums && a.g.accumulate)) continue;
-        if (sums && !me.wait(a.g.rows.status)) break;
         const int m0 = tile.m0 + me.first;
         const int width = m0 < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;  // columns of the warp's rows
+        // accumulate: the lane's row, on its way to L2 beside the products
+        const uint16_t* old = static_cast<const uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + m0 + me.lane) * a.g.n + tile.n0;
+        const bool add = a.g.accumulate && m0 + me.lane < a.g.m;
+        if (add)
+            for (int c = 0; c < width; c += kCols) asm volatile("prefetch.global.L2 [%0];" ::"l"(old + c));
+        if (sums && !me.wait(a.g.rows.status)) break;
         if (sums && width == 0) me.release();
         for (int c0 = 0; c0 < width; c0 += kPieces * kCols) {
             uint32_t w[kPieces][32] = {};
@@ -293,17 +298,18 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
                 tmem_load32(me.columns(c), r);
                 tmem_load32(me.columns(c + 32), r + 32);
                 tmem_wait(r, 64);
-                if (a.g.accumulate && m0 + me.lane < a.g.m) {
-                    const uint16_t* p = static_cast<const uint16_t*>(a.g.out) +
-                                        (int64_t(tile.e) * a.g.m + m0 + me.lane) * a.g.n + tile.n0 + c;
+                if (add) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        x[j] = c + j * 8 < width ? *reinterpret_cast<const uint4*>(old + c + j * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        if (tile.n0 + c + j * 8 >= a.g.n) break;
-                        float x[8];
-                        unpack8(*reinterpret_cast<const uint4*>(p + j * 8), x);
+                        float f[8];
+                        unpack8(x[j], f);
 #pragma unroll
                         for (int l = 0; l < 8; l++)
-                            r[j * 8 + l] = __float_as_uint(__uint_as_float(r[j * 8 + l]) + x[l]);
+                            r[j * 8 + l] = __float_as_uint(__uint_as_float(r[j * 8 + l]) + f[l]);
                     }
                 }
 #pragma unroll
