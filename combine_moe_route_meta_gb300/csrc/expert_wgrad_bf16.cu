@@ -212,51 +212,60 @@ struct EpilogueWarp {
     }
 };
 
-// A lane's column of up to 32 rows to p and the rows behind it. No test stands between whole pieces' stores: with one at each,
-// 128 experts take 1080 us for 700.
-template <bool ADD>
-__device__ __forceinline__ void put_column(float* p, int64_t stride, const uint32_t (&r)[32], int rows) {
-    const auto put = [&](int i) {
-        if constexpr (ADD)
-            asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p + i * stride), "f"(__uint_as_float(r[i])) : "memory");
-        else
-            p[i * stride] = __uint_as_float(r[i]);
-    };
+// A lane's column of up to 32 rows, from p and the rows behind it, or to them. No test stands between whole pieces' accesses:
+// with one at each store, 128 experts take 1080 us for 700.
+__device__ __forceinline__ void get_column(float (&r)[32], const float* p, int64_t stride, int rows) {
     if (rows >= 32) {
 #pragma unroll
-        for (int i = 0; i < 32; i++) put(i);
+        for (int i = 0; i < 32; i++) r[i] = p[i * stride];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++) r[i] = i < rows ? p[i * stride] : 0.0f;
+    }
+}
+__device__ __forceinline__ void put_column(float* p, int64_t stride, const float (&r)[32], int rows) {
+    if (rows >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; i++) p[i * stride] = r[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 32; i++)
-            if (i < rows) put(i);
+            if (i < rows) p[i * stride] = r[i];
     }
 }
 // Lanes are columns of out.
+template <bool ADD>
 __device__ __forceinline__ void epilogue_fp32(const GradArgs& a, PairShared* s, int rank, int warp) {
     EpilogueWarp me(s, rank, warp);
     const int64_t stride = a.g.m;
-    const bool add = a.g.accumulate;
     for (Tiles<float> t(a, blockIdx.x / 2, gridDim.x / 2); t.e < a.g.rows.E; t.next()) {
         const Tile tile(a, s, t);
         const bool sums = tile.rows > 0;
-        if (!me.takes(sums) || (!sums && add)) continue;
-        if (sums && !me.wait(a.g.rows.status)) break;
+        if (!me.takes(sums) || (!sums && ADD)) continue;
         const int column = tile.m0 + me.first + me.lane;
         const int rows = tile.m0 + me.first < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;
-        if (sums && rows == 0) me.release();
+        const int mine = column < a.g.m ? rows : 0;
         float* p = static_cast<float*>(a.g.out) + (int64_t(tile.e) * a.g.n + tile.n0) * stride + column;
+        float old[32];
+        if (ADD) get_column(old, p, stride, mine);
+        if (sums && !me.wait(a.g.rows.status)) break;
+        if (sums && rows == 0) me.release();
         for (int c = 0; c < rows; c += 32, p += 32 * stride) {
-            uint32_t r[32] = {};
+            uint32_t w[32] = {};
             if (sums) {
-                tmem_load32(me.columns(c), r);
-                tmem_wait(r, 32);
+                tmem_load32(me.columns(c), w);
+                tmem_wait(w, 32);
                 if (c + 32 >= rows) me.release();
             }
-            const int left = column < a.g.m ? rows - c : 0;
-            if (add)
-                put_column<true>(p, stride, r, left);
-            else
-                put_column<false>(p, stride, r, left);
+            float r[32];
+#pragma unroll
+            for (int i = 0; i < 32; i++) r[i] = __uint_as_float(w[i]);
+            if (ADD) {
+#pragma unroll
+                for (int i = 0; i < 32; i++) r[i] += old[i];
+                if (c + 32 < rows) get_column(old, p + 32 * stride, stride, mine - c - 32);
+            }
+            put_column(p, stride, r, mine - c);
             __syncwarp();
         }
     }
@@ -270,6 +279,7 @@ __device__ __forceinline__ uint32_t pack_sums(const uint32_t* r) {
 // Lanes are rows of out. A warp's 32 rows, 128 bytes of each at a time, go through shared memory in the 128-byte swizzle to
 // a tensor store. Two pieces are taken before they are written, so that the accumulator is free a piece earlier (32 experts
 // of one row 31.5 -> 29.4 us).
+template <bool ADD>
 __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, uint32_t staging, int rank, int warp,
                                               const CUtensorMap* map_out) {
     constexpr int kCols = 64, kPieces = 2;
@@ -278,12 +288,12 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
     for (Tiles<uint16_t> t(a, blockIdx.x / 2, gridDim.x / 2); t.e < a.g.rows.E; t.next()) {
         const Tile tile(a, s, t);
         const bool sums = tile.rows > 0;
-        if (!me.takes(sums) || (!sums && a.g.accumulate)) continue;
+        if (!me.takes(sums) || (!sums && ADD)) continue;
         const int m0 = tile.m0 + me.first;
         const int width = m0 < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;  // columns of the warp's rows
         // accumulate: the lane's row, on its way to L2 beside the products
         const uint16_t* old = static_cast<const uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + m0 + me.lane) * a.g.n + tile.n0;
-        const bool add = a.g.accumulate && m0 + me.lane < a.g.m;
+        const bool add = ADD && m0 + me.lane < a.g.m;
         if (add)
             for (int c = 0; c < width; c += kCols) asm volatile("prefetch.global.L2 [%0];" ::"l"(old + c));
         if (sums && !me.wait(a.g.rows.status)) break;
@@ -340,7 +350,7 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
     if (me.lane == 0) bulk_wait_all();
 }
 
-template <typename T>
+template <typename T, bool ADD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     weight_grad_kernel(const __grid_constant__ GradArgs a, const __grid_constant__ GradMaps maps,
                        const __grid_constant__ CUtensorMap map_out) {
@@ -358,9 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (rank == 0) mma_role<T>(a, s, slots);
     } else if (warp >= 4) {
         if constexpr (kFp32<T>)
-            epilogue_fp32(a, s, rank, warp);
+            epilogue_fp32<ADD>(a, s, rank, warp);
         else
-            epilogue_bf16(a, s, slots + a.slots * kSlot, rank, warp, &map_out);
+            epilogue_bf16<ADD>(a, s, slots + a.slots * kSlot, rank, warp, &map_out);
     }
     pair_end(s);
 }
@@ -368,7 +378,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }  // namespace
 
 cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& grad) {
-    auto kern = grad.fp32 ? weight_grad_kernel<float> : weight_grad_kernel<uint16_t>;
+    auto kern = grad.fp32 ? (grad.accumulate ? weight_grad_kernel<float, true> : weight_grad_kernel<float, false>)
+                          : (grad.accumulate ? weight_grad_kernel<uint16_t, true> : weight_grad_kernel<uint16_t, false>);
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
     const cudaError_t err = allow_shared_memory(kern, kSharedMost);
     if (err != cudaSuccess) return err;

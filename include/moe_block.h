@@ -104,8 +104,7 @@ moe_status_t moe_expert_gemm_dswiglu_bf16(moe_mode_t mode, const uint16_t *grad_
  *   m, n             columns of a and of b: multiples of 8, at most 2^24
  *   rows             (masked: max_tokens_per_expert) at most 2^26 here
  *   grad             type of out: MOE_GRAD_BF16 (rounded once) or MOE_GRAD_FP32
- *   accumulate       0: out is overwritten; 1: the sum is added to it in fp32 (MOE_GRAD_FP32: where subnormal
- *                    values may count as 0; MOE_GRAD_BF16: and rounded)
+ *   accumulate       0: out is overwritten; 1: the sum is added to it in fp32 (MOE_GRAD_BF16: and rounded)
  *   a [rows, m], b [rows, n] bf16; out [E, m, n]; all 16-byte aligned, out overlaps neither; else as above.
  */
 moe_status_t moe_expert_wgrad_bf16(moe_mode_t mode, const uint16_t *a, const uint16_t *b, int num_experts,
