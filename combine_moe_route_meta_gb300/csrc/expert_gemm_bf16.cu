@@ -35,14 +35,18 @@ constexpr int kMaxRows = 256;  // of a tile
 constexpr int kCols = 256;
 constexpr int kChunkRows = 16;                               // rows of the accumulator at a time
 constexpr uint32_t kStaged = kChunkRows * 128 * 4;           // ... of a block's 128 columns in fp32
-constexpr uint32_t kStaging = 2 * 2 * kStaged;               // two groups of four epilogue warps, two buffers each
-static_assert(1024 + kPairRing + kStaging + pair_shared_bytes(MOE_MAX_EXPERTS) <= 227 * 1024,
-              "shared memory of an SM");
+constexpr uint32_t kStaging = 2 * kStaged;                   // two groups of four epilogue warps
+// Bytes of the ring: what is left, in swizzle atoms.
+constexpr uint32_t ring_bytes(int E) {
+    return uint32_t(kPairShared - 1024 - kStaging - pair_shared_bytes(E)) / 1024 * 1024;
+}
+static_assert(ring_bytes(MOE_MAX_EXPERTS) >= 6 * 2 * kPairBytes, "six slots of the largest tiles");
 
 struct GemmArgs {
     RowGemm g;
     int chunks;   // slots per tile: ceil(k / kPairK)
     int tiles_n;  // column tiles
+    uint32_t ring;
 };
 
 struct Tile {
@@ -80,7 +84,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
 // Bytes of a slot, a multiple of the swizzle's atoms, and how many there are: by the largest tile. One token's 8 experts of
 // 2 x 768 x 4096: 18.4 us, with five slots of 32 KB 20.0; 128 experts of 32 rows, 4096 x 2048: 331 and 349 us.
 __device__ __forceinline__ uint32_t slot_bytes(const PairShared* s) { return kPairBytes + uint32_t((s->most + 31) & ~31) * 64; }
-__device__ __forceinline__ int ring_slots(uint32_t slot) { return min(kPairSlots, int(kPairRing / slot)); }
+__device__ __forceinline__ int ring_slots(const GemmArgs& a, uint32_t slot) { return min(kPairSlots, int(a.ring / slot)); }
 
 constexpr int kBoxes = 4;
 struct RowMaps {
@@ -95,7 +99,7 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
     const uint32_t own = smem_addr(s->full), counted = leaders(own), empty = smem_addr(s->empty);
     const uint32_t leader = elect_one();
     const uint32_t slot_size = uniform(slot_bytes(s));
-    const int stages = uniform(ring_slots(slot_size));
+    const int stages = uniform(ring_slots(a, slot_size));
     int st = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
@@ -143,7 +147,7 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, PairShared* s, uint3
     const int last = (a.g.k - (a.chunks - 1) * kPairK + 15) / 16;  // steps of 16 in the last slot
     const uint32_t leader = elect_one();
     const uint32_t slot_size = uniform(slot_bytes(s));
-    const int stages = uniform(ring_slots(slot_size));
+    const int stages = uniform(ring_slots(a, slot_size));
     int st = 0, n_tile = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
@@ -183,8 +187,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
     const int lane = threadIdx.x % 32, quad = warp % 4, group = (warp - 4) / 4;
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
     const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n, n = a.g.n;
-    float* buffers = staging + group * (2 * kStaged / 4);
-    int n_tile = 0, turn = 0;
+    float* stage = staging + group * (kStaged / 4);
+    int n_tile = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
         const Tile tile = find_tile<OP>(a, s, t);
         const int acc = n_tile & 1;
@@ -217,10 +221,9 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(done);
             }
-            float* stage = buffers + (turn ^= 1) * (kStaged / 4);
+            group_sync(group);  // what was there before has been read
 #pragma unroll
             for (int j = 0; j < kChunkRows; j++) stage[j * 128 + quad * 32 + lane] = v[j];
-            // one barrier for two buffers: who writes this one again has passed the next one's barrier, as has who reads it
             group_sync(group);
             if constexpr (OP == RowOp::kSwiglu) {
 #pragma unroll
@@ -268,8 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // slots on swizzle atoms
     const uint32_t slots = smem_addr(base);
-    float* staging = reinterpret_cast<float*>(base + kPairRing);
-    PairShared* s = reinterpret_cast<PairShared*>(base + kPairRing + kStaging);
+    float* staging = reinterpret_cast<float*>(base + a.ring);
+    PairShared* s = reinterpret_cast<PairShared*>(base + a.ring + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
     pair_start(s, a.g.rows, a.tiles_n, kPairEpilogueWarps);
     if (warp == 0) {
@@ -285,9 +288,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <RowOp OP, bool KN>
 cudaError_t launch(const LaunchCtx& ctx, const RowGemm& g) {
     auto kern = row_gemm_kernel<OP, KN>;
-    constexpr size_t smem = 1024 + size_t(kPairRing) + kStaging;
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
-    const cudaError_t err = allow_shared_memory(kern, smem + pair_shared_bytes(MOE_MAX_EXPERTS));
+    const cudaError_t err = allow_shared_memory(kern, kPairShared);
     if (err != cudaSuccess) return err;
     constexpr uint64_t halves = OP == RowOp::kSwiglu ? 2 : 1;
     const uint64_t k = uint64_t(g.k), n = uint64_t(g.n), E = uint64_t(g.rows.E);
@@ -301,8 +303,8 @@ cudaError_t launch(const LaunchCtx& ctx, const RowGemm& g) {
     }
     if (!(KN ? make_map_bf16(&map_w, g.w, 3, dkn, bkn) : make_map_bf16(&map_w, g.w, 4, dnk, bnk)))
         return cudaErrorInvalidValue;
-    const GemmArgs a{g, (g.k + kPairK - 1) / kPairK, (g.n + kTileCols<OP> - 1) / kTileCols<OP>};
-    return launch_pairs(ctx, kern, smem + pair_shared_bytes(g.rows.E), a, maps, map_w);
+    const GemmArgs a{g, (g.k + kPairK - 1) / kPairK, (g.n + kTileCols<OP> - 1) / kTileCols<OP>, ring_bytes(g.rows.E)};
+    return launch_pairs(ctx, kern, 1024 + a.ring + kStaging + pair_shared_bytes(g.rows.E), a, maps, map_w);
 }
 
 }  // namespace

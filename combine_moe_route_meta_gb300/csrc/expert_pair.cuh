@@ -13,8 +13,8 @@ namespace moe {
 
 constexpr int kPairK = 64;                                 // values of the summed index in a slot: rows of 128 bytes
 constexpr uint32_t kPairBytes = 128 * 128;                 // 128 of these rows: an operand's part of a slot in one block
-constexpr uint32_t kPairRing = 10 * kPairBytes;            // of slots
-constexpr int kPairSlots = 10;                             // at most
+constexpr int kPairSlots = 12;                             // of a ring, at most
+constexpr size_t kPairShared = 227 * 1024;                 // shared memory of a block, at most
 constexpr int kPairEpilogueWarps = 8;
 constexpr int kPairWarps = 4 + kPairEpilogueWarps;         // 0: loads, 1: products, 2, 3: none
 constexpr int kPairThreads = kPairWarps * 32;

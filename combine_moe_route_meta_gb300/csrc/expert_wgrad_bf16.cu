@@ -39,8 +39,7 @@ template <typename T>
 constexpr size_t shared_bytes(int slots, int E) {
     return 1024 + slots * kSlot + (kFp32<T> ? 0 : kStaging) + pair_shared_bytes(E);
 }
-constexpr size_t kSharedMost = 227 * 1024;
-static_assert(shared_bytes<float>(6, MOE_MAX_EXPERTS) <= kSharedMost && shared_bytes<uint16_t>(5, MOE_MAX_EXPERTS) <= kSharedMost,
+static_assert(shared_bytes<float>(6, MOE_MAX_EXPERTS) <= kPairShared && shared_bytes<uint16_t>(5, MOE_MAX_EXPERTS) <= kPairShared,
               "shared memory of an SM");
 
 struct GradArgs {
@@ -381,7 +380,7 @@ cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& grad) {
     auto kern = grad.fp32 ? (grad.accumulate ? weight_grad_kernel<float, true> : weight_grad_kernel<float, false>)
                           : (grad.accumulate ? weight_grad_kernel<uint16_t, true> : weight_grad_kernel<uint16_t, false>);
     // first: it makes the device's context current in a thread that has made no CUDA call yet, and the maps need one
-    const cudaError_t err = allow_shared_memory(kern, kSharedMost);
+    const cudaError_t err = allow_shared_memory(kern, kPairShared);
     if (err != cudaSuccess) return err;
     WeightGrad g = grad;
     if (g.fp32) g.a = grad.b, g.m = grad.n, g.b = grad.a, g.n = grad.m;
@@ -397,7 +396,7 @@ cudaError_t launch_weight_grad(const LaunchCtx& ctx, const WeightGrad& grad) {
     }
     if (!g.fp32 && !make_map_bf16(&map_out, g.out, 3, dout, bout)) return cudaErrorInvalidValue;
     // as many slots as fit: a sixth makes 128 ragged experts in bf16 563 -> 533 us, a seventh in fp32 nothing
-    const int E = g.rows.E, slots = g.fp32 || shared_bytes<uint16_t>(6, E) <= kSharedMost ? 6 : 5;
+    const int E = g.rows.E, slots = g.fp32 || shared_bytes<uint16_t>(6, E) <= kPairShared ? 6 : 5;
     const size_t smem = g.fp32 ? shared_bytes<float>(slots, E) : shared_bytes<uint16_t>(slots, E);
     const GradArgs a{g, (g.m + kTile - 1) / kTile, (g.n + kTile - 1) / kTile, slots};
     return launch_pairs(ctx, kern, smem, a, maps, map_out);
