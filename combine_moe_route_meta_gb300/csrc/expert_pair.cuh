@@ -108,16 +108,16 @@ __device__ __forceinline__ int pick_tile_rows(const uint32_t (&tiles)[kRowChoice
 __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n, int readers) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kPairSlots; i++) {
-            mbar_init(smem_addr(&s->full[i]), 1);
-            mbar_init(smem_addr(&s->empty[i]), 1);
-        }
-        for (int i = 0; i < 2; i++) {
-            mbar_init(smem_addr(&s->acc_full[i]), 1);
-            mbar_init(smem_addr(&s->acc_empty[i]), 2 * readers);
+    if (threadIdx.x < kPairSlots) {
+        mbar_init(smem_addr(&s->full[threadIdx.x]), 1);
+        mbar_init(smem_addr(&s->empty[threadIdx.x]), 1);
+        if (threadIdx.x < 2) {
+            mbar_init(smem_addr(&s->acc_full[threadIdx.x]), 1);
+            mbar_init(smem_addr(&s->acc_empty[threadIdx.x]), 2 * readers);
         }
         mbar_fence_init();
+    }
+    if (threadIdx.x == 0) {
         s->dead = 0;
         s->tiles = 0;
         s->prefix()[0] = 0;
