@@ -25,15 +25,20 @@
 // A slot's time is 150 + 0.77 N ns: loads into shared memory and operands out of it move 100 bytes a clock in all. Under the
 // power limit (1.38 kW) long runs are some 10 % slower.
 #include <cstdint>
+#include <type_traits>
 
 #include "expert_pair.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxRows = 256;  // of a tile
+// Rows of a tile beyond 256 are the N side of a second product on the same weights: of 288 rows, 160 and 128. The accumulators
+// of a pair's tiles lie at the two ends of tensor memory in turn; where two of them meet, in 64 columns at most, the epilogue
+// reads these first, and the next tile's products wait for that alone.
+constexpr int kWideFirst = 160;
+constexpr int kChunkRows = 16;  // rows of the accumulator that a group of epilogue warps takes at a time
+static_assert(2 * kWideRows - int(kPairTmemColumns) <= 4 * kChunkRows, "two pieces of both groups are what may meet");
 constexpr int kCols = 256;
-constexpr int kChunkRows = 16;                               // rows of the accumulator at a time
 constexpr uint32_t kStaged = kChunkRows * 128 * 4;           // ... of a block's 128 columns in fp32
 constexpr uint32_t kStaging = 2 * kStaged;                   // two groups of four epilogue warps
 // Bytes of the ring: what is left, in swizzle atoms.
@@ -53,6 +58,10 @@ struct Tile {
     int e, n0, row0, rows;  // expert, first column, first row, rows
     // N of the products; each block loads half of it
     __device__ __forceinline__ int n() const { return (rows + 31) & ~31; }
+    __device__ __forceinline__ bool wide() const { return n() > 256; }
+    __device__ __forceinline__ int first() const { return wide() ? kWideFirst : n(); }  // N of the first product
+    // The first column of the accumulator of the i-th of a pair's tiles.
+    __device__ __forceinline__ int column(int i) const { return i & 1 ? int(kPairTmemColumns) - max(n(), 256) : 0; }
 };
 
 template <RowOp OP>
@@ -104,8 +113,7 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs) {
         const Tile tile = find_tile<OP>(a, s, t);
-        const int half = tile.n() / 2;
-        const int row0 = tile.row0 + rank * half;
+        const int half = tile.n() / 2, first = tile.first() / 2;  // of the block; those of the first product
         const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
         const uint32_t bytes = 2 * (kPairBytes + half * 128);
         for (int c = 0; c < a.chunks; c++) {
@@ -121,15 +129,19 @@ __device__ __forceinline__ void load_role(const GemmArgs& a, PairShared* s, uint
                     // (k, column, half, expert); SwiGLU: 64 columns of both halves
                     pair_load_4d(slot, map_w, k0, n0, 0, tile.e, bar);
                 }
-                int at = 0;
+                uint32_t to = slot + kPairBytes;
+                const auto load_rows = [&](int row, int count) {
 #pragma unroll
-                for (int i = 0; i < kBoxes; i++) {
-                    const int box = 128 >> i;
-                    if (half & box) {
-                        pair_load_2d(slot + kPairBytes + at * 128, &maps.a[i], k0, row0 + at, bar);
-                        at += box;
+                    for (int i = 0; i < kBoxes; i++) {
+                        const int box = 128 >> i;
+                        if (count & box) {
+                            pair_load_2d(to, &maps.a[i], k0, row, bar);
+                            to += box * 128, row += box;
+                        }
                     }
-                }
+                };
+                load_rows(tile.row0 + rank * first, first);
+                if (half > first) load_rows(tile.row0 + 2 * first + rank * (half - first), half - first);
             }
             __syncwarp();
             if (++st == stages) st = 0, ph ^= 1;
@@ -148,30 +160,43 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, PairShared* s, uint3
     const uint32_t leader = elect_one();
     const uint32_t slot_size = uniform(slot_bytes(s));
     const int stages = uniform(ring_slots(a, slot_size));
-    int st = 0, n_tile = 0;
+    int st = 0, n_tile = 0, edge = 0;
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
         const Tile tile = find_tile<OP>(a, s, t);
-        const uint32_t idesc = pair_idesc_bf16(tile.n(), KN, false);
-        const int acc = n_tile & 1;
-        const uint32_t d = tmem + acc * kMaxRows;
+        const uint32_t idesc = pair_idesc_bf16(tile.first(), KN, false), idesc2 = pair_idesc_bf16(kWideRows - kWideFirst, KN, false);
+        const int acc = n_tile & 1, column = tile.column(n_tile);
+        const uint32_t d = tmem + column;
         if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
+        // the tile before, at the other end
+        if (n_tile > 0 && (acc == 0 ? tile.n() > edge : column < edge) &&
+            !pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->top_empty[acc ^ 1]), (n_tile - 1) >> 1 & 1))
+            return;
+        edge = acc == 0 ? tile.n() : column;  // where this one ends, towards the middle
         tc_fence_after();
-        for (int c = 0; c < a.chunks; c++) {
-            if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return;
-            tc_fence_after();
-            const uint32_t off = st * (slot_size / 16);
-            const int steps = c + 1 < a.chunks ? 4 : last;
+        // a loop for either kind of tile: a branch in a slot's products costs every slot some 10 ns
+        const auto products = [&](auto wide) {
+            for (int c = 0; c < a.chunks; c++) {
+                if (!pair_wait_warp(s, a.g.rows.status, full + 8 * st, ph)) return false;
+                tc_fence_after();
+                const uint32_t off = st * (slot_size / 16);
+                const int steps = c + 1 < a.chunks ? 4 : last;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if (j >= steps) break;
-                // 16 values of k: 32 bytes further in the rows; or 16 rows of 128 bytes
-                pair_mma_bf16(leader, d, da + off + (KN ? 128 : 2) * j, db + off + 2 * j, idesc, c > 0 || j > 0);
+                for (int j = 0; j < 4; j++) {
+                    if (j >= steps) break;
+                    // 16 values of k: 32 bytes further in the rows; or 16 rows of 128 bytes
+                    const uint64_t w = da + off + (KN ? 128 : 2) * j, r = db + off + 2 * j;
+                    pair_mma_bf16(leader, d, w, r, idesc, c > 0 || j > 0);
+                    if constexpr (wide.value)
+                        pair_mma_bf16(leader, d + kWideFirst, w, r + kWideFirst / 2 * 8, idesc2, c > 0 || j > 0);
+                }
+                pair_commit(leader, empty + 8 * st);
+                if (c + 1 == a.chunks) pair_commit(leader, smem_addr(&s->acc_full[acc]));
+                if (++st == stages) st = 0, ph ^= 1;
             }
-            pair_commit(leader, empty + 8 * st);
-            if (c + 1 == a.chunks) pair_commit(leader, smem_addr(&s->acc_full[acc]));
-            if (++st == stages) st = 0, ph ^= 1;
-        }
+            return true;
+        };
+        if (!(tile.wide() ? products(std::true_type()) : products(std::false_type()))) return;
     }
 }
 
@@ -188,75 +213,96 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
     const uint32_t tmem = s->tmem + (uint32_t(quad * 32) << 16);  // the 32 lanes that the warp may read
     const int pairs = gridDim.x / 2, tiles = s->tiles * a.tiles_n, n = a.g.n;
     float* stage = staging + group * (kStaged / 4);
+    constexpr int kPieces = 2;  // taken before they are written
+    const bool meet = s->most > 256;
     int n_tile = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
         const Tile tile = find_tile<OP>(a, s, t);
-        const int acc = n_tile & 1;
+        const int acc = n_tile & 1, times = tile.n() / (2 * kChunkRows), column = tile.column(n_tile);
         const int n0 = tile.n0 + rank * (kTileCols<OP> / 2);
         if (!group_all(group, pair_wait(s, a.g.rows.status, smem_addr(&s->acc_full[acc]), n_tile >> 1 & 1))) return;
         tc_fence_after();
-        const uint32_t done = leaders(smem_addr(&s->acc_empty[acc]));
-        if (group * kChunkRows >= tile.rows || n0 >= n) {  // nothing to finish
-            if (lane == 0) mbar_arrive_cluster(done);
+        const uint32_t done = leaders(smem_addr(&s->acc_empty[acc])), top = leaders(smem_addr(&s->top_empty[acc]));
+        if (n0 >= n) {  // nothing to finish
+            if (lane == 0) {
+                if (meet) mbar_arrive_cluster(top);
+                mbar_arrive_cluster(done);
+            }
             continue;
         }
-        for (int j0 = group * kChunkRows; j0 < tile.rows; j0 += 2 * kChunkRows) {
-            uint2 gate[4], up[4];
-            if constexpr (OP == RowOp::kDswiglu) {
-                // gate and up of the rows and columns that this lane will finish, on their way beside the accumulator
+        // from the end that the next tile's accumulator may meet
+        for (int i0 = 0; i0 < times; i0 += kPieces) {
+            int j0[kPieces];
+            uint2 gate[kPieces][4], up[kPieces][4];
+            float v[kPieces][kChunkRows];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int j = j0 + quad * 4 + i, col = n0 + lane * 4;
-                    if (j >= tile.rows || col >= n) continue;
-                    const uint16_t* p = a.g.gate_up + (int64_t(tile.row0) + j) * 2 * n + col;
-                    gate[i] = ld_v2(p);
-                    up[i] = ld_v2(p + n);
+            for (int x = 0; x < kPieces; x++) {
+                j0[x] = i0 + x < times ? (acc ? i0 + x : times - 1 - i0 - x) * 2 * kChunkRows + group * kChunkRows : tile.rows;
+                if constexpr (OP == RowOp::kDswiglu) {
+                    // gate and up of the rows and columns that this lane will finish, on their way beside the accumulator
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int j = j0[x] + quad * 4 + i, col = n0 + lane * 4;
+                        if (j >= tile.rows || col >= n) continue;
+                        const uint16_t* p = a.g.gate_up + (int64_t(tile.row0) + j) * 2 * n + col;
+                        gate[x][i] = ld_v2(p);
+                        up[x][i] = ld_v2(p + n);
+                    }
                 }
             }
             __syncwarp();
-            float v[16];
-            tmem_load16(tmem + acc * kMaxRows + j0, v);
-            if (j0 + 2 * kChunkRows >= tile.rows) {  // the warp's last of this accumulator
+#pragma unroll
+            for (int x = 0; x < kPieces; x++)
+                if (j0[x] < tile.rows) tmem_load16(tmem + column + j0[x], v[x]);
+            const bool met = meet && i0 == 0, last = i0 + kPieces >= times;
+            if (met || last) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(done);
-            }
-            group_sync(group);  // what was there before has been read
-#pragma unroll
-            for (int j = 0; j < kChunkRows; j++) stage[j * 128 + quad * 32 + lane] = v[j];
-            group_sync(group);
-            if constexpr (OP == RowOp::kSwiglu) {
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int j = quad * 4 + i * 2 + lane / 16, c = lane % 16 * 4, col = n0 + c;
-                    if (j0 + j >= tile.rows || col >= n) continue;
-                    const int64_t r = int64_t(tile.row0) + j0 + j;
-                    const float4 g = *reinterpret_cast<const float4*>(stage + j * 128 + c);
-                    const float4 u = *reinterpret_cast<const float4*>(stage + j * 128 + 64 + c);
-                    st_v2(a.g.out + r * n + col, pack4(make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z),
-                                                                   swiglu(g.w, u.w))));
-                    if (a.g.gate_up) {
-                        st_v2(a.g.gate_up + r * 2 * n + col, pack4(g));
-                        st_v2(a.g.gate_up + (r * 2 + 1) * n + col, pack4(u));
-                    }
+                if (lane == 0) {
+                    if (met) mbar_arrive_cluster(top);
+                    if (last) mbar_arrive_cluster(done);
                 }
-            } else {
+            }
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int j = quad * 4 + i, col = n0 + lane * 4;
-                    if (j0 + j >= tile.rows || col >= n) continue;
-                    const int64_t r = int64_t(tile.row0) + j0 + j;
-                    const float4 x = *reinterpret_cast<const float4*>(stage + j * 128 + lane * 4);
-                    if constexpr (OP == RowOp::kPlain) {
-                        st_v2(a.g.out + r * n + col, pack4(x));
-                    } else {
-                        float4 dg, du;
-                        dswiglu(bf16_lo(gate[i].x), bf16_lo(up[i].x), x.x, &dg.x, &du.x);
-                        dswiglu(bf16_hi(gate[i].x), bf16_hi(up[i].x), x.y, &dg.y, &du.y);
-                        dswiglu(bf16_lo(gate[i].y), bf16_lo(up[i].y), x.z, &dg.z, &du.z);
-                        dswiglu(bf16_hi(gate[i].y), bf16_hi(up[i].y), x.w, &dg.w, &du.w);
-                        st_v2(a.g.out + r * 2 * n + col, pack4(dg));
-                        st_v2(a.g.out + (r * 2 + 1) * n + col, pack4(du));
+            for (int x = 0; x < kPieces; x++) {
+                if (j0[x] >= tile.rows) continue;
+                group_sync(group);  // what was there before has been read
+#pragma unroll
+                for (int j = 0; j < kChunkRows; j++) stage[j * 128 + quad * 32 + lane] = v[x][j];
+                group_sync(group);
+                if constexpr (OP == RowOp::kSwiglu) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int j = quad * 4 + i * 2 + lane / 16, c = lane % 16 * 4, col = n0 + c;
+                        if (j0[x] + j >= tile.rows || col >= n) continue;
+                        const int64_t r = int64_t(tile.row0) + j0[x] + j;
+                        const float4 g = *reinterpret_cast<const float4*>(stage + j * 128 + c);
+                        const float4 u = *reinterpret_cast<const float4*>(stage + j * 128 + 64 + c);
+                        st_v2(a.g.out + r * n + col, pack4(make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z),
+                                                                       swiglu(g.w, u.w))));
+                        if (a.g.gate_up) {
+                            st_v2(a.g.gate_up + r * 2 * n + col, pack4(g));
+                            st_v2(a.g.gate_up + (r * 2 + 1) * n + col, pack4(u));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int j = quad * 4 + i, col = n0 + lane * 4;
+                        if (j0[x] + j >= tile.rows || col >= n) continue;
+                        const int64_t r = int64_t(tile.row0) + j0[x] + j;
+                        const float4 sums = *reinterpret_cast<const float4*>(stage + j * 128 + lane * 4);
+                        if constexpr (OP == RowOp::kPlain) {
+                            st_v2(a.g.out + r * n + col, pack4(sums));
+                        } else {
+                            float4 dg, du;
+                            dswiglu(bf16_lo(gate[x][i].x), bf16_lo(up[x][i].x), sums.x, &dg.x, &du.x);
+                            dswiglu(bf16_hi(gate[x][i].x), bf16_hi(up[x][i].x), sums.y, &dg.y, &du.y);
+                            dswiglu(bf16_lo(gate[x][i].y), bf16_lo(up[x][i].y), sums.z, &dg.z, &du.z);
+                            dswiglu(bf16_hi(gate[x][i].y), bf16_hi(up[x][i].y), sums.w, &dg.w, &du.w);
+                            st_v2(a.g.out + r * 2 * n + col, pack4(dg));
+                            st_v2(a.g.out + (r * 2 + 1) * n + col, pack4(du));
+                        }
                     }
                 }
             }
@@ -274,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     float* staging = reinterpret_cast<float*>(base + a.ring);
     PairShared* s = reinterpret_cast<PairShared*>(base + a.ring + kStaging);
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
-    pair_start(s, a.g.rows, a.tiles_n, kPairEpilogueWarps);
+    pair_start(s, a.g.rows, a.tiles_n, a.chunks, kPairEpilogueWarps);
     if (warp == 0) {
         load_role<OP, KN>(a, s, slots, rank, maps, &map_w);
     } else if (warp == 1) {

@@ -21,8 +21,8 @@ constexpr int kPairThreads = kPairWarps * 32;
 constexpr uint32_t kPairTmemColumns = 512;                 // two accumulators of 256
 
 struct PairShared {
-    // full, acc_empty: the leader's alone are used
-    uint64_t full[kPairSlots], empty[kPairSlots], acc_full[2], acc_empty[2];
+    // full, acc_empty, top_empty: the leader's alone are used
+    uint64_t full[kPairSlots], empty[kPairSlots], acc_full[2], acc_empty[2], top_empty[2];
     uint32_t tmem;
     int dead;   // a wait gave up
     int tiles;  // row tiles of all experts
@@ -83,8 +83,13 @@ __device__ __forceinline__ void group_sync(int group) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// The most rows of a tile: 256, 128 or 64, whichever makes the last pair finish first, if the tiles were all alike: a tile of
-// n rows takes 150 + 0.77 n ns for each 64 values of k (measured: 248 ns for 128 rows, 293 for 192, 346 for 256). Small
+// What a tile of n rows costs for each 64 values of k, in ns (measured: 277 for 192 rows, 345 for 256, 388 for 288); and what
+// one of more than 256 costs besides, because its products and the next tile's cannot run beside its epilogue's start.
+__device__ __forceinline__ float tile_cost(float n) { return 75.0f + 1.05f * n; }
+constexpr float kWideCost = 2000.0f;
+constexpr int kWideRows = 288;
+
+// The most rows of a tile: 256, 128 or 64, whichever makes the last pair finish first, if the tiles were all alike. Small
 // tiles are for few of them: 16 experts of 356 rows, dSwiGLU 2112 x 704: 29 us with 128 rows, 36 with 256.
 constexpr int kRowChoices = 3;
 // 256 >> the result.
@@ -95,17 +100,25 @@ __device__ __forceinline__ int pick_tile_rows(const uint32_t (&tiles)[kRowChoice
     for (int i = 0; i < kRowChoices; i++) {
         const float rounds = __fdividef(float(tiles[i]) * float(tiles_n), float(pairs));
         if (tiles[i] == 0 || (i > 0 && rounds > 16.0f)) continue;  // many tiles: the last round hardly matters
-        const float cost = ceilf(rounds) * (150.0f + 0.77f * __fdividef(float(rows), float(tiles[i])));
+        const float cost = ceilf(rounds) * tile_cost(__fdividef(float(rows), float(tiles[i])));
         if (cost < least) least = cost, best = i;
     }
     return best;
 }
+// An expert's rows in `tiles` of up to 256, or in fewer of up to 288 where k (of `chunks` times 64) is long enough: one of 280
+// rows for two of 140. (256 experts of 256 +- 16 rows, SwiGLU 7168 -> 1024: 1303 us for 1420; with k = 1536 it would lose.)
+__device__ __forceinline__ uint32_t wide_tiles(uint32_t rows, uint32_t tiles, int chunks) {
+    const uint32_t wide = (rows + kWideRows - 1) / kWideRows;
+    if (tiles < 2 || wide == tiles) return tiles;
+    const float n = __fdividef(float(rows), float(tiles)), n_wide = __fdividef(float(rows), float(wide));
+    return float(wide) * (tile_cost(n_wide) * chunks + kWideCost) < float(tiles) * tile_cost(n) * chunks ? wide : tiles;
+}
 
 // The start of a kernel, by all threads of both blocks: barriers (`readers`: warps of a block that read an accumulator),
 // tensor memory, the experts' rows. tiles_n > 0: their row
-// tiles too, with so many column tiles each; experts that share rows so that there are more tiles than the output could
+// tiles too, with so many column tiles each and `chunks` slots a tile; experts that share rows so that there are more tiles than the output could
 // have are refused.
-__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n, int readers) {
+__device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n, int chunks, int readers) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);
     if (threadIdx.x < kPairSlots) {
@@ -114,6 +127,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
         if (threadIdx.x < 2) {
             mbar_init(smem_addr(&s->acc_full[threadIdx.x]), 1);
             mbar_init(smem_addr(&s->acc_empty[threadIdx.x]), 2 * readers);
+            mbar_init(smem_addr(&s->top_empty[threadIdx.x]), 2 * readers);
         }
         mbar_fence_init();
     }
@@ -137,7 +151,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
             most = max(most, c);
             // kept below what 32 lanes could overflow with, and above what experts that share no row have
 #pragma unroll
-            for (int i = 0; i < kRowChoices; i++) tiles[i] = min(tiles[i] + (c + (256u >> i) - 1) / (256u >> i), 1u << 26);
+            for (int i = 0; i < kRowChoices; i++) tiles[i] = min(tiles[i] + ((c + (256u >> i) - 1) >> (8 - i)), 1u << 26);
         }
         all = __reduce_add_sync(kFullMask, all);
         most = __reduce_max_sync(kFullMask, most);
@@ -149,9 +163,16 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
             if (lane == 0) set_status(rows.status, MOE_ERR_INVALID_ARG);
         } else {
             const int shift = 8 - pick_tile_rows(tiles, all, tiles_n, gridDim.x / 2);
+            const bool wide = shift == 8 && most > 256;
+            most = wide ? 0 : min(most, 1u << shift);
             int sum = 0;
             for (int e0 = 0; e0 < E; e0 += 32) {
-                int v = e0 + lane < E ? int((uint32_t(s->count(E)[e0 + lane]) + (1u << shift) - 1) >> shift) : 0;
+                const uint32_t c = e0 + lane < E ? s->count(E)[e0 + lane] : 0;
+                int v = int((c + (1u << shift) - 1) >> shift);
+                if (wide) {
+                    v = int(wide_tiles(c, v, chunks));
+                    if (v > 0) most = max(most, (c + v - 1) / v);
+                }
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int u = __shfl_up_sync(kFullMask, v, o);
@@ -160,7 +181,8 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
                 if (e0 + lane < E) s->prefix()[e0 + lane + 1] = sum + v;
                 sum += __shfl_sync(kFullMask, v, 31);
             }
-            if (lane == 0) s->tiles = sum, s->most = int(min(most, 1u << shift));
+            if (wide) most = __reduce_max_sync(kFullMask, most);
+            if (lane == 0) s->tiles = sum, s->most = int(most);
         }
     }
     __syncwarp();

@@ -358,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t slots = smem_addr(base);
     PairShared* s = reinterpret_cast<PairShared*>(base + a.slots * kSlot + (kFp32<T> ? 0 : kStaging));
     const int warp = threadIdx.x / 32, rank = int(cluster_rank());
-    pair_start(s, a.g.rows, 0, kPairEpilogueWarps / 2);
+    pair_start(s, a.g.rows, 0, 0, kPairEpilogueWarps / 2);
     if (warp == 0) {
         load_role<T, false>(a, s, slots, rank, maps.a);
     } else if (warp == 2) {

@@ -426,3 +426,60 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         m.moe_expert_gemm_bf16("normal", a, r.count, w, out, r.status, **r.where)
+
+
+# With a long k an expert's rows may lie in tiles of up to 288, whose accumulators meet: such tiles before and behind each
+# other, small ones, and experts of several, in some rounds of a pair's tiles.
+WIDE = len(LAYOUTS)
+LAYOUTS += [("normal", [270, 288, 257, 40, 0, 530, 289, 576, 17, 283, 860, 256] * 2, dict(spare=2)),
+            ("masked", [288, 1, 287, 0, 260, 200, 288, 33] * 4, dict(M=288))]
+
+
+@pytest.mark.parametrize("op", ["nk", "kn", "swiglu", "dswiglu"])
+@pytest.mark.parametrize("shape", [(2056, 2056), (520, 4104), (1032, 7176)])
+@pytest.mark.parametrize("i", [WIDE, WIDE + 1])
+def test_more_than_256_rows(i, shape, op):
+    if op == "swiglu":
+        test_swiglu(i, shape, True)
+    elif op == "dswiglu":
+        test_dswiglu(i, shape, True)
+    else:
+        test_product(i, shape, op == "kn")
+
+
+def test_more_than_256_rows_repeated():
+    r = Rows("normal", [264] * 60 + [31, 288, 290, 0, 281] * 8, seed=9)
+    n, k = 1536, 2048
+    a, w = r.values(k), r.weights(n, k)
+    outs = [filled((r.rows, n), torch.bfloat16) for _ in range(3)]
+    for out in outs:
+        moe().moe_expert_gemm_bf16(r.mode, a, r.count, w, out, r.status, **r.where)
+    r.ok()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_added_subnormal_gradients(dtype):
+    r = Rows("normal", [3, 0, 40])
+    a, b = torch.zeros(r.rows, 264, dtype=torch.bfloat16, device="cuda"), r.values(136)
+    out = torch.full((3, 264, 136), 2.0 ** -130, dtype=dtype, device="cuda")
+    moe().moe_expert_wgrad_bf16(r.mode, a, b, r.count, out, r.status, accumulate=True, **r.where)
+    r.ok()
+    assert bool((out == 2.0 ** -130).all())
+
+
+@pytest.mark.parametrize("E", [128, 200, 1024])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.float32, False), (torch.float32, True), (torch.bfloat16, True)])
+def test_weight_gradient_of_many_experts(E, dtype, accumulate):
+    """The ring has another number of slots where there are many experts."""
+    r = Rows("normal", [(7 * e) % 150 for e in range(E)], seed=4)
+    a, b = r.values(72), r.values(136)
+    out = torch.randn(E, 72, 136, device="cuda", generator=r.gen).to(dtype)
+    old = out.double() if accumulate else torch.zeros_like(out, dtype=torch.float64)
+    moe().moe_expert_wgrad_bf16(r.mode, a, b, r.count, out, r.status, accumulate=accumulate, **r.where)
+    r.ok()
+    for e, at in r.each():
+        x, y = a[at].double(), b[at].double()
+        want = old[e] + x.T @ y
+        bound = 1.01 * acc(150) * (x.abs().T @ y.abs()) + (HALF[dtype] + HALF[torch.float32]) * want.abs() + 2.0 ** -23 * old[e].abs()
+        close(out[e], want, bound)
