@@ -4,7 +4,7 @@
 //   SwiGLU    h = up * silu(gate) of two such products
 //   dSwiGLU   the gradient of gate and up from such a product
 //
-// Persistent pairs of SMs, each walking over tiles of 256 columns x up to 256 rows of one expert. The weights are the M
+// Persistent pairs of SMs, each walking over tiles of 256 columns x up to 288 rows of one expert. The weights are the M
 // side of the products, 128 columns in each block (SwiGLU: 64 gate columns and the 64 up columns beside them), and the
 // rows the N side, half of them in each block: N follows the expert's rows in steps of 32, so that few rows, or a few more
 // than a tile, cost little more than they are. Warps have roles:
@@ -15,15 +15,16 @@
 // Tiles run with the row tiles of one column block next to each other, so a weight tile comes from DRAM once. Two
 // accumulators: the next tile's products run beside the epilogue. Every wait is bounded (MOE_ERR_TIMEOUT).
 //
-// What it measured (one GB300, single passes; 6777 GB/s is the copy bandwidth, cuBLAS reaches 1.93 PFLOP/s):
-//   8 experts of 8192 rows, 4096 x 4096:    1175 us either way of the weights, 1.87 PFLOP/s
+// What it measured (one GB300, single passes; 6777 GB/s is the copy bandwidth, cuBLAS reaches 1.92 PFLOP/s):
+//   8 experts of 8192 rows, 4096 x 4096:    1165 us either way of the weights, 1.89 PFLOP/s
 //   256 experts of 256 rows, 7168 -> 1024:  SwiGLU 1280 us, 6.7 TB/s: bound by reading the weights
-//   the same with 256 +- 16 rows:           1485 us: half of the experts take two tiles
-//   128 experts of 512 +- 21 rows:          dSwiGLU 4096 -> 768 338 us, 1536 -> 4096 555 us, 1.5 PFLOP/s
-//   128 experts of 32 rows, 4096 -> 2048:   330 us, 6.6 TB/s
-//   8 experts of one row, SwiGLU 4096 -> 768: 18.5 us, of which 4.5 are the kernel's start
-// A slot's time is 150 + 0.77 N ns: loads into shared memory and operands out of it move 100 bytes a clock in all. Under the
-// power limit (1.38 kW) long runs are some 10 % slower.
+//   the same with 256 +- 16 rows:           1330 us, 1370 with gate and up kept: half of the experts are in a tile of 288
+//   128 experts of 512 +- 21 rows:          dSwiGLU 4096 -> 768 325 us, 1536 -> 4096 530 us, 1.55 PFLOP/s
+//   128 experts of 32 rows, 4096 -> 2048:   333 us, 6.6 TB/s
+//   8 experts of one row, SwiGLU 4096 -> 768: 18 us, of which 4.5 are the kernel's start
+// A slot takes 345 ns with 256 rows (the products alone some 290) and 277 with 192, where what an SM takes in from L2 bounds
+// it: 53 bytes a clock. The ring hides the rest of its latency: 6 slots of 256 rows for 5 make the ragged products 3 to 5 %
+// faster. Under the power limit (1.38 kW) long runs are some 10 % slower.
 #include <cstdint>
 #include <type_traits>
 
@@ -81,17 +82,23 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& a, PairShared* s, int 
     }
     const int rows_t = prefix[lo + 1] - prefix[lo];
     const int i = int(t - int64_t(prefix[lo]) * a.tiles_n);
-    const int m = i % rows_t;
+    int col = i, m = 0;
+    if (rows_t > 1) {
+        // the row tiles of a column turn from one round of the pairs to the next: the last of an expert is smaller, and the
+        // same pairs would get it each time and run ahead of those that read the same weights (480 rows: 604 us, not 700)
+        col = i / rows_t, m = i - col * rows_t;
+        m = (m + (t - m) / int(gridDim.x / 2)) % rows_t;
+    }
     // an expert's rows are shared out evenly among its tiles, in steps of 32
     const int count = s->count(E)[lo], each = (count + rows_t - 1) / rows_t;
     const int step = (each + 31) & ~31;
     const int first = min(m * step, count);
-    return Tile{uniform(lo), uniform(i / rows_t * kTileCols<OP>), uniform(s->base(E)[lo] + first),
+    return Tile{uniform(lo), uniform(col * kTileCols<OP>), uniform(s->base(E)[lo] + first),
                 uniform(min(step, count - first))};
 }
 
 // Bytes of a slot, a multiple of the swizzle's atoms, and how many there are: by the largest tile. One token's 8 experts of
-// 2 x 768 x 4096: 18.4 us, with five slots of 32 KB 20.0; 128 experts of 32 rows, 4096 x 2048: 331 and 349 us.
+// 2 x 768 x 4096: 18.4 us, with slots of 32 KB 20.0; 128 experts of 32 rows, 4096 x 2048: 331 and 349 us.
 __device__ __forceinline__ uint32_t slot_bytes(const PairShared* s) { return kPairBytes + uint32_t((s->most + 31) & ~31) * 64; }
 __device__ __forceinline__ int ring_slots(const GemmArgs& a, uint32_t slot) { return min(kPairSlots, int(a.ring / slot)); }
 
