@@ -171,7 +171,8 @@ __device__ __forceinline__ void mma_role(const GemmArgs& a, PairShared* s, uint3
     uint32_t ph = 0;
     for (int t = blockIdx.x / 2; t < tiles; t += pairs, n_tile++) {
         const Tile tile = find_tile<OP>(a, s, t);
-        const uint32_t idesc = pair_idesc_bf16(tile.first(), KN, false), idesc2 = pair_idesc_bf16(kWideRows - kWideFirst, KN, false);
+        const uint32_t idesc = pair_idesc_bf16(tile.first(), KN, false);
+        const uint32_t idesc2 = pair_idesc_bf16(kWideRows - kWideFirst, KN, false);
         const int acc = n_tile & 1, column = tile.column(n_tile);
         const uint32_t d = tmem + column;
         if (!pair_wait_cluster(s, a.g.rows.status, smem_addr(&s->acc_empty[acc]), (n_tile >> 1 & 1) ^ 1)) return;
@@ -244,7 +245,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
             float v[kPieces][kChunkRows];
 #pragma unroll
             for (int x = 0; x < kPieces; x++) {
-                j0[x] = i0 + x < times ? (acc ? i0 + x : times - 1 - i0 - x) * 2 * kChunkRows + group * kChunkRows : tile.rows;
+                const int i = i0 + x;
+                j0[x] = i < times ? ((acc ? i : times - 1 - i) * 2 + group) * kChunkRows : tile.rows;
                 if constexpr (OP == RowOp::kDswiglu) {
                     // gate and up of the rows and columns that this lane will finish, on their way beside the accumulator
 #pragma unroll

@@ -117,9 +117,8 @@ __device__ __forceinline__ uint32_t wide_tiles(uint32_t rows, uint32_t tiles, in
 }
 
 // The start of a kernel, by all threads of both blocks: barriers (`readers`: warps of a block that read an accumulator),
-// tensor memory, the experts' rows. tiles_n > 0: their row
-// tiles too, with so many column tiles each and `chunks` slots a tile; experts that share rows so that there are more tiles than the output could
-// have are refused.
+// tensor memory, the experts' rows. tiles_n > 0: their row tiles too, with so many column tiles each and `chunks` slots a
+// tile; experts that share rows so that there are more tiles than the output could have are refused.
 __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows, int tiles_n, int chunks, int readers) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = rows.E;
     if (warp == 1) pair_tmem_alloc(smem_addr(&s->tmem), kPairTmemColumns);

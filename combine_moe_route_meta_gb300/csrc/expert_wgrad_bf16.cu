@@ -39,8 +39,8 @@ template <typename T>
 constexpr size_t shared_bytes(int slots, int E) {
     return 1024 + slots * kSlot + (kFp32<T> ? 0 : kStaging) + pair_shared_bytes(E);
 }
-static_assert(shared_bytes<float>(6, MOE_MAX_EXPERTS) <= kPairShared && shared_bytes<uint16_t>(5, MOE_MAX_EXPERTS) <= kPairShared,
-              "shared memory of an SM");
+static_assert(shared_bytes<float>(6, MOE_MAX_EXPERTS) <= kPairShared, "shared memory of an SM");
+static_assert(shared_bytes<uint16_t>(5, MOE_MAX_EXPERTS) <= kPairShared, "shared memory of an SM");
 
 struct GradArgs {
     WeightGrad g;  // a: the M side, of m columns; b: the N side, of n
@@ -291,7 +291,8 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
         const int m0 = tile.m0 + me.first;
         const int width = m0 < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;  // columns of the warp's rows
         // accumulate: the lane's row, on its way to L2 beside the products
-        const uint16_t* old = static_cast<const uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + m0 + me.lane) * a.g.n + tile.n0;
+        const uint16_t* old =
+            static_cast<const uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + m0 + me.lane) * a.g.n + tile.n0;
         const bool add = ADD && m0 + me.lane < a.g.m;
         if (add)
             for (int c = 0; c < width; c += kCols) asm volatile("prefetch.global.L2 [%0];" ::"l"(old + c));
