@@ -41,6 +41,8 @@ def _rows(mode: str, a: torch.Tensor, K: int, E: int, M: int, seg_indptr, name: 
     if a.dim() < 2 or a.shape[-1] != K:
         raise ValueError(f"{name}: rows of {K} values needed, got shape {tuple(a.shape)}")
     if _mode(mode) == MOE_MODE_MASKED:
+        if a.dim() == 3 and a.shape[1] != M:  # rows of another stride than the kernels'
+            raise ValueError(f"{name}: [E, {M}, {K}] expected in masked mode, got shape {tuple(a.shape)}")
         return E * M
     if seg_indptr is None:
         raise ValueError("seg_indptr: needed in normal mode")
@@ -284,7 +286,8 @@ class BF16MoELayer:
     MOE_LAYER_MAX_TOKENS, never with ``train``) :func:`moe_layer_few_tokens` instead. With ``train`` a call keeps what
     :meth:`backward` needs until the next call. Weight gradients are ``grad_dtype`` (fp32 or bf16), in kept buffers that
     ``accumulate`` adds to. No call allocates, so a call of a fixed size can be captured in a CUDA graph. All calls share
-    the layer's buffers: one at a time, a backward pass after its own forward pass.
+    the layer's buffers: one at a time, a backward pass after its own forward pass, which reads that call's topk_ids and
+    topk_weights again: they have to hold what they held.
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, topk: int, max_tokens: int, *, train: bool = False,
@@ -295,6 +298,8 @@ class BF16MoELayer:
                              f"{tuple(w2.shape)}")
         if w13.dtype is not _BF16 or w2.dtype is not _BF16:
             raise ValueError(f"w13, w2: bf16 weights expected, got {w13.dtype} and {w2.dtype}")
+        if max_tokens < 1 or topk < 1:
+            raise ValueError(f"max_tokens and topk: 1 or more expected, got {max_tokens} and {topk}")
         if grad_dtype not in (_F32, _BF16):
             raise ValueError(f"grad_dtype: torch.float32 or torch.bfloat16 expected, got {grad_dtype}")
         self.w13, self.w2, self.K, self.T, self.train = w13, w2, topk, max_tokens, train

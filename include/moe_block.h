@@ -143,7 +143,8 @@ moe_status_t moe_combine_backward(moe_mode_t mode, const uint16_t *grad_out, con
  *                    scales [T, hidden/128] fp32 or UE8M0 bytes. rstd [T] fp32. out, codes or both.
  *                    sum may be x or residual itself; no other output overlaps an input.
  *   eps              > 0 and finite
- * A row of infinities or NaNs leaves the others as they are.
+ * All in binary32: a row whose squares overflow it (values beyond 2^63) has r = 0. A row of infinities or NaNs
+ * leaves the others as they are.
  */
 moe_status_t moe_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,
                          int64_t num_tokens, int hidden, moe_quant_t quant, uint16_t *out, uint8_t *codes,

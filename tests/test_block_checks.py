@@ -234,3 +234,24 @@ def test_binding_checks_norm():
             moe.moe_rmsnorm_backward(a["g"], a["s"], a["w"], a["r"], a["gx"], a["gw"], ws, a["gs"])
     with pytest.raises(ValueError, match="no CPU path"):
         moe.moe_rmsnorm_backward(x, x, w, r, x, torch.zeros(H), ws)
+
+
+def test_masked_rows_of_another_stride():
+    bf = dict(dtype=torch.bfloat16)
+    count, st = torch.ones(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    a, w, out = torch.zeros(4, 9, 64, **bf), torch.zeros(4, 32, 64, **bf), torch.zeros(4, 9, 32, **bf)
+    with pytest.raises(ValueError, match=r"a: \[E, 8, 64\] expected"):
+        moe.moe_expert_gemm_bf16("masked", a, count, w, out, st, max_tokens_per_expert=8)
+    with pytest.raises(ValueError, match=r"grad_out: \[E, 8, 64\] expected"):
+        moe.moe_expert_gemm_dswiglu_bf16("masked", a, count, torch.zeros(4, 64, 32, **bf), torch.zeros(36, 64, **bf),
+                                         torch.zeros(36, 64, **bf), st, max_tokens_per_expert=8)
+    with pytest.raises(ValueError, match=r"b: \[E, 8, 32\] expected"):
+        moe.moe_expert_wgrad_bf16("masked", torch.zeros(32, 64, **bf), out, count, torch.zeros(4, 64, 32), st,
+                                  max_tokens_per_expert=8)
+
+
+def test_layer_sizes():
+    w13, w2 = torch.zeros(4, 64, 32, dtype=torch.bfloat16), torch.zeros(4, 32, 32, dtype=torch.bfloat16)
+    for topk, tokens in ((2, 0), (0, 4), (2, -1)):
+        with pytest.raises(ValueError, match="max_tokens and topk"):
+            moe.BF16MoELayer(w13, w2, topk, tokens)
