@@ -4,12 +4,13 @@
 // A row stays in registers between its one reading and its one writing. A lane has runs of 8 columns, threads next to
 // each other neighbouring runs, so accesses are of 16 bytes and the 128 values of an FP8 group lie in 16 neighbouring
 // lanes. Rows of up to 1024 columns are a warp's, longer ones a block's. As many blocks as fit go from row to row, with the
-// next row's loads on their way beside this one's reduction. The gradient of the weight is a sum over rows: each of at most
-// kGradBlocks blocks sums its rows in registers and writes one line of partial sums; a second kernel adds the lines in order.
+// next row's loads on their way beside this one's reduction; large gradients have up to four rows ahead in shared memory. The
+// gradient of the weight is a sum over rows: each of at most kGradBlocks blocks sums its rows in registers and writes one line
+// of partial sums; a second kernel adds the lines in order.
 //
 // Bound by DRAM; one GB300, whose copy bandwidth is 6777 GB/s, cold L2:
-//   16384 x 4096, residual:  FP8 72 us (6.5 TB/s), bf16 87 us (6.1), gradient 90 us (5.9)
-//   8192 x 7168:             FP8 64 us (6.4 TB/s), bf16 76 us (6.1), gradient 89 us (5.3)
+//   16384 x 4096, residual:  FP8 72 us (6.5 TB/s), bf16 87 us (6.1), gradient 82 us (6.6)
+//   8192 x 7168:             FP8 64 us (6.4 TB/s), bf16 76 us (6.1), gradient 77 us (6.1)
 //   128 x 7168:              FP8 2.8 us, bf16 2.3 us, gradient 5.7 us (two launches)
 // One row a block, and no loads ahead: 100, 97 and 147 us for the first.
 #include <cstdint>
@@ -23,6 +24,8 @@ namespace moe {
 namespace {
 
 constexpr int kGradBlocks = 304;
+constexpr int64_t kManyValues = 1 << 24;
+constexpr size_t kRowsAhead = 108 * 1024;  // shared memory for rows on their way, for two blocks on an SM
 constexpr int kWarpColumns = 1024;  // of a warp's row, at most
 // Warps of a block with a row each: the gradient's blocks are few, so they have more warps where registers allow.
 template <int V, bool GRAD>
@@ -247,6 +250,110 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_backward_kernel(NormGrad a) {
     }
 }
 
+// A thread's parts of the next rows of N tensors, on their way to its own places in shared memory: `stages` rows ahead, without
+// registers, and without a barrier since nobody else reads them. A tensor may be null: zeros.
+template <int V, int N>
+struct RowsAhead {
+    uint32_t mine;  // this thread's place of the first run
+    int stages, st = 0;
+    const uint16_t* from[N];
+    __device__ __forceinline__ uint32_t place(int x, int v) const {
+        return mine + uint32_t(((st * N + x) * V + v) * blockDim.x) * 16;
+    }
+    // The part of row t into the current stage; nothing beyond the last row.
+    __device__ __forceinline__ void load(int64_t t, int64_t T, int H, const Place<false>& at) {
+        if (t < T) {
+#pragma unroll
+            for (int x = 0; x < N; x++)
+#pragma unroll
+                for (int v = 0; v < V; v++)
+                    if (from[x] && at.column(v) < H)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place(x, v)),
+                                     "l"(from[x] + t * H + at.column(v))
+                                     : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++st == stages) st = 0;
+    }
+    __device__ __forceinline__ void start(int64_t T, int H, const Place<false>& at) {
+        for (int i = 0; i < stages; i++) load(at.first + i * at.step, T, H, at);
+    }
+    // The oldest row, which lies in the current stage. The next load() comes after a barrier: the stage has been read then.
+    __device__ __forceinline__ void take(uint4 (&r)[N][V], int H, const Place<false>& at) {
+        if (stages == 4)
+            asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+        for (int x = 0; x < N; x++)
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                r[x][v] = make_uint4(0, 0, 0, 0);
+                if (from[x] && at.column(v) < H)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(r[x][v].x), "=r"(r[x][v].y), "=r"(r[x][v].z), "=r"(r[x][v].w)
+                                 : "r"(place(x, v))
+                                 : "memory");
+            }
+    }
+};
+
+// The same of rows of a block, with the rows ahead in shared memory.
+template <int V>
+__global__ void __launch_bounds__(512) rmsnorm_backward_ahead_kernel(NormGrad a, int stages) {
+    __shared__ float part[2][32];
+    extern __shared__ float4 rows[];
+    pdl_wait();
+    const Place<false> at;
+    uint4 w[V];
+    float acc[V][8] = {};
+    load_row(w, a.weight, 0, a.H, at);
+    RowsAhead<V, 3> ahead{smem_addr(rows) + threadIdx.x * 16, stages, 0, {a.s, a.grad, a.grad_sum}};
+    ahead.start(a.T, a.H, at);
+    float next = at.first < a.T ? __ldg(a.rstd + at.first) : 0.0f;
+    int turn = 0;
+    for (int64_t t = at.first; t < a.T; t += at.step, turn ^= 1) {
+        uint4 row[3][V];
+        ahead.take(row, a.H, at);
+        const float r = next;
+        if (t + at.step < a.T) next = __ldg(a.rstd + t + at.step);
+        float hat[V][8], gw[V][8], dot = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            float wv[8];
+            unpack8(row[0][v], hat[v]);
+            unpack8(row[1][v], gw[v]);
+            unpack8(w[v], wv);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                hat[v][j] *= r;
+                acc[v][j] = fmaf(gw[v][j], hat[v][j], acc[v][j]);
+                gw[v][j] *= wv[j];
+                dot = fmaf(gw[v][j], hat[v][j], dot);
+            }
+        }
+        const float mean = __fdiv_rn(row_sum<false>(dot, part, turn), float(a.H));
+        ahead.load(t + stages * at.step, a.T, a.H, at);
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (at.column(v) >= a.H) continue;
+            float d[8], f[8];
+            unpack8(row[2][v], f);
+#pragma unroll
+            for (int j = 0; j < 8; j++) d[j] = fmaf(r, fmaf(-mean, hat[v][j], gw[v][j]), f[j]);
+            st_v4(a.grad_x + t * a.H + at.column(v), pack8(d));
+        }
+    }
+    float* line = a.partial + int64_t(blockIdx.x) * a.H;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        const int c = at.column(v);
+        if (c >= a.H) continue;
+        *reinterpret_cast<float4*>(line + c) = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+        *reinterpret_cast<float4*>(line + c + 4) = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+    }
+}
+
 // grad_weight[c] = the sum of `n` lines: up to 32 threads a column, each every 32nd line, then these in order.
 constexpr int kParts = 32;
 __global__ void __launch_bounds__(32 * kParts) add_lines_kernel(const float* lines, int n, int H, float* out) {
@@ -296,6 +403,20 @@ cudaError_t launch_grad(const LaunchCtx& ctx, const NormGrad& a, int threads) {
     return launch_pdl(ctx, rmsnorm_backward_kernel<V, WARP, THREADS>, dim3(unsigned(norm_backward_blocks(a.T, a.H))),
                       dim3(threads), smem, a);
 }
+// Rows ahead in shared memory, four of them where two blocks on an SM have room: from 16 M values on, of up to 8192 columns.
+// (16384 x 4096 82 us, by registers 90.5; 8192 x 7168 77 and 89.5; 2432 x 7168 29.6 and 32.2; 1800 x 4096 16.0 and 15.1.
+// The norm itself has registers for more blocks, and loses: 16384 x 4096 in bf16 92 us for 87.)
+template <int V>
+cudaError_t launch_grad_ahead(const LaunchCtx& ctx, const NormGrad& a, int threads) {
+    const int64_t blocks = norm_backward_blocks(a.T, a.H);
+    if (a.T * a.H < kManyValues) return launch_grad<V, false, 512>(ctx, a, threads);
+    auto kern = rmsnorm_backward_ahead_kernel<V>;
+    const size_t row = size_t(3) * V * 16 * threads;
+    const int stages = row * 4 <= kRowsAhead ? 4 : 2;
+    const cudaError_t err = allow_shared_memory(kern, kRowsAhead);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(ctx, kern, dim3(unsigned(blocks)), dim3(threads), stages * row, a, stages);
+}
 template <int V>
 cudaError_t launch_grad_warps(const LaunchCtx& ctx, const NormGrad& a) {
     return launch_grad<V, true, kWarpRows<V, true> * 32>(ctx, a, kWarpRows<V, true> * 32);
@@ -338,9 +459,9 @@ cudaError_t launch_rmsnorm_backward(const LaunchCtx& ctx, const NormGrad& a) {
         else if (a.H <= kWarpColumns)
             err = launch_grad_warps<4>(ctx, a);
         else if (V == 1)
-            err = launch_grad<1, false, 512>(ctx, a, threads);
+            err = launch_grad_ahead<1>(ctx, a, threads);
         else if (V == 2)
-            err = launch_grad<2, false, 512>(ctx, a, threads);
+            err = launch_grad_ahead<2>(ctx, a, threads);
         else if (threads <= 512)
             err = launch_grad<4, false, 512>(ctx, a, threads);
         else

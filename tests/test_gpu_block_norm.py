@@ -241,3 +241,29 @@ def test_offsets_past_32_bits():
     dx, _ = m.rmsnorm_backward(y.out, x, w, y.rstd)
     want, _ = m.rmsnorm_backward(last.out, x[-2:].contiguous(), w, last.rstd)
     assert torch.equal(dx[-2:], want)
+
+
+# Gradients of so many values have their rows on the way in shared memory, two or four of them.
+AHEAD = [(2049, 8192), (4111, 4104), (8200, 2056), (16400, 1032), (2347, 7168)]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("T,H", AHEAD)
+def test_gradient_of_many_rows(T, H, residual):
+    test_gradient(T, H, residual)
+
+
+@pytest.mark.parametrize("T,H", AHEAD[:3])
+def test_gradient_of_many_rows_in_place(T, H):
+    m = moe()
+    x, res, w, gen = _inputs(T, H, seed=8)
+    y = m.rmsnorm(x, w, EPS, residual=res, keep=True)
+    g, gs = (torch.randn(T, H, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    dx, dw = m.rmsnorm_backward(g, y.sum, w, y.rstd, gs)
+    n = m.moe_rmsnorm_backward_workspace_size(T, H)
+    for first in (True, False):
+        which = (g if first else gs).clone()
+        got_w, ws = filled((H,), torch.float32), filled((n,), torch.uint8)
+        m.moe_rmsnorm_backward(which if first else g, y.sum, w, y.rstd, which, got_w, ws, gs if first else which)
+        torch.cuda.synchronize()
+        assert torch.equal(which, dx) and torch.equal(got_w, dw)
