@@ -267,3 +267,9 @@ def test_gradient_of_many_rows_in_place(T, H):
         m.moe_rmsnorm_backward(which if first else g, y.sum, w, y.rstd, which, got_w, ws, gs if first else which)
         torch.cuda.synchronize()
         assert torch.equal(which, dx) and torch.equal(got_w, dw)
+
+
+@pytest.mark.parametrize("T,H", [(900, 12288), (700, 16384), (611, 10240)])
+def test_long_rows(T, H):
+    test_bf16(T, H, True)
+    test_fp8(T, H, "fp8g128")
