@@ -19,9 +19,9 @@
 //
 // What it measured (one GB300, single passes):
 //   8 experts of 8192 rows, 4096 x 4096 in fp32:            1150 us, 1.91 PFLOP/s
-//   128 experts of 512 +- 21 rows, 1536 x 4096 in fp32:     690 us: 3.2 GB of results beside 8 GB of loads from L2
+//   128 experts of 512 +- 21 rows, 1536 x 4096 in fp32:     695 us: 3.2 GB of results beside 8 GB of loads from L2
 //   ... in bf16:                                            533 us, 1.55 PFLOP/s
-//   32 experts of one row, 1040 x 1544 in bf16:             24.7 us, 4.2 TB/s; without a row 21 us
+//   32 experts of one row, 1040 x 1544 in bf16:             24 us, 4.3 TB/s; without a row 19.5 us
 #include <cstdint>
 
 #include "expert_pair.cuh"
@@ -232,6 +232,16 @@ __device__ __forceinline__ void put_column(float* p, int64_t stride, const float
             if (i < rows) p[i * stride] = r[i];
     }
 }
+// An expert without rows: zeros to `rows` rows of up to 512 bytes, whole ones by a warp. (32 experts without a row, 1040 x 1544
+// in fp32: 35 us, 38 by 128 bytes at a time.)
+template <typename T>
+__device__ __forceinline__ void put_zeros(T* p, int64_t stride, int rows, int columns, int quad, int lane) {
+    const int c = lane * int(16 / sizeof(T));
+    if (c >= columns) return;
+#pragma unroll 8
+    for (int r = quad; r < rows; r += 4) st_v4(p + r * stride + c, make_uint4(0, 0, 0, 0));
+}
+
 // Lanes are columns of out.
 template <bool ADD>
 __device__ __forceinline__ void epilogue_fp32(const GradArgs& a, PairShared* s, int rank, int warp) {
@@ -241,21 +251,25 @@ __device__ __forceinline__ void epilogue_fp32(const GradArgs& a, PairShared* s, 
         const Tile tile(a, s, t);
         const bool sums = tile.rows > 0;
         if (!me.takes(sums) || (!sums && ADD)) continue;
+        if (!sums) {
+            const int c0 = tile.m0 + rank * 128;
+            put_zeros(static_cast<float*>(a.g.out) + (int64_t(tile.e) * a.g.n + tile.n0) * stride + c0, stride,
+                      min(tile.blocks * 128, a.g.n - tile.n0), a.g.m - c0, warp % 4, me.lane);
+            continue;
+        }
         const int column = tile.m0 + me.first + me.lane;
         const int rows = tile.m0 + me.first < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;
         const int mine = column < a.g.m ? rows : 0;
         float* p = static_cast<float*>(a.g.out) + (int64_t(tile.e) * a.g.n + tile.n0) * stride + column;
         float old[32];
         if (ADD) get_column(old, p, stride, mine);
-        if (sums && !me.wait(a.g.rows.status)) break;
-        if (sums && rows == 0) me.release();
+        if (!me.wait(a.g.rows.status)) break;
+        if (rows == 0) me.release();
         for (int c = 0; c < rows; c += 32, p += 32 * stride) {
-            uint32_t w[32] = {};
-            if (sums) {
-                tmem_load32(me.columns(c), w);
-                tmem_wait(w, 32);
-                if (c + 32 >= rows) me.release();
-            }
+            uint32_t w[32];
+            tmem_load32(me.columns(c), w);
+            tmem_wait(w, 32);
+            if (c + 32 >= rows) me.release();
             float r[32];
 #pragma unroll
             for (int i = 0; i < 32; i++) r[i] = __uint_as_float(w[i]);
@@ -288,6 +302,12 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
         const Tile tile(a, s, t);
         const bool sums = tile.rows > 0;
         if (!me.takes(sums) || (!sums && ADD)) continue;
+        if (!sums) {
+            const int r0 = tile.m0 + rank * 128;
+            put_zeros(static_cast<uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + r0) * a.g.n + tile.n0, a.g.n,
+                      min(128, a.g.m - r0), min(tile.blocks * 128, a.g.n - tile.n0), warp % 4, me.lane);
+            continue;
+        }
         const int m0 = tile.m0 + me.first;
         const int width = m0 < a.g.m ? min(tile.blocks * 128, a.g.n - tile.n0) : 0;  // columns of the warp's rows
         // accumulate: the lane's row, on its way to L2 beside the products
@@ -296,14 +316,14 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
         const bool add = ADD && m0 + me.lane < a.g.m;
         if (add)
             for (int c = 0; c < width; c += kCols) asm volatile("prefetch.global.L2 [%0];" ::"l"(old + c));
-        if (sums && !me.wait(a.g.rows.status)) break;
-        if (sums && width == 0) me.release();
+        if (!me.wait(a.g.rows.status)) break;
+        if (width == 0) me.release();
         for (int c0 = 0; c0 < width; c0 += kPieces * kCols) {
-            uint32_t w[kPieces][32] = {};
+            uint32_t w[kPieces][32];
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
                 const int c = c0 + i * kCols;
-                if (!sums || c >= width) break;
+                if (c >= width) break;
                 uint32_t r[64];
                 tmem_load32(me.columns(c), r);
                 tmem_load32(me.columns(c + 32), r + 32);
@@ -325,7 +345,7 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
 #pragma unroll
                 for (int j = 0; j < 32; j++) w[i][j] = pack_sums(r + 2 * j);
             }
-            if (sums && c0 + kPieces * kCols >= width) me.release();
+            if (c0 + kPieces * kCols >= width) me.release();
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
                 const int c = c0 + i * kCols;
