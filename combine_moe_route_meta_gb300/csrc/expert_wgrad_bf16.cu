@@ -255,6 +255,7 @@ __device__ __forceinline__ void epilogue_fp32(const GradArgs& a, PairShared* s, 
             const int c0 = tile.m0 + rank * 128;
             put_zeros(static_cast<float*>(a.g.out) + (int64_t(tile.e) * a.g.n + tile.n0) * stride + c0, stride,
                       min(tile.blocks * 128, a.g.n - tile.n0), a.g.m - c0, warp % 4, me.lane);
+            __syncwarp();
             continue;
         }
         const int column = tile.m0 + me.first + me.lane;
@@ -306,6 +307,7 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
             const int r0 = tile.m0 + rank * 128;
             put_zeros(static_cast<uint16_t*>(a.g.out) + (int64_t(tile.e) * a.g.m + r0) * a.g.n + tile.n0, a.g.n,
                       min(128, a.g.m - r0), min(tile.blocks * 128, a.g.n - tile.n0), warp % 4, me.lane);
+            __syncwarp();
             continue;
         }
         const int m0 = tile.m0 + me.first;
@@ -328,11 +330,15 @@ __device__ __forceinline__ void epilogue_bf16(const GradArgs& a, PairShared* s, 
                 tmem_load32(me.columns(c), r);
                 tmem_load32(me.columns(c + 32), r + 32);
                 tmem_wait(r, 64);
-                if (add) {
+                if constexpr (ADD) {
+                    // by all lanes, zeros in those past the matrix, and together again behind: the next piece is loaded from
+                    // the accumulator by the whole warp, which must not have parted at a last row tile's end
                     uint4 x[8];
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        x[j] = c + j * 8 < width ? *reinterpret_cast<const uint4*>(old + c + j * 8) : make_uint4(0, 0, 0, 0);
+                        x[j] = add && c + j * 8 < width ? *reinterpret_cast<const uint4*>(old + c + j * 8)
+                                                        : make_uint4(0, 0, 0, 0);
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         float f[8];

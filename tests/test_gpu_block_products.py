@@ -483,3 +483,25 @@ def test_weight_gradient_of_many_experts(E, dtype, accumulate):
         want = old[e] + x.T @ y
         bound = 1.01 * acc(150) * (x.abs().T @ y.abs()) + (HALF[dtype] + HALF[torch.float32]) * want.abs() + 2.0 ** -23 * old[e].abs()
         close(out[e], want, bound)
+
+
+@pytest.mark.parametrize("m", [8, 16, 24, 40, 136, 264, 272, 520])
+@pytest.mark.parametrize("n", [64, 72, 136, 200, 264, 392])
+def test_added_bf16_gradients_of_rows_that_part_a_warp(m, n):
+    """Row counts that end inside a warp's 32 rows of the result, with one to four pieces of its columns: lanes with and
+    without a row add, and load the next piece together. Added twice, on repetition the same bits."""
+    r = Rows("normal", [70, 0, 1, 33, 16, 0, 130], seed=m + n)
+    a, b = r.values(m), r.values(n)
+    first = torch.randn(r.E, m, n, device="cuda", generator=r.gen).bfloat16()
+    outs = []
+    for _ in range(2):
+        out = first.clone()
+        moe().moe_expert_wgrad_bf16(r.mode, a, b, r.count, out, r.status, accumulate=True, **r.where)
+        outs.append(out)
+    r.ok()
+    assert torch.equal(*outs)
+    for e, at in r.each():
+        x, y = a[at].double(), b[at].double()
+        want, old = first[e].double() + x.T @ y, first[e].double().abs()
+        bound = 1.01 * acc(int(r.counts[e])) * (x.abs().T @ y.abs()) + (HALF[torch.bfloat16] + 2.0 ** -23) * want.abs()
+        close(outs[0][e], want, bound + 2.0 ** -23 * old)
