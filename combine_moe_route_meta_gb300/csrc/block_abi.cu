@@ -84,8 +84,7 @@ moe_status_t moe_expert_wgrad_bf16(moe_mode_t mode, const uint16_t* a, const uin
     moe_status_t st = check_rows(mode, num_experts, max_tokens_per_expert, &rows, m, n, seg_indptr, masked_m, dev_status);
     if (st != MOE_OK) return st;
     if (int64_t(num_experts) * (m / 256 + 1) * (n / 256 + 1) > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;  // tiles
-    // an expert's sum ends well within the limit of a wait
-    if ((mode == MOE_MODE_MASKED ? max_tokens_per_expert : rows) > (1 << 26)) return MOE_ERR_UNSUPPORTED;
+    if ((mode == MOE_MODE_MASKED ? max_tokens_per_expert : rows) > moe::kMostSummedRows) return MOE_ERR_UNSUPPORTED;
     if (!out || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!a || !b)) return MOE_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(b, 16)) return MOE_ERR_INVALID_ARG;

@@ -32,7 +32,8 @@ struct RowGemm {
 };
 cudaError_t launch_row_gemm(const LaunchCtx& ctx, const RowGemm& g);
 
-// Sums over an expert's rows (expert_wgrad_bf16.cu).
+// Sums over an expert's rows (expert_wgrad_bf16.cu): over at most so many, so that every wait for one can be bounded.
+constexpr int64_t kMostSummedRows = 1 << 26;
 struct WeightGrad {
     RowLayout rows;
     const uint16_t* a;  // [rows, m]

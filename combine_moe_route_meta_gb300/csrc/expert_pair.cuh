@@ -45,12 +45,14 @@ __device__ __forceinline__ bool gave_up(PairShared* s, int32_t* status) {
     set_status(status, MOE_ERR_TIMEOUT);
     return false;
 }
-__device__ __forceinline__ bool pair_wait(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {
-    return mbar_wait(bar, parity) || gave_up(s, status);
+__device__ __forceinline__ bool pair_wait(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+    return mbar_wait(bar, parity, limit_ns) || gave_up(s, status);
 }
 // The same for a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool pair_wait_warp(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {
-    return __all_sync(kFullMask, pair_wait(s, status, bar, parity));
+__device__ __forceinline__ bool pair_wait_warp(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity,
+                                               uint64_t limit_ns = kWaitLimitNs) {
+    return __all_sync(kFullMask, pair_wait(s, status, bar, parity, limit_ns));
 }
 // ... for a phase that threads of the other block complete too
 __device__ __forceinline__ bool pair_wait_cluster(PairShared* s, int32_t* status, uint32_t bar, uint32_t parity) {

@@ -33,6 +33,11 @@ constexpr int kTile = 256;
 constexpr uint32_t kSlot = 2 * kPairBytes;  // 64 rows of 128 columns of each operand
 constexpr uint32_t kStaged = 32 * 128;      // bf16: an epilogue warp's rows on their way out
 constexpr uint32_t kStaging = kPairEpilogueWarps * kStaged;
+// A group of epilogue warps waits for up to two sums, the other group's and its own next one. A slot takes 345 ns, and up to
+// 600 at the 1.2 of 2.07 GHz that the power limit can leave.
+constexpr uint64_t kMostSlotNs = 600;
+constexpr uint64_t kSumsLimitNs = 2 * kWaitLimitNs;
+static_assert(2 * (kMostSummedRows / kPairK) * kMostSlotNs <= kSumsLimitNs, "two of the longest sums end within a wait");
 template <typename T>
 constexpr bool kFp32 = sizeof(T) == 4;
 template <typename T>
@@ -198,7 +203,7 @@ struct EpilogueWarp {
         return acc == group;
     }
     __device__ __forceinline__ bool wait(int32_t* status) const {
-        if (!pair_wait_warp(s, status, smem_addr(&s->acc_full[acc]), phase)) return false;
+        if (!pair_wait_warp(s, status, smem_addr(&s->acc_full[acc]), phase, kSumsLimitNs)) return false;
         tc_fence_after();
         return true;
     }

@@ -255,3 +255,11 @@ def test_layer_sizes():
     for topk, tokens in ((2, 0), (0, 4), (2, -1)):
         with pytest.raises(ValueError, match="max_tokens and topk"):
             moe.BF16MoELayer(w13, w2, topk, tokens)
+
+
+def test_longest_sums_of_a_weight_gradient():
+    """2^26 rows are the most that are taken (the kernel's waits are bounded for two such sums: it asserts so as it is
+    compiled)."""
+    most = 1 << 26
+    assert _wgrad(E=1, M=most, out=None) == INVALID and _wgrad(E=1, M=most + 1, out=None) == UNSUPPORTED
+    assert _wgrad(mode=0, seg=FAKE, rows=most, out=None) == INVALID
