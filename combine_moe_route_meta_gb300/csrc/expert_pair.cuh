@@ -136,7 +136,7 @@ __device__ __forceinline__ void pair_start(PairShared* s, const RowLayout& rows,
     }
     if (threadIdx.x == 0) {
         s->dead = 0;
-        s->tiles = 0;
+        s->tiles = 0, s->most = 0;
         s->prefix()[0] = 0;
     }
     pdl_wait();

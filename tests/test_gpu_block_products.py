@@ -505,3 +505,30 @@ def test_added_bf16_gradients_of_rows_that_part_a_warp(m, n):
         want, old = first[e].double() + x.T @ y, first[e].double().abs()
         bound = 1.01 * acc(int(r.counts[e])) * (x.abs().T @ y.abs()) + (HALF[torch.bfloat16] + 2.0 ** -23) * want.abs()
         close(outs[0][e], want, bound + 2.0 ** -23 * old)
+
+
+@pytest.mark.parametrize("op", ["product", "transposed", "swiglu", "dswiglu"])
+def test_segments_that_overlap_too_far(op):
+    """Refused by every product, nothing written, and the next call is as ever; the ring has its size from no tile then."""
+    m = moe()
+    E, rows, n, k = 64, 300, 72, 136
+    gen = torch.Generator(device="cuda").manual_seed(40)
+    a = torch.randn(rows, k, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(E, *((k, n) if op in ("transposed", "dswiglu") else (2 * n if op == "swiglu" else n, k)), device="cuda",
+                    generator=gen).bfloat16()
+    gu = torch.randn(rows, 2 * n, device="cuda", generator=gen).bfloat16()
+    outs = []
+    for count, seg in (([rows] * E, [0] * (E + 1)), ([rows] + [0] * (E - 1), [0] + [rows] * E)):
+        out, st = filled((rows, 2 * n if op == "dswiglu" else n), torch.bfloat16), m.new_status()
+        c, where = torch.tensor(count, dtype=torch.int32, device="cuda"), dict(seg_indptr=torch.tensor(seg, device="cuda"))
+        for _ in range(3):
+            if op == "swiglu":
+                m.moe_expert_gemm_swiglu_bf16("normal", a, c, w, out, st, **where)
+            elif op == "dswiglu":
+                m.moe_expert_gemm_dswiglu_bf16("normal", a, c, w, gu, out, st, **where)
+            else:
+                m.moe_expert_gemm_bf16("normal", a, c, w, out, st, transposed=op == "transposed", **where)
+        torch.cuda.synchronize()
+        outs.append((int(st), out))
+    assert outs[0][0] == m.MOE_ERR_INVALID_ARG and bool((outs[0][1].view(torch.uint8) == 0xa5).all())
+    assert outs[1][0] == 0 and bool(outs[1][1].isfinite().all()) and not bool((outs[1][1].view(torch.uint8) == 0xa5).all())
