@@ -46,7 +46,8 @@ constexpr uint32_t kStaging = 2 * kStaged;                   // two groups of fo
 constexpr uint32_t ring_bytes(int E) {
     return uint32_t(kPairShared - 1024 - kStaging - pair_shared_bytes(E)) / 1024 * 1024;
 }
-static_assert(ring_bytes(MOE_MAX_EXPERTS) >= 6 * 2 * kPairBytes, "six slots of the largest tiles");
+static_assert(ring_bytes(MOE_MAX_EXPERTS) >= 6 * 2 * kPairBytes, "six slots of tiles of 256 rows");
+static_assert(ring_bytes(MOE_MAX_EXPERTS) >= 5 * (kPairBytes + kWideRows * 64), "five slots of the largest tiles");
 
 struct GemmArgs {
     RowGemm g;

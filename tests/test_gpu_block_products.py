@@ -532,3 +532,14 @@ def test_segments_that_overlap_too_far(op):
         outs.append((int(st), out))
     assert outs[0][0] == m.MOE_ERR_INVALID_ARG and bool((outs[0][1].view(torch.uint8) == 0xa5).all())
     assert outs[1][0] == 0 and bool(outs[1][1].isfinite().all()) and not bool((outs[1][1].view(torch.uint8) == 0xa5).all())
+
+
+# Beyond some 490 experts their counts leave shared memory for five slots of the largest tiles, not six.
+FIVE = len(LAYOUTS)
+LAYOUTS += [("normal", [(257 + e // 8 % 32) if e % 8 == 3 else e % 2 for e in range(E)], dict(spare=1)) for E in (520, 1024)]
+
+
+@pytest.mark.parametrize("op", ["nk", "kn", "swiglu", "dswiglu"])
+@pytest.mark.parametrize("i", [FIVE, FIVE + 1])
+def test_more_than_256_rows_of_many_experts(i, op):
+    test_more_than_256_rows(i, (392, 2056), op)
