@@ -13,7 +13,8 @@ import torch
 
 from . import (MOE_MODE_MASKED, MOE_QUANT_FP8_G128, MOE_QUANT_FP8_G128_UE8M0, MOE_QUANT_NONE, _check, check_status,
                load_library, moe_combine_ex, moe_dispatch_ex, moe_route_meta_ex, new_status, new_workspace)
-from .experts import MOE_LAYER_MAX_TOKENS, _current, _mode, _on, _pointers, moe_layer_few_tokens, new_layer_workspace
+from .experts import MOE_LAYER_MAX_TOKENS, _current, _mode, _on, moe_layer_few_tokens, new_layer_workspace
+from .experts import _pointers as _device_pointers
 
 __all__ = [
     "MOE_WEIGHTS_NK", "MOE_WEIGHTS_KN", "MOE_GRAD_BF16", "MOE_GRAD_FP32", "MOE_NORM_MAX_HIDDEN", "NormOutput",
@@ -35,6 +36,17 @@ _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float3
 # ---------------------------------------------------------------------------
 # thin wrappers with the C names
 # ---------------------------------------------------------------------------
+
+def _pointers(*specs):
+    """The device pointers of (tensor or None, bytes needed, name, dtype), which are tensors of the current device, where
+    the kernels run."""
+    out = _device_pointers(*specs)
+    device = torch._C._cuda_getDevice()
+    for spec in specs:
+        if spec[0] is not None and spec[0].get_device() != device:
+            raise ValueError(f"{spec[2]}: tensors of the current device expected")
+    return out
+
 
 def _rows(mode: str, a: torch.Tensor, K: int, E: int, M: int, seg_indptr, name: str = "a") -> int:
     """Rows of a layout whose row buffer `a` has K columns."""

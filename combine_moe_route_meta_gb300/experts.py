@@ -45,26 +45,19 @@ def _mode(mode: str) -> int:
 
 def _pointers(*specs):
     """Checks (tensor or None, bytes needed, name, dtype) and returns the data pointers: element types and sizes of all of
-    them first, then that they are contiguous tensors of the current device, where the kernels run."""
-    out, wrong, device = [], None, None
+    them first, then that they are contiguous device tensors."""
+    out, wrong = [], None
     for t, nbytes, name, dtype in specs:
         if t is None:
             out.append(None)
             continue
         if t.dtype is not dtype or t.nbytes < nbytes:
             _need(t, nbytes, name, dtype)
-        if wrong is None:
-            if not (t.is_cuda and t.is_contiguous()):
-                wrong = t
-            elif device is None:
-                device = t.get_device()
-            elif t.get_device() != device:
-                wrong = t
+        if wrong is None and not (t.is_cuda and t.is_contiguous()):
+            wrong = t
         out.append(t.data_ptr())
     if wrong is not None:
         _ptr(wrong)
-    if device is not None and (wrong is not None or device != torch._C._cuda_getDevice()):
-        raise ValueError("tensors of the current device expected")
     return out
 
 

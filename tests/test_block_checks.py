@@ -263,3 +263,33 @@ def test_longest_sums_of_a_weight_gradient():
     most = 1 << 26
     assert _wgrad(E=1, M=most, out=None) == INVALID and _wgrad(E=1, M=most + 1, out=None) == UNSUPPORTED
     assert _wgrad(mode=0, seg=FAKE, rows=most, out=None) == INVALID
+
+
+class _OnDevice:
+    """What the binding asks of a tensor, as one of a GPU's would answer."""
+
+    def __init__(self, device, dtype=torch.bfloat16):
+        self.device_index, self.dtype, self.nbytes, self.is_cuda = device, dtype, 64, True
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.device_index
+
+    def data_ptr(self):
+        return 0x1000
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The block's operators refuse them; the NVFP4 experts' take them as they did before there was a block, by peer access."""
+    from combine_moe_route_meta_gb300 import block, experts
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    mixed = [(_OnDevice(d), 64, f"t{d}", torch.bfloat16) for d in (0, 1)] + [(None, 0, "absent", torch.float32)]
+    assert experts._pointers(*mixed) == [0x1000, 0x1000, None]
+    assert experts._pointers(mixed[1]) == [0x1000]
+    with pytest.raises(ValueError, match="t1: tensors of the current device"):
+        block._pointers(*mixed)
+    with pytest.raises(ValueError, match="t1: tensors of the current device"):
+        block._pointers(mixed[1])
+    assert block._pointers(mixed[0], mixed[2]) == [0x1000, None]
