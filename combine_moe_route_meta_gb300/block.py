@@ -356,6 +356,9 @@ class BF16MoELayer:
         if x.shape != (T, self.H) or topk_ids.shape != (T, self.K) or topk_weights.shape != (T, self.K):
             raise ValueError(f"x, topk_ids, topk_weights: [T, {self.H}], [T, {self.K}] and [T, {self.K}] expected, got "
                              f"{tuple(x.shape)}, {tuple(topk_ids.shape)} and {tuple(topk_weights.shape)}")
+        # all of them before the first launch: the route metadata and the few-token kernels do not ask for the device
+        _pointers((x, 0, "x", _BF16), (topk_ids, 0, "topk_ids", _I32), (topk_weights, 0, "topk_weights", _F32),
+                  (self.w13, 0, "w13", _BF16), (self.w2, 0, "w2", _BF16))
         out = self.out[:T]
         self.seen = None
         if self.few and T <= self.few:

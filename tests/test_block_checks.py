@@ -293,3 +293,37 @@ def test_tensors_of_another_device(monkeypatch):
     with pytest.raises(ValueError, match="t1: tensors of the current device"):
         block._pointers(mixed[1])
     assert block._pointers(mixed[0], mixed[2]) == [0x1000, None]
+
+
+class _GpuTensor(torch.Tensor):
+    """A host tensor that says it is one of GPU 1."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("few", [0, 4])
+def test_layer_refuses_before_its_first_launch(few, monkeypatch):
+    from combine_moe_route_meta_gb300 import block
+
+    def launched(*args, **kwargs):
+        raise AssertionError("launched")
+
+    for name in ("moe_route_meta_ex", "moe_layer_few_tokens"):
+        monkeypatch.setattr(block, name, launched)
+    gpu = 0
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: gpu, raising=False)
+    w13, w2 = (torch.zeros(s, dtype=torch.bfloat16).as_subclass(_GpuTensor) for s in ((4, 64, 32), (4, 32, 32)))
+    layer = block.BF16MoELayer(w13, w2, 2, 4, few_tokens=few)
+    good = dict(x=torch.zeros(4, 32, dtype=torch.bfloat16), ids=torch.zeros(4, 2, dtype=torch.int32), w=torch.zeros(4, 2))
+    good = {k: t.as_subclass(_GpuTensor) for k, t in good.items()}
+    with pytest.raises(ValueError, match="x: tensors of the current device"):
+        layer(*good.values())
+    gpu = 1
+    for bad in (dict(x=good["x"].float()), dict(ids=good["ids"].long()), dict(w=good["w"].double()),
+                dict(w=torch.zeros(2, 4).T.as_subclass(_GpuTensor)), dict(x=torch.zeros(4, 32, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            layer(*(good | bad).values())
+    with pytest.raises(AssertionError, match="launched"):
+        layer(*good.values())
