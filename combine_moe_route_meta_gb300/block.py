@@ -389,12 +389,12 @@ class BF16MoELayer:
         T, seg = ids.shape[0], self.seg_indptr
         if grad_out.shape != (T, self.H):
             raise ValueError(f"grad_out: [{T}, {self.H}] expected, got {tuple(grad_out.shape)}")
-        self.seen = None                       # the rows are overwritten below
         n = T * self.K
         where = dict(seg_indptr=seg, stream=stream)
         grad_rows = self.rows_out[:n]          # the experts' outputs become their gradients
         moe_combine_backward("normal", grad_out, grad_rows, ids, weights, self.E, self.src2dst, seg, grad_rows,
                              self.grad_topk_weights, self.status, expert_out_rows=n, stream=stream)
+        self.seen = None                       # the rows are gone, but not if that call was refused
         moe_expert_wgrad_bf16("normal", grad_rows, self.rows_h[:n], self.masked_m, self.grad_w2, self.status, accumulate,
                               **where)
         gate_up = self.gate_up[:n]             # and gate and up theirs

@@ -327,3 +327,13 @@ def test_layer_refuses_before_its_first_launch(few, monkeypatch):
             layer(*(good | bad).values())
     with pytest.raises(AssertionError, match="launched"):
         layer(*good.values())
+
+
+def test_a_refused_backward_pass_can_be_made_again():
+    w13, w2 = torch.zeros(4, 64, 32, dtype=torch.bfloat16), torch.zeros(4, 32, 32, dtype=torch.bfloat16)
+    layer = moe.BF16MoELayer(w13, w2, 2, 4, train=True)
+    layer.seen = (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))   # as a forward pass leaves it
+    for grad in (torch.zeros(3, 32, dtype=torch.bfloat16), torch.zeros(4, 32), torch.zeros(4, 32, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):                                      # shape, type, no GPU
+            layer.backward(grad)
+        assert layer.seen is not None
