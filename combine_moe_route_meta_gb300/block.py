@@ -50,15 +50,23 @@ def _pointers(*specs):
 
 def _rows(mode: str, a: torch.Tensor, K: int, E: int, M: int, seg_indptr, name: str = "a") -> int:
     """Rows of a layout whose row buffer `a` has K columns."""
-    if a.dim() < 2 or a.shape[-1] != K:
+    if a.dim() < 2:
         raise ValueError(f"{name}: rows of {K} values needed, got shape {tuple(a.shape)}")
-    if _mode(mode) == MOE_MODE_MASKED:
-        if a.dim() == 3 and a.shape[1] != M:  # rows of another stride than the kernels'
-            raise ValueError(f"{name}: [E, {M}, {K}] expected in masked mode, got shape {tuple(a.shape)}")
+    _row_buffer(mode, a, K, M, name)
+    if mode == "masked":
         return E * M
     if seg_indptr is None:
         raise ValueError("seg_indptr: needed in normal mode")
     return a.shape[:-1].numel()
+
+
+def _row_buffer(mode: str, t: Optional[torch.Tensor], K: int, M: int, name: str) -> None:
+    """Refuses a buffer whose rows have another length or stride than the kernels' K columns and M rows an expert; one
+    without a shape that says (one dimension) is theirs to lay out."""
+    if _mode(mode) == MOE_MODE_MASKED and t is not None and t.dim() == 3 and tuple(t.shape[1:]) != (M, K):
+        raise ValueError(f"{name}: [E, {M}, {K}] expected in masked mode, got shape {tuple(t.shape)}")
+    if t is not None and t.dim() >= 2 and t.shape[-1] != K:
+        raise ValueError(f"{name}: rows of {K} values needed, got shape {tuple(t.shape)}")
 
 
 def _layout(mode: str, E: int, masked_m, seg_indptr, dev_status):
@@ -78,6 +86,7 @@ def moe_expert_gemm_bf16(mode: str, a: torch.Tensor, masked_m: torch.Tensor, w: 
     if transposed:
         N, K = K, N
     rows = _rows(mode, a, K, E, max_tokens_per_expert, seg_indptr)
+    _row_buffer(mode, out, N, max_tokens_per_expert, "out")
     pm, pseg, pst, pa, pw, po = _pointers(
         *_layout(mode, E, masked_m, seg_indptr, dev_status), (a, 2 * rows * K, "a", _BF16), (w, 0, "w", _BF16),
         (out, 2 * rows * N, "out", _BF16))
@@ -97,6 +106,8 @@ def moe_expert_gemm_swiglu_bf16(mode: str, a: torch.Tensor, masked_m: torch.Tens
         raise ValueError(f"w13: gate and up rows do not fit {N} rows")
     N //= 2
     rows = _rows(mode, a, K, E, max_tokens_per_expert, seg_indptr)
+    _row_buffer(mode, h, N, max_tokens_per_expert, "h")
+    _row_buffer(mode, gate_up, 2 * N, max_tokens_per_expert, "gate_up")
     pm, pseg, pst, pa, pw, ph, pg = _pointers(
         *_layout(mode, E, masked_m, seg_indptr, dev_status), (a, 2 * rows * K, "a", _BF16), (w13, 0, "w13", _BF16),
         (h, 2 * rows * N, "h", _BF16), (gate_up, 4 * rows * N, "gate_up", _BF16))
@@ -113,6 +124,8 @@ def moe_expert_gemm_dswiglu_bf16(mode: str, grad_out: torch.Tensor, masked_m: to
     grad_gate_up [rows, 2*inter] (grad_gate_up may be gate_up)."""
     E, K, N = w2.shape
     rows = _rows(mode, grad_out, K, E, max_tokens_per_expert, seg_indptr, "grad_out")
+    _row_buffer(mode, gate_up, 2 * N, max_tokens_per_expert, "gate_up")
+    _row_buffer(mode, grad_gate_up, 2 * N, max_tokens_per_expert, "grad_gate_up")
     pm, pseg, pst, pa, pw, pg, po = _pointers(
         *_layout(mode, E, masked_m, seg_indptr, dev_status), (grad_out, 2 * rows * K, "grad_out", _BF16),
         (w2, 0, "w2", _BF16), (gate_up, 4 * rows * N, "gate_up", _BF16),
@@ -159,6 +172,8 @@ def moe_combine_backward(mode: str, grad_out: torch.Tensor, expert_out: Optional
     masked = _mode(mode) == MOE_MODE_MASKED
     # normal layout: a declared capacity; 0: N rows, known only on the device
     rows = num_experts * max_tokens_per_expert if masked else int(expert_out_rows)
+    _row_buffer(mode, expert_out, H, max_tokens_per_expert, "expert_out")
+    _row_buffer(mode, grad_expert_out, H, max_tokens_per_expert, "grad_expert_out")
     pg, pe, pi, pw, ps, pseg, pge, pgw, pst = _pointers(
         (grad_out, 0, "grad_out", _BF16), (expert_out, 2 * rows * H, "expert_out", _BF16),
         (topk_ids, 0, "topk_ids", _I32), (topk_weights, 4 * T * K, "topk_weights", _F32),

@@ -337,3 +337,44 @@ def test_a_refused_backward_pass_can_be_made_again():
         with pytest.raises(ValueError):                                      # shape, type, no GPU
             layer.backward(grad)
         assert layer.seen is not None
+
+
+def _bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def test_results_of_another_stride():
+    """Outputs and kept values whose shape says another row length or another number of rows an expert than the kernels
+    write: large enough, and every expert but the first would find its rows elsewhere."""
+    count, st = torch.ones(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    seg, masked = torch.zeros(5, dtype=torch.int64), dict(max_tokens_per_expert=8)
+    a, w, w13, w2 = _bf(4, 8, 64), _bf(4, 32, 64), _bf(4, 64, 64), _bf(4, 64, 32)
+    for out in (_bf(4, 9, 32), _bf(4, 8, 64), _bf(32, 64)):
+        with pytest.raises(ValueError, match="^out: "):
+            moe.moe_expert_gemm_bf16("masked", a, count, w, out, st, **masked)
+        with pytest.raises(ValueError, match="^h: "):
+            moe.moe_expert_gemm_swiglu_bf16("masked", a, count, w13, out, st, **masked)
+    for gu in (_bf(4, 9, 64), _bf(4, 16, 32), _bf(64, 32)):
+        with pytest.raises(ValueError, match="^gate_up: "):
+            moe.moe_expert_gemm_swiglu_bf16("masked", a, count, w13, _bf(4, 8, 32), st, gu, **masked)
+        with pytest.raises(ValueError, match="^gate_up: "):
+            moe.moe_expert_gemm_dswiglu_bf16("masked", a, count, w2, gu, _bf(4, 8, 64), st, **masked)
+        with pytest.raises(ValueError, match="^grad_gate_up: "):
+            moe.moe_expert_gemm_dswiglu_bf16("masked", a, count, w2, _bf(4, 8, 64), gu, st, **masked)
+    with pytest.raises(ValueError, match="^out: "):
+        moe.moe_expert_gemm_bf16("normal", a.view(32, 64), count, w, _bf(32, 40), st, seg_indptr=seg)
+    with pytest.raises(ValueError, match="no CPU path"):     # in one dimension
+        moe.moe_expert_gemm_bf16("masked", a, count, w, _bf(4 * 8 * 32), st, **masked)
+    T, K, H = 3, 2, 64
+    ids, s2d = torch.zeros(T, K, dtype=torch.int32), torch.zeros(T * K, dtype=torch.int32)
+
+    def combine(mode, eo, ge, **kw):
+        moe.moe_combine_backward(mode, _bf(T, H), eo, ids, torch.zeros(T, K), 4, s2d, seg, ge, torch.zeros(T, K), st, **kw)
+
+    for bad in (_bf(4, 9, H), _bf(4, 8, 2 * H), _bf(32, 72)):
+        with pytest.raises(ValueError, match="^expert_out: "):
+            combine("masked", bad, _bf(4, 8, H), **masked)
+        with pytest.raises(ValueError, match="^grad_expert_out: "):
+            combine("masked", _bf(4, 8, H), bad, **masked)
+    with pytest.raises(ValueError, match="^grad_expert_out: "):
+        combine("normal", _bf(6, H), _bf(6, 72), expert_out_rows=6)
