@@ -196,8 +196,11 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional
                 rstd: Optional[torch.Tensor] = None, quant: str = "none", codes: Optional[torch.Tensor] = None,
                 scales: Optional[torch.Tensor] = None, stream=None) -> None:
     """Root-mean-square norm of x + residual [T, hidden]: into out in bf16 and, with `quant`, into codes [T, hidden] uint8
-    and scales [T, hidden/128] (fp32, or uint8 for fp8g128_ue8m0); the sum into sum, 1/rms into rstd [T] fp32."""
+    and scales [T, hidden/128] (fp32, or uint8 for fp8g128_ue8m0); the sum into sum (only with a residual), 1/rms into rstd
+    [T] fp32."""
     T, H = x.shape
+    if sum is not None and residual is None:
+        raise ValueError("sum: without a residual it is x, and not written")
     q = _norm_quant(quant)
     n = 2 * T * H
     sdtype = _F32 if q == MOE_QUANT_FP8_G128 else torch.uint8

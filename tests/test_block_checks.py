@@ -378,3 +378,11 @@ def test_results_of_another_stride():
             combine("masked", _bf(4, 8, H), bad, **masked)
     with pytest.raises(ValueError, match="^grad_expert_out: "):
         combine("normal", _bf(6, H), _bf(6, 72), expert_out_rows=6)
+
+
+def test_norm_refuses_a_sum_that_it_would_not_write():
+    x, w = _bf(3, 256), _bf(256)
+    with pytest.raises(ValueError, match="^sum: "):
+        moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), sum=_bf(3, 256))
+    with pytest.raises(ValueError, match="no CPU path"):
+        moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), residual=x, sum=_bf(3, 256))
