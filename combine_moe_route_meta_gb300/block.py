@@ -202,6 +202,8 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional
     if sum is not None and residual is None:
         raise ValueError("sum: without a residual it is x, and not written")
     q = _norm_quant(quant)
+    if not q and (codes is not None or scales is not None):
+        raise ValueError("codes, scales: not written without quant")
     n = 2 * T * H
     sdtype = _F32 if q == MOE_QUANT_FP8_G128 else torch.uint8
     px, pw, po, pr, psum, prs, pc, psc = _pointers(

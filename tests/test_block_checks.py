@@ -386,3 +386,10 @@ def test_norm_refuses_a_sum_that_it_would_not_write():
         moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), sum=_bf(3, 256))
     with pytest.raises(ValueError, match="no CPU path"):
         moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), residual=x, sum=_bf(3, 256))
+
+
+def test_norm_refuses_codes_that_it_would_not_write():
+    x, w, codes, scales = _bf(3, 256), _bf(256), torch.zeros(3, 256, dtype=torch.uint8), torch.zeros(3, 2)
+    for kw in (dict(codes=codes, scales=scales), dict(codes=codes), dict(scales=scales)):
+        with pytest.raises(ValueError, match="^codes, scales: "):
+            moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), **kw)
