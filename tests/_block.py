@@ -75,3 +75,19 @@ def close(got, want, bound):
         at = np.unravel_index(i, tuple(got.shape))
         raise AssertionError(f"{int(bad.sum())} of {bad.numel()} values off, worst at {tuple(int(v) for v in at)}: got "
                              f"{float(got.flatten()[i])}, want {float(want.flatten()[i])} within {float(bound.flatten()[i])}")
+
+
+def along(grad, bound, loss, seed, step=1e-5):
+    """`grad`, whose values are within `bound` of the gradient, against differences of loss(change) in 64 bits. Directions have
+    the gradient's own signs: the derivative is then as large as what the roundings of its terms could add up to is small,
+    2^-8 of it, and the same bound refuses a gradient that is 5 % too large or too small, or lacks a part as large. The
+    differences themselves are good to 1e-6 of it."""
+    gen = torch.Generator(device=grad.device).manual_seed(seed)
+    g = grad.double().nan_to_num(0)
+    for _ in range(4):
+        d = g.sign() * torch.randn(g.shape, device=g.device, generator=gen, dtype=torch.float64).abs()
+        want = (loss(step * d) - loss(-step * d)) / (2 * step)
+        got = float((g * d).sum())
+        most = float((bound * d.abs()).sum()) + 1e-6 * abs(want)
+        assert got > 0 and abs(got - want) <= most, (got, want, most)
+        assert abs(1.05 * got - want) > most and abs(0.95 * got - want) > most, (got, want, most)

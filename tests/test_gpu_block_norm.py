@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from _block import HALF, acc, close
+from _block import HALF, acc, along, close
 from _harness import bytes_of, filled, moe
 
 pytestmark = pytest.mark.gpu
@@ -273,3 +273,24 @@ def test_gradient_of_many_rows_in_place(T, H):
 def test_long_rows(T, H):
     test_bf16(T, H, True)
     test_fp8(T, H, "fp8g128")
+
+
+def test_gradient_along_itself():
+    m = moe()
+    T, H = 5, 64
+    x, res, w, gen = _inputs(T, H, seed=5)
+    y = m.rmsnorm(x, w, EPS, residual=res, keep=True)
+    g = torch.randn(T, H, device="cuda", generator=gen).bfloat16()
+    dx, dw = m.rmsnorm_backward(g, y.sum, w, y.rstd)
+    s, wd, gd = y.sum.double(), w.double(), g.double()
+
+    def loss(ds, dw):
+        v = s + ds
+        return float((v * (v.square().mean(-1, keepdim=True) + EPS).rsqrt() * (wd + dw) * gd).sum())
+
+    # as in test_gradient
+    r = (s.square().mean(-1, keepdim=True) + EPS).rsqrt()
+    hat, gw = (s * r).abs(), (gd * wd).abs()
+    parts = r * (gw + hat * (gw * hat).mean(-1, keepdim=True))
+    along(dx, 1.01 * B * dx.double().abs() + 7 * R * parts, lambda c: loss(c, 0), 20)
+    along(dw, 2 * (2 * R + acc(T)) * (gd.abs() * hat).sum(0), lambda c: loss(0, c), 21)

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from _block import HALF, Rows, acc, close, untouched
+from _block import HALF, Rows, acc, along, close, untouched
 from _harness import filled, moe
 
 pytestmark = pytest.mark.gpu
@@ -543,3 +543,41 @@ LAYOUTS += [("normal", [(257 + e // 8 % 32) if e % 8 == 3 else e % 2 for e in ra
 @pytest.mark.parametrize("i", [FIVE, FIVE + 1])
 def test_more_than_256_rows_of_many_experts(i, op):
     test_more_than_256_rows(i, (392, 2056), op)
+
+
+def test_each_gradient_along_itself():
+    """Each operator's gradient by itself, of values that it is given exactly, so that its own rounding is all it is off by."""
+    m = moe()
+    r = Rows("normal", [3, 0, 6, 2], align=4, seed=5)
+    H, I, B = 24, 16, HALF[torch.bfloat16]
+    x, w13, w2, g, gu = r.values(H), r.weights(2 * I, H), r.weights(H, I), r.values(H), r.values(2 * I, 2.0)
+    experts = [(e, at) for e, at in r.each() if r.counts[e]]
+    d, dx = torch.zeros_like(gu), torch.zeros_like(x)
+    m.moe_expert_gemm_dswiglu_bf16("normal", g, r.count, w2, gu, d, r.status, **r.where)
+    m.moe_expert_gemm_bf16("normal", gu, r.count, w13, dx, r.status, transposed=True, **r.where)
+    d13 = torch.zeros_like(w13, dtype=torch.float32)
+    m.moe_expert_wgrad_bf16("normal", gu, x, r.count, d13, r.status, **r.where)
+    r.ok()
+    x64, w64, g64, gu64 = (t.double().nan_to_num(0) for t in (x, w13, g, gu))
+
+    def through_swiglu(change):
+        y = gu64 + change
+        h = y[:, I:] * torch.nn.functional.silu(y[:, :I])
+        return sum(float((h[at] @ w2[e].double().T * g64[at]).sum()) for e, at in experts)
+
+    def product(dx, dw):
+        return sum(float(((x64[at] + dx[at]) @ (w64[e] + dw[e]).T * gu64[at]).sum()) for e, at in experts)
+
+    # as in test_dswiglu, the sums' and the factors' own errors before they cancel
+    dh, mag = (r.per_expert(a, lambda v, e, w=w: v @ w[e]) for a, w in ((g, w2.double()), (g.abs(), w2.double().abs())))
+    G, U = gu64[:, :I], gu64[:, I:]
+    p, q = torch.sigmoid(G), torch.sigmoid(-G)
+    parts, err = U.abs() * p * (1 + G.abs() * q), 1.01 * acc(H) * mag
+    own = torch.cat(((parts + 1) * err + 2.0 ** -18 * dh.abs() * parts, (G * p).abs() * err + 2.0 ** -18 * (dh * G * p).abs()), 1)
+    along(d, 1.01 * B * d.double().abs() + 2 * own, through_swiglu, 6)
+    terms = r.per_expert(gu.abs(), lambda v, e: v @ w64[e].abs())
+    along(dx, 1.01 * B * dx.double().nan_to_num(0).abs() + 2 * acc(2 * I) * terms, lambda c: product(c, 0 * w64), 7)
+    terms = torch.zeros_like(w64)
+    for e, at in experts:
+        terms[e] = gu64[at].abs().T @ x64[at].abs()
+    along(d13, 2.0 ** -23 * d13.double().abs() + 2 * acc(6) * terms, lambda c: product(0 * x64, c), 8)

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from _block import HALF, acc, close
+from _block import HALF, acc, along, close
 from _harness import filled, moe
 
 pytestmark = pytest.mark.gpu
@@ -200,3 +200,20 @@ def test_offsets_past_32_bits():
     close(w, want, acc(16 * 9) * mag)
     assert torch.equal(eo[at], (grad.float() * 0.5).bfloat16())
     assert np.isclose(float(eo.view(-1).count_nonzero()), float((grad * 0.5).count_nonzero()))
+
+
+def test_gradient_along_itself():
+    c = Case(12, 64, 5, 3, invalid=0.3, seed=3)
+    t, k = torch.nonzero(c.row >= 0, as_tuple=True)
+    eo, g, wd = c.eo.double().nan_to_num(0), c.grad.double(), c.w.double()
+
+    def loss(de, dw):
+        return float(((eo + de)[c.row[t, k]] * (wd + dw)[t, k][:, None] * g[t]).sum())
+
+    rows, gw = torch.zeros(c.rows, c.H, dtype=torch.bfloat16, device="cuda"), torch.zeros(c.T, c.K, device="cuda")
+    c.run(c.eo, rows, gw)
+    torch.cuda.synchronize()
+    along(rows, 1.01 * HALF[torch.bfloat16] * rows.double().abs(), lambda d: loss(d, 0), 5)
+    terms = torch.zeros_like(wd)
+    terms[t, k] = (eo[c.row[t, k]].abs() * g[t].abs()).sum(-1)
+    along(gw, 2 * acc(64) * terms, lambda d: loss(0, d), 6)
