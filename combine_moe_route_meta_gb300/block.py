@@ -252,7 +252,8 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     or both (`bf16`: by default the rows are bf16 where they are not FP8). `keep` also returns what
     :func:`rmsnorm_backward` needs. The result is allocated on `stream`.
 
-    FP8 rows go through the dispatch as they are (quant="fp8_passthrough"), and their scale rows as bytes alike."""
+    Codes go through the dispatch as they are (quant="fp8_passthrough"); it moves rows of a multiple of 32 bytes. So do scale
+    rows, as bytes, where they are such rows (fp32: hidden a multiple of 1024; UE8M0: of 4096), and else padded to 32."""
     if stream is not None:
         with _current(stream):
             return rmsnorm(x, weight, eps, residual, quant, bf16, keep)

@@ -393,3 +393,16 @@ def test_norm_refuses_codes_that_it_would_not_write():
     for kw in (dict(codes=codes, scales=scales), dict(codes=codes), dict(scales=scales)):
         with pytest.raises(ValueError, match="^codes, scales: "):
             moe.moe_rmsnorm(x, w, 1e-6, _bf(3, 256), **kw)
+
+
+def test_which_scale_rows_the_dispatch_passes_through():
+    """As the norm's documentation says: fp32 scale rows have hidden / 32 bytes, UE8M0 ones hidden / 128."""
+    def passes(nbytes):
+        return moe.load_library().moe_dispatch_ex(0, moe.MOE_QUANT_FP8_PASSTHROUGH, 0, FAKE, 0, nbytes, FAKE, 2, 4, 0, 0, FAKE,
+                                                  FAKE, 0.0, FAKE, None, FAKE, None) == 0
+
+    for hidden in (128, 512, 1024, 2048, 2176, 2560, 4096, 7168, 8192):
+        assert passes(hidden)
+        assert passes(hidden // 32) == (hidden % 1024 == 0) and passes(hidden // 128) == (hidden % 4096 == 0)
+        for nbytes in (hidden // 32, hidden // 128):
+            assert passes((nbytes + 31) // 32 * 32)

@@ -294,3 +294,32 @@ def test_gradient_along_itself():
     parts = r * (gw + hat * (gw * hat).mean(-1, keepdim=True))
     along(dx, 1.01 * B * dx.double().abs() + 7 * R * parts, lambda c: loss(c, 0), 20)
     along(dw, 2 * (2 * R + acc(T)) * (gd.abs() * hat).sum(0), lambda c: loss(0, c), 21)
+
+
+@pytest.mark.parametrize("mode", ["normal", "masked"])
+@pytest.mark.parametrize("quant", ["fp8g128", "fp8g128_ue8m0"])
+@pytest.mark.parametrize("H", [2048, 2176, 7168])
+def test_padded_scale_rows_through_the_dispatch(H, quant, mode):
+    m = moe()
+    T, E, K = 33, 6, 2
+    x, res, w, gen = _inputs(T, H, seed=11)
+    ids = torch.rand(T, E, device="cuda", generator=gen).argsort(1)[:, :K].int().contiguous()
+    y = m.rmsnorm(x, w, EPS, residual=res, quant=quant)
+    scale_bytes = y.scales.view(torch.uint8).view(T, -1)
+    n = scale_bytes.shape[1]
+    padded = torch.zeros(T, (n + 31) // 32 * 32, dtype=torch.uint8, device="cuda")
+    padded[:, :n] = scale_bytes
+    meta, st = m.route_meta(ids, E), m.new_status()
+    rows, M = (T * K, 0) if mode == "normal" else (E * T, T)
+    outs = []
+    for src in (y.codes, padded):
+        out = torch.zeros(rows, src.shape[1], dtype=torch.uint8, device="cuda")
+        m.moe_dispatch_ex(mode, "fp8_passthrough", "row", src, ids, E, meta.src2dst, meta.seg_indptr, out, None, st,
+                          max_tokens_per_expert=M)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    at, token, e = meta.src2dst.long(), torch.arange(T * K, device="cuda") // K, ids.flatten().long()
+    if mode == "masked":
+        at = e * T + at - meta.seg_indptr[e]
+    assert torch.equal(outs[0][at], y.codes[token]) and torch.equal(outs[1][at, :n], scale_bytes[token])
