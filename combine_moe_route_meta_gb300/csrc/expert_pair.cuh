@@ -18,7 +18,7 @@ constexpr uint32_t kPairBytes = 128 * 128;                 // 128 of these rows:
 constexpr int kPairSlots = 8;
 constexpr size_t kPairShared = 227 * 1024;                 // shared memory of a block, at most
 constexpr int kPairEpilogueWarps = 8;
-constexpr int kPairWarps = 4 + kPairEpilogueWarps;         // 0: loads, 1: products, 2, 3: none
+constexpr int kPairWarps = 4 + kPairEpilogueWarps;         // 0, 1: loads, products; 2: b's loads of the sums; 3: none
 constexpr int kPairThreads = kPairWarps * 32;
 constexpr uint32_t kPairTmemColumns = 512;                 // two accumulators of 256
 
