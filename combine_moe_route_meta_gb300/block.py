@@ -225,6 +225,9 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional
     q = _norm_quant(quant)
     if not q and (codes is not None or scales is not None):
         raise ValueError("codes, scales: not written without quant")
+    for t, name, width in ((out, "out", H), (residual, "residual", H), (sum, "sum", H), (codes, "codes", H),
+                           (scales, "scales", H // 128)):
+        _row_buffer("normal", t, width, 0, name)
     n = 2 * T * H
     sdtype = _F32 if q == MOE_QUANT_FP8_G128 else torch.uint8
     px, pw, po, pr, psum, prs, pc, psc = _pointers(
@@ -246,6 +249,8 @@ def moe_rmsnorm_backward(grad_out: torch.Tensor, s: torch.Tensor, weight: torch.
     of the residual alike, grad_sum being what else flows into their sum, and grad_weight [hidden] fp32."""
     T, H = s.shape
     n = 2 * T * H
+    for t, name in ((grad_out, "grad_out"), (grad_sum, "grad_sum"), (grad_x, "grad_x")):
+        _row_buffer("normal", t, H, 0, name)
     pg, ps, pw, pr, pgs, pgx, pgw, pws = _pointers(
         (grad_out, n, "grad_out", _BF16), (s, 0, "s", _BF16), (weight, 2 * H, "weight", _BF16), (rstd, 4 * T, "rstd", _F32),
         (grad_sum, n, "grad_sum", _BF16), (grad_x, n, "grad_x", _BF16), (grad_weight, 4 * H, "grad_weight", _F32),
@@ -280,6 +285,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
             return rmsnorm(x, weight, eps, residual, quant, bf16, keep)
     T, H = x.shape
     q, n = _norm_quant(quant), 2 * T * H
+    _row_buffer("normal", residual, H, 0, "residual")
     px, pw, pr = _pointers((x, 0, "x", _BF16), (weight, 2 * H, "weight", _BF16), (residual, n, "residual", _BF16))
     if bf16 is None:
         bf16 = not q
@@ -312,6 +318,8 @@ def rmsnorm_backward(grad_out: torch.Tensor, s: torch.Tensor, weight: torch.Tens
             return rmsnorm_backward(grad_out, s, weight, rstd, grad_residual)
     T, H = s.shape
     n = 2 * T * H
+    _row_buffer("normal", grad_out, H, 0, "grad_out")
+    _row_buffer("normal", grad_residual, H, 0, "grad_residual")
     pg, ps, pw, pr, pgs = _pointers((grad_out, n, "grad_out", _BF16), (s, 0, "s", _BF16), (weight, 2 * H, "weight", _BF16),
                                     (rstd, 4 * T, "rstd", _F32), (grad_residual, n, "grad_residual", _BF16))
     lib = load_library()

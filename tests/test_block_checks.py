@@ -406,3 +406,23 @@ def test_which_scale_rows_the_dispatch_passes_through():
         assert passes(hidden // 32) == (hidden % 1024 == 0) and passes(hidden // 128) == (hidden % 4096 == 0)
         for nbytes in (hidden // 32, hidden // 128):
             assert passes((nbytes + 31) // 32 * 32)
+
+
+def test_norms_rows_of_another_length():
+    x, w, wide = _bf(3, 256), _bf(256), _bf(3, 264)
+    for kw in (dict(out=wide), dict(residual=wide), dict(residual=x, sum=wide)):
+        with pytest.raises(ValueError, match=f"^{list(kw)[-1]}: rows of 256"):
+            moe.moe_rmsnorm(x, w, 1e-6, **(dict(out=_bf(3, 256)) | kw))
+    good = dict(codes=torch.zeros(3, 256, dtype=torch.uint8), scales=torch.zeros(3, 2))
+    for bad in (dict(codes=torch.zeros(3, 384, dtype=torch.uint8)), dict(scales=torch.zeros(3, 3))):
+        with pytest.raises(ValueError, match=f"^{list(bad)[0]}: rows of"):
+            moe.moe_rmsnorm(x, w, 1e-6, quant="fp8g128", **(good | bad))
+    with pytest.raises(ValueError, match="^residual: "):
+        moe.rmsnorm(x, w, residual=wide)
+    r, gw, ws = torch.zeros(3), torch.zeros(256), torch.zeros(1 << 16, dtype=torch.uint8)
+    for name, a in (("grad_out", (wide, x, None)), ("grad_x", (x, wide, None)), ("grad_sum", (x, x, wide))):
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            moe.moe_rmsnorm_backward(a[0], x, w, r, a[1], gw, ws, a[2])
+    for name, a in (("grad_out", (wide, None)), ("grad_residual", (x, wide))):
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            moe.rmsnorm_backward(a[0], x, w, r, a[1])
