@@ -305,9 +305,10 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& a, PairShared* s, 
                         if constexpr (OP == RowOp::kPlain) {
                             st_v2(a.g.out + r * n + col, pack4(sums));
                         } else {
-                            // Rounded to bf16, from fp32 sums and factors: the two products that read these gradients next (of the rows,
-                            // transposed, and of the gate and up weights) take bf16. What goes through both roundings is 0.0023 off in
-                            // norm, 0.0017 with these values kept in fp32; that would be twice the bytes written here and read twice.
+                            // Rounded to bf16, from fp32 sums and factors: the two products that read these gradients
+                            // next (of the rows, transposed, and of the gate and up weights) take bf16. What goes
+                            // through both roundings is 0.0023 off in norm, 0.0017 with these values kept in fp32; that
+                            // would be twice the bytes written here and read twice.
                             float4 dg, du;
                             dswiglu(bf16_lo(gate[x][i].x), bf16_lo(up[x][i].x), sums.x, &dg.x, &du.x);
                             dswiglu(bf16_hi(gate[x][i].x), bf16_hi(up[x][i].x), sums.y, &dg.y, &du.y);
