@@ -88,7 +88,8 @@ moe_status_t moe_expert_gemm_swiglu_bf16(moe_mode_t mode, const uint16_t *a, int
  * with G, U = gate_up[r, i], gate_up[r, inter + i], and dh in fp32. The gradients are rounded to bf16 because
  * the products that read them (moe_expert_gemm_bf16 with MOE_WEIGHTS_KN, moe_expert_wgrad_bf16) take bf16 rows:
  * the rows' gradient through both is 0.0023 off in norm, and would be 0.0017 off, its own rounding, if they were
- * kept in fp32. p and 1 - p are within 2^-20 (for G below -87 the step of a subnormal exp(G) comes on top). The gradients of an infinite or NaN G or U are unspecified.
+ * kept in fp32. p and 1 - p are within 2^-20 (for G below -87 the step of a subnormal exp(G) comes on top). The
+ * gradients of an infinite or NaN G or U are unspecified.
  *   grad_out [rows, k], w2 [E, k, inter], gate_up and grad_gate_up [rows, 2*inter]; grad_gate_up may be gate_up
  *   itself, and overlaps it in no other way; else as above.
  */
